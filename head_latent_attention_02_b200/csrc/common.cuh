@@ -1,4 +1,5 @@
-// common.cuh -- shared definitions of libmla's kernels (single translation unit).
+// common.cuh -- shared definitions of libmla's kernels.  Each translation unit
+// that includes it is a module with a status word of its own.
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -12,6 +13,17 @@ namespace mla {
 __device__ int g_status;
 
 __device__ __forceinline__ void set_status(int code) { atomicCAS(&g_status, 0, code); }
+
+// Reads and clears the status word of the module (translation unit) that
+// calls it; mla_get_status asks every module after synchronising the stream.
+static inline int take_module_status() {
+  int v = 0;
+  const int zero = 0;
+  if (cudaMemcpyFromSymbol(&v, g_status, sizeof(int)) != cudaSuccess ||
+      cudaMemcpyToSymbol(g_status, &zero, sizeof(int)) != cudaSuccess)
+    return MLA_ERR_CUDA;
+  return v;
+}
 
 template <typename T> __device__ __forceinline__ float to_f(T x);
 template <> __device__ __forceinline__ float to_f<float>(float x) { return x; }

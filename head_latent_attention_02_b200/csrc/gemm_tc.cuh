@@ -1,0 +1,399 @@
+// gemm_tc.cuh -- bf16 matrix products with fused epilogues on sm_100a tensor
+// cores: D[m, n] = sum_k A[m, k] B[n, k], both operands K-major, fp32
+// accumulation in tensor memory.
+//
+//   linear  out = act(x W^T + bias) + residual (mla_linear)
+//   expand  K_h = W_UK[h] c and V_h = W_UV[h] c for the cached latents c of a
+//           page list, per head (the key and value rows of mla_chunk_attn)
+//
+// Tile.  A cluster of two CTAs computes 256 x BN (cta_group::2, BN <= 256):
+// each CTA holds 128 rows of A and half of B's rows in shared memory, and the
+// pair's MMA reads both halves of B, so a CTA loads (128 + BN / 2) x 64
+// elements for every 128 x BN x 64 product -- at BN = 256 two thirds of what
+// two independent 128 x 256 tiles would take from L2, whose bandwidth is
+// what such tiles run into first.  Two accumulators (2 x 256 tensor-memory
+// columns) let the epilogue of one tile overlap the next one's products.
+//
+// Roles per CTA (192 threads): warp 0 loads its CTA's operand halves by TMA
+// into a ring of stages (64 of K each); warp 1 of the first CTA issues the
+// MMAs of the pair; warps 2-5 read the accumulator (32 lanes each) and apply
+// the epilogue.
+//
+// Work.  A pair takes whole tiles pair, pair + pairs, ... ; or (split) a
+// contiguous run of (tile, k-step) units, so that few tiles with a long K
+// still fill every SM.  A split tile's partial sums go to the workspace, a
+// slot of the pair that made them, and a second launch (mla_linear.cu) adds them in the
+// order of the pairs: the result does not depend on timing.
+//
+// Every wait is bounded and records MLA_ERR_TIMEOUT when it gives up.
+#pragma once
+#include <cuda.h>
+
+#include "common.cuh"
+#include "ptx.cuh"
+
+namespace mla {
+namespace gm {
+
+constexpr int kRows = 128;               // A rows of a CTA
+constexpr int kPairRows = 256;
+constexpr int kKStep = 64;               // K of a stage: 128 bytes of bf16
+constexpr int kABytes = kRows * 128;     // 16 KB
+constexpr int kMaxBN = 256;
+constexpr int kMaxStages = 12;
+constexpr int kThreads = 192;
+constexpr int kSmemMax = 232448;
+constexpr int kBarBytes = 512;
+constexpr int kTmemCols = 512;
+constexpr int kGroupM = 8;               // row tiles that share a pass over the column tiles
+
+enum Act : int { kNone = 0, kSilu = 1, kGelu = 2 };
+
+// 64 rows of the paged cache that a chunk call attends (mla_chunk.cu).
+struct PageEntry {
+  int row;      // physical cache row of the page's first row; past the cache: no rows
+  int kpos;     // request position of that row
+  int n;        // rows that hold data (0 .. 64)
+  int ver;      // relocation version
+};
+
+struct Params {
+  int k_steps, n_mt, n_nt, BN, stages;
+  int chunk;                 // split: units of a pair's run; 0: whole tiles
+  // linear: the M x N result; swapped: A holds W's rows and B x's
+  int swapped, M, N, act;
+  long long res_stride, out_stride;
+  const float* bias;
+  const __nv_bfloat16* residual;
+  __nv_bfloat16* out;
+  float* partial;            // split: [2 x pairs][BN][256]
+  int vec;                   // out and residual rows take 16-byte accesses
+  // expand
+  const PageEntry* pages;    // four entries a row tile
+  const int* n_tiles;        // device: row tiles in use
+  int n_heads;               // heads of this launch
+  long long rows_cap;        // rows per head of the key and value scratch
+  __nv_bfloat16* k_out;      // [n_heads][rows_cap][128]
+  __nv_bfloat16* v_out;
+};
+
+struct Bars {
+  uint64_t full[kMaxStages], empty[kMaxStages];
+  uint64_t acc_full[2], acc_empty[2];
+  uint32_t tmem_base;
+};
+static_assert(sizeof(Bars) <= kBarBytes, "barrier block too large");
+
+struct Seg {
+  int tile, k0, k1;
+};
+
+// The i-th segment of a pair's work; false when there is none.
+__device__ __forceinline__ bool segment(const Params& p, int tiles, int pair, int pairs, int i, Seg* s) {
+  if (p.chunk) {
+    const long long U = (long long)tiles * p.k_steps;
+    const long long u0 = (long long)pair * p.chunk;
+    const long long u1 = u0 + p.chunk < U ? u0 + p.chunk : U;
+    const long long at = i == 0 ? u0 : (u0 / p.k_steps + i) * p.k_steps;
+    if (at >= u1) return false;
+    s->tile = (int)(at / p.k_steps);
+    s->k0 = (int)(at % p.k_steps);
+    s->k1 = (int)(u1 - at < p.k_steps - s->k0 ? s->k0 + (u1 - at) : p.k_steps);
+  } else {
+    const long long t = pair + (long long)i * pairs;
+    if (t >= tiles) return false;
+    s->tile = (int)t;
+    s->k0 = 0;
+    s->k1 = p.k_steps;
+  }
+  return true;
+}
+
+// Row and column tile of tile t: kGroupM row tiles wide, so that the tiles in
+// flight at one time share rows of both operands in L2.
+__device__ __forceinline__ void tile_at(const Params& p, int t, int* mt, int* nt) {
+  const int g = t / (kGroupM * p.n_nt);
+  const int first = g * kGroupM;
+  const int wide = min(kGroupM, p.n_mt - first);
+  const int in = t - g * kGroupM * p.n_nt;
+  *mt = first + in % wide;
+  *nt = in / wide;
+}
+
+__device__ __forceinline__ float activate(float x, int act) {
+  if (act == kSilu) return x / (1.f + __expf(-x));
+  if (act == kGelu) return 0.5f * x * (1.f + erff(x * 0.70710678118654752f));
+  return x;
+}
+
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  const __nv_bfloat162 t = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&t);
+}
+__device__ __forceinline__ float lo_f(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float hi_f(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+
+// Eight consecutive results of one row: out[m][n .. n + 8) = act(v + bias) +
+// residual.  Handles columns past N and rows that take no 16-byte access.
+__device__ __forceinline__ void finish8(const Params& p, int m, int n, const float* v) {
+  __nv_bfloat16* o = p.out + (long long)m * p.out_stride + n;
+  const __nv_bfloat16* r = p.residual ? p.residual + (long long)m * p.res_stride + n : nullptr;
+  float y[8];
+  if (p.vec && n + 8 <= p.N) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) y[j] = activate(v[j] + (p.bias ? __ldg(p.bias + n + j) : 0.f), p.act);
+    if (r) {
+      const uint4 u = *reinterpret_cast<const uint4*>(r);
+      y[0] += lo_f(u.x); y[1] += hi_f(u.x); y[2] += lo_f(u.y); y[3] += hi_f(u.y);
+      y[4] += lo_f(u.z); y[5] += hi_f(u.z); y[6] += lo_f(u.w); y[7] += hi_f(u.w);
+    }
+    *reinterpret_cast<uint4*>(o) =
+        make_uint4(pack2(y[0], y[1]), pack2(y[2], y[3]), pack2(y[4], y[5]), pack2(y[6], y[7]));
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (n + j < p.N) {
+        float t = activate(v[j] + (p.bias ? __ldg(p.bias + n + j) : 0.f), p.act);
+        if (r) t += __bfloat162float(r[j]);
+        o[j] = __float2bfloat16_rn(t);
+      }
+  }
+}
+
+enum Mode : int { kLinear = 0, kExpand = 1 };
+
+// linear: ta over A, box {64, 128}; tb over B, box {64, BN / 2}.  expand: ta
+// over the cache rows, box {64, 64}; tb / tv over W_UK / W_UV seen as
+// [heads x 128, 512], box {64, 128}: the first CTA's half of B is W_UK[h],
+// the second's W_UV[h], so columns 0 .. 127 of the tile are keys and the rest
+// values.
+template <int kMode>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+gemm_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtensorMap ta,
+            const __grid_constant__ CUtensorMap tb, const __grid_constant__ CUtensorMap tv) {
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const int S = p.stages;
+  const int b_bytes = p.BN / 2 * 128;
+  const int stage = kABytes + b_bytes;
+  Bars* bar = reinterpret_cast<Bars*>(smem + S * stage);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank();
+  const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < S; ++i) {
+      mbar_init(&bar->full[i], 1);
+      mbar_init(&bar->empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&bar->acc_full[i], 1);
+      mbar_init(&bar->acc_empty[i], 8);    // four epilogue warps of each CTA
+    }
+    fence_mbar_init();
+  }
+  if (warp == 1) tmem_alloc_pair(&bar->tmem_base, kTmemCols);
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();
+  tc_fence_after();
+  const uint32_t tmem = bar->tmem_base;
+  // what this kernel reads of the launch before it (the page list, the
+  // attention's values) is complete after this wait
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int tiles = kMode == kExpand ? *p.n_tiles * p.n_heads : p.n_mt * p.n_nt;
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ loads
+    if (lane == 0) {
+      prefetch_tmap(&ta);
+      prefetch_tmap(rank && kMode == kExpand ? &tv : &tb);
+      bool ok = true;
+      Seg s;
+      for (int i = 0, n = 0; ok && segment(p, tiles, pair, pairs, i, &s); ++i) {
+        int mt, nt, y0 = 0, y1 = 0;
+        if (kMode == kExpand) {
+          mt = s.tile / p.n_heads;
+          nt = s.tile % p.n_heads;
+          y0 = p.pages[4 * mt + 2 * rank].row;
+          y1 = p.pages[4 * mt + 2 * rank + 1].row;
+        } else {
+          tile_at(p, s.tile, &mt, &nt);
+        }
+        for (int k = s.k0; k < s.k1; ++k, ++n) {
+          const int slot = n % S;
+          if (!mbar_wait_cluster(&bar->empty[slot], ((n / S) & 1) ^ 1)) {
+            set_status(MLA_ERR_TIMEOUT);
+            ok = false;
+            break;
+          }
+          // the pair's bytes are counted on the first CTA's barrier
+          if (rank == 0) mbar_arrive_expect_tx(&bar->full[slot], 2 * stage);
+          const uint32_t fb = mapa(smem_u32(&bar->full[slot]), 0);
+          uint8_t* dst = smem + slot * stage;
+          if (kMode == kExpand) {
+            tma_load_2d_pair(dst, &ta, fb, k * kKStep, y0);
+            tma_load_2d_pair(dst + kABytes / 2, &ta, fb, k * kKStep, y1);
+            tma_load_2d_pair(dst + kABytes, rank ? &tv : &tb, fb, k * kKStep, nt * 128);
+          } else {
+            tma_load_2d_pair(dst, &ta, fb, k * kKStep, mt * kPairRows + (int)rank * kRows);
+            tma_load_2d_pair(dst + kABytes, &tb, fb, k * kKStep, nt * p.BN + (int)rank * (p.BN / 2));
+          }
+        }
+      }
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA
+    if (rank == 0 && lane == 0) {
+      const uint32_t idesc = idesc_bf16_f32(kPairRows, p.BN, false, false);
+      bool ok = true;
+      Seg s;
+      for (int i = 0, n = 0; ok && segment(p, tiles, pair, pairs, i, &s); ++i) {
+        const int ab = i & 1;
+        if (!mbar_wait_cluster(&bar->acc_empty[ab], ((i >> 1) & 1) ^ 1)) {
+          set_status(MLA_ERR_TIMEOUT);
+          break;
+        }
+        tc_fence_after();
+        for (int k = s.k0; k < s.k1; ++k, ++n) {
+          const int slot = n % S;
+          if (!mbar_wait_cluster(&bar->full[slot], (n / S) & 1)) {
+            set_status(MLA_ERR_TIMEOUT);
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t a0 = smem_u32(smem + slot * stage), b0 = a0 + kABytes;
+#pragma unroll
+          for (int ks = 0; ks < 4; ++ks)
+            mma_pair_bf16_ss(tmem + ab * kMaxBN, smem_desc_sw128(a0 + ks * 32, 16, 1024),
+                             smem_desc_sw128(b0 + ks * 32, 16, 1024), idesc,
+                             (k == s.k0 && ks == 0) ? 0u : 1u);
+          mma_pair_commit_both(&bar->empty[slot]);
+        }
+        if (ok) mma_pair_commit_both(&bar->acc_full[ab]);
+      }
+    }
+  } else {
+    // ------------------------------------------------------------ epilogue
+    const int quad = warp & 3;
+    const int row = (int)rank * kRows + quad * 32 + lane;      // row of the pair's tile
+    Seg s;
+    for (int i = 0; segment(p, tiles, pair, pairs, i, &s); ++i) {
+      const int ab = i & 1;
+      const uint32_t acc = tmem + ab * kMaxBN + ((uint32_t)(quad * 32) << 16);
+      PageEntry pe = {0, 0, 0, 0};
+      int mt, nt;
+      if (kMode == kExpand) {
+        mt = s.tile / p.n_heads;
+        nt = s.tile % p.n_heads;
+        pe = p.pages[4 * mt + row / 64];
+      } else {
+        tile_at(p, s.tile, &mt, &nt);
+      }
+      if (!__all_sync(0xffffffffu, mbar_wait_cluster(&bar->acc_full[ab], (i >> 1) & 1))) {
+        if (lane == 0) set_status(MLA_ERR_TIMEOUT);
+        break;
+      }
+      tc_fence_after();
+      if constexpr (kMode == kExpand) {
+        // Rows without data are zeros (a weight of zero times NaN is NaN).  A
+        // value that is not finite is stored as zero and marks the row's key
+        // as NaN instead: queries that see the row get NaN, queries whose mask
+        // hides it are not touched by it.
+        const bool live = row % 64 < pe.n;
+        const long long at = ((long long)nt * p.rows_cap + (long long)mt * kPairRows + row) * 128;
+        bool fine = true;
+#pragma unroll 1
+        for (int c = 96; c >= 0; c -= 32) {
+          float v[32];
+          tmem_ld32_sync(acc + 128 + c, v);
+          uint32_t w[16];
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            const bool f0 = fabsf(v[2 * j]) <= 3.38953139e38f, f1 = fabsf(v[2 * j + 1]) <= 3.38953139e38f;
+            fine = fine && f0 && f1;
+            w[j] = pack2(live && f0 ? v[2 * j] : 0.f, live && f1 ? v[2 * j + 1] : 0.f);
+          }
+          uint4* o = reinterpret_cast<uint4*>(p.v_out + at + c);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) o[j] = make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+        }
+#pragma unroll 1
+        for (int c = 96; c >= 0; c -= 32) {
+          float v[32];
+          tmem_ld32_sync(acc + c, v);
+          if (c == 0 && !fine) v[0] = __int_as_float(0x7fc00000);
+          uint32_t w[16];
+#pragma unroll
+          for (int j = 0; j < 16; ++j) w[j] = live ? pack2(v[2 * j], v[2 * j + 1]) : 0u;
+          uint4* o = reinterpret_cast<uint4*>(p.k_out + at + c);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) o[j] = make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+        }
+      } else if (s.k1 - s.k0 < p.k_steps) {
+        // part of a tile: the pair's first slot holds a segment that starts
+        // its run, the second one that ends it
+        const bool first = (long long)s.tile * p.k_steps + s.k0 == (long long)pair * p.chunk;
+        float* o = p.partial + ((long long)(2 * pair + (first ? 0 : 1)) * p.BN) * kPairRows + row;
+#pragma unroll 1
+        for (int c = 0; c < p.BN; c += 32) {
+          float v[32];
+          tmem_ld32_sync(acc + c, v);
+#pragma unroll
+          for (int j = 0; j < 32; ++j) o[(long long)(c + j) * kPairRows] = v[j];
+        }
+      } else if (p.swapped) {
+        const int n = mt * kPairRows + row;        // feature of this lane
+        const float bias = p.bias && n < p.N ? __ldg(p.bias + n) : 0.f;
+#pragma unroll 1
+        for (int c = 0; c < p.BN; c += 32) {
+          const int m0 = nt * p.BN + c;
+          if (m0 >= p.M) break;
+          float v[32];
+          tmem_ld32_sync(acc + c, v);
+#pragma unroll
+          for (int j = 0; j < 32; ++j) {
+            if (n >= p.N || m0 + j >= p.M) continue;
+            float y = activate(v[j] + bias, p.act);
+            if (p.residual) y += __bfloat162float(p.residual[(long long)(m0 + j) * p.res_stride + n]);
+            p.out[(long long)(m0 + j) * p.out_stride + n] = __float2bfloat16_rn(y);
+          }
+        }
+      } else {
+        const int m = mt * kPairRows + row;
+#pragma unroll 1
+        for (int c = 0; c < p.BN; c += 32) {
+          const int n0 = nt * p.BN + c;
+          if (n0 >= p.N) break;
+          float v[32];
+          tmem_ld32_sync(acc + c, v);
+          if (m < p.M) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              if (n0 + 8 * j < p.N) finish8(p, m, n0 + 8 * j, v + 8 * j);
+          }
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster_addr(mapa(smem_u32(&bar->acc_empty[ab]), 0));
+    }
+  }
+
+  // the launch after this one may be scheduled; it waits for this one's end
+  // before it reads its results
+  asm volatile("griddepcontrol.launch_dependents;");
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();     // no CTA leaves while the pair's MMAs may read its shared memory
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem, kTmemCols);
+  }
+}
+
+}  // namespace gm
+}  // namespace mla

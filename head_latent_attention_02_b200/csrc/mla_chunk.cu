@@ -1,0 +1,589 @@
+// mla_chunk.cu -- attention of a ragged chunk of new tokens over the paged
+// latent cache (mla_chunk_attn): host side, planner and the small kernels.
+//
+// Two routes compute the same result, chosen by a rule on sizes (chunk_route):
+//   expanded   bf16 rows of 512 + 64, 128-wide heads: keys and values are
+//              expanded once per call into the workspace (gemm_tc.cuh), the
+//              rotary keys moved to their request positions, and the direct
+//              form attends over them (chunk_tc.cuh).  For chunks.
+//   absorbed   everything else -- few tokens, fp32, other widths: each token is
+//              a one-token sequence of mla_decode between mla_absorb_q and the
+//              value expansion of mla_out_proj.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+
+#include "mla.h"
+#include "common.cuh"
+#include "ptx.cuh"
+#include "host_tma.cuh"
+#include "gemm_tc.cuh"
+#include "chunk_tc.cuh"
+
+namespace mla {
+namespace {
+
+constexpr int kPlanThreads = 1024;
+constexpr float kNaN = __builtin_nanf("");
+
+struct ChunkArgs {
+  int B, n_tok, H, d_n, d_r, d_v, n_ver, max_pages, max_segs;
+  long long n_pages;
+  double rope_base;
+  int delta[kMaxVersions];
+  const void* q;
+  const int32_t* tok_start;
+  const int32_t* q_pos;
+  const void* cache;
+  const int32_t* block_table;
+  const mla_seg_t* segs;
+};
+
+// Pages of sequence b's segments; -1 when its token range or its segment table
+// is invalid (the rules of mla_decode).
+__device__ int sequence_pages(const ChunkArgs& a, int b) {
+  const int t0 = a.tok_start[b], t1 = a.tok_start[b + 1];
+  if (t0 < 0 || t1 < t0 || t1 > a.n_tok) return -1;
+  const mla_seg_t* sg = a.segs + (size_t)b * a.max_segs;
+  int prev_end = 0, pages = 0;
+  for (int s = 0; s < a.max_segs; ++s) {
+    const int rb = sg[s].row_begin, re = sg[s].row_end;
+    if (re == rb) continue;
+    if (rb < prev_end || re < rb || rb % kPage != 0 || (long long)re > (long long)a.max_pages * kPage ||
+        sg[s].q_version < 0 || sg[s].q_version >= a.n_ver)
+      return -1;
+    prev_end = re;
+    pages += (re - rb + kPage - 1) / kPage;
+  }
+  return pages;
+}
+
+// The i-th page of sequence b's segments (i below sequence_pages): false when
+// its id is out of range.
+__device__ bool page_at(const ChunkArgs& a, int b, int i, gm::PageEntry* e) {
+  const mla_seg_t* sg = a.segs + (size_t)b * a.max_segs;
+  for (int s = 0; s < a.max_segs; ++s) {
+    const int len = sg[s].row_end - sg[s].row_begin;
+    if (len <= 0) continue;
+    const int np = (len + kPage - 1) / kPage;
+    if (i >= np) {
+      i -= np;
+      continue;
+    }
+    const int row = sg[s].row_begin + i * kPage;
+    const int page = a.block_table[(size_t)b * a.max_pages + row / kPage];
+    if (page < 0 || page >= a.n_pages) return false;
+    e->row = page * kPage;
+    e->kpos = sg[s].key_pos_base + i * kPage;
+    e->n = min(kPage, sg[s].row_end - row);
+    e->ver = sg[s].q_version;
+    return true;
+  }
+  return false;
+}
+
+// Exclusive sums of x over the block's threads on top of *carry, which ends as
+// the running total; scratch holds 33 ints.
+__device__ int block_scan(int x, int* scratch, int* carry) {
+  const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
+  int y = x;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int z = __shfl_up_sync(0xffffffffu, y, d);
+    if (lane >= d) y += z;
+  }
+  if (lane == 31) scratch[wid] = y;
+  __syncthreads();
+  if (wid == 0) {
+    int t = scratch[lane];
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int z = __shfl_up_sync(0xffffffffu, t, d);
+      if (lane >= d) t += z;
+    }
+    scratch[lane] = t;
+  }
+  __syncthreads();
+  const int out = *carry + (wid ? scratch[wid - 1] : 0) + y - x;
+  const int total = scratch[31];
+  __syncthreads();
+  if (threadIdx.x == 0) *carry += total;
+  __syncthreads();
+  return out;
+}
+
+// last index i in [0, n) with off[i] <= x (off ascending, off[0] <= x)
+__device__ __forceinline__ int last_at_most(const int* off, int n, int x) {
+  int lo = 0, hi = n - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (off[mid] <= x) lo = mid; else hi = mid - 1;
+  }
+  return lo;
+}
+
+// One CTA: validates the sequences, lists their pages (an even number each, so
+// that a 128-row tile belongs to one sequence; a multiple of four in all) and
+// their 256-token items.  seq: page offset [B + 1], item offset [B + 1], flag
+// [B].  A sequence that does not fit `cap` pages is invalid.
+__global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(
+    const __grid_constant__ ChunkArgs a, int cap, ck::Plan* plan, int* seq, ck::Item* items,
+    gm::PageEntry* pages) {
+  asm volatile("griddepcontrol.launch_dependents;");
+  __shared__ int scratch[33], n_pg, n_it, used;
+  int* pg = seq;
+  int* itm = seq + a.B + 1;
+  int* bad = seq + 2 * (a.B + 1);
+  if (threadIdx.x == 0) n_pg = n_it = used = 0;
+  __syncthreads();
+  for (int b0 = 0; b0 < a.B; b0 += kPlanThreads) {
+    const int b = b0 + threadIdx.x;
+    int np = 0, ni = 0;
+    bool wrong = false;
+    if (b < a.B) {
+      const int t0 = a.tok_start[b], t1 = a.tok_start[b + 1];
+      const int k = sequence_pages(a, b);
+      wrong = k < 0;
+      if (t0 >= 0 && t1 > t0 && t1 <= a.n_tok) {
+        ni = (t1 - t0 - 1) / ck::kItemTokens + 1;
+        np = wrong ? 0 : (k + 1) / 2 * 2;
+      }
+    }
+    const int po = block_scan(np, scratch, &n_pg);
+    const int io = block_scan(ni, scratch, &n_it);
+    if (b < a.B) {
+      if ((long long)po + np > cap) wrong = true;
+      pg[b] = min(po, cap);
+      itm[b] = io;
+      bad[b] = wrong ? 1 : 0;
+      if (wrong) set_status(MLA_ERR_BAD_INDEX);
+      else atomicMax(&used, po + np);
+    }
+  }
+  __syncthreads();
+  const int in_use = used, whole = (in_use + 3) / 4 * 4;      // cap is a multiple of four
+  if (threadIdx.x == 0) {
+    pg[a.B] = min(n_pg, cap);
+    itm[a.B] = n_it;
+    plan->n_items = n_it;
+    plan->n_row_tiles = whole / 4;
+  }
+  __syncthreads();
+  for (int e = threadIdx.x; e < whole; e += kPlanThreads) {
+    gm::PageEntry pe = {INT32_MAX - 2 * kPage, INT32_MAX, 0, 0};   // no rows
+    if (e < in_use) {
+      const int b = last_at_most(pg, a.B, e);
+      if (!bad[b] && e - pg[b] < sequence_pages(a, b) && !page_at(a, b, e - pg[b], &pe)) {
+        set_status(MLA_ERR_BAD_INDEX);
+        atomicExch(&bad[b], 2);
+      }
+    }
+    pages[e] = pe;
+  }
+  __syncthreads();
+  const int total = itm[a.B];
+  for (int i = threadIdx.x; i < total; i += kPlanThreads) {
+    const int b = last_at_most(itm, a.B, i);
+    // the last tokens, which see the most rows, first
+    const int k = itm[b + 1] - 1 - i;
+    ck::Item it;
+    it.b = b;
+    it.tok0 = a.tok_start[b] + k * ck::kItemTokens;
+    it.n = min(ck::kItemTokens, a.tok_start[b + 1] - it.tok0);
+    it.entry = pg[b];
+    it.tiles = atomicAdd(&bad[b], 0) ? -1 : (pg[b + 1] - pg[b]) / 2;
+    items[i] = it;
+  }
+}
+
+// Rotary keys of the listed pages at their request positions: kr[64 e + r] =
+// R(delta[version]) k_rope of page entry e's row r (a plain copy where delta
+// is zero); rows without data are zeros.  One block of 256 threads per entry,
+// four threads a row.
+__global__ void __launch_bounds__(256) chunk_rotary_kernel(const __grid_constant__ ChunkArgs a,
+                                                           const ck::Plan* plan,
+                                                           const gm::PageEntry* pages,
+                                                           __nv_bfloat16* kr) {
+  asm volatile("griddepcontrol.launch_dependents;");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  __shared__ double2 cs[ck::kDr / 2];
+  if ((int)blockIdx.x >= 4 * plan->n_row_tiles) return;
+  const gm::PageEntry e = pages[blockIdx.x];
+  const int delta = e.n > 0 ? a.delta[e.ver] : 0;
+  if (delta != 0) {
+    for (int i = threadIdx.x; i < ck::kDr / 2; i += 256)
+      sincos((double)delta * pow(a.rope_base, -2.0 * i / ck::kDr), &cs[i].y, &cs[i].x);
+    __syncthreads();
+  }
+  const int r = threadIdx.x >> 2, part = threadIdx.x & 3;
+  uint4 u[2] = {make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)};
+  if (r < e.n) {
+    const uint4* src = reinterpret_cast<const uint4*>(
+        static_cast<const __nv_bfloat16*>(a.cache) +
+        ((long long)e.row + r) * (ck::kDc + ck::kDr) + ck::kDc + part * 16);
+    u[0] = src[0];
+    u[1] = src[1];
+    if (delta != 0) {
+      uint32_t* w = reinterpret_cast<uint32_t*>(u);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const double2 t = cs[part * 8 + i];
+        const double x0 = gm::lo_f(w[i]), x1 = gm::hi_f(w[i]);
+        w[i] = gm::pack2((float)(x0 * t.x - x1 * t.y), (float)(x0 * t.y + x1 * t.x));
+      }
+    }
+  }
+  uint4* dst = reinterpret_cast<uint4*>(kr + ((long long)blockIdx.x * kPage + r) * ck::kDr + part * 16);
+  dst[0] = u[0];
+  dst[1] = u[1];
+}
+
+// ------------------------------------------------------------ absorbed route
+enum TokState : int { kLive = 0, kNone = 1, kBad = 2 };
+
+// Tokens [t0, t0 + gridDim.x) as one-token sequences: their block-table and
+// segment rows, their queries split into both parts, a zero rotation position
+// (q is rotated already; absorption then turns it by -delta alone), and
+// whether they belong to a sequence.  A token without one, or of an invalid
+// one, gets no segments.  One block per token.
+template <typename T>
+__global__ void __launch_bounds__(256) chunk_spread_kernel(const __grid_constant__ ChunkArgs a,
+                                                           int t0, int32_t* table,
+                                                           mla_seg_t* segs, T* q_nope, T* q_rope,
+                                                           int32_t* rot_pos, int* state) {
+  __shared__ int s_b, s_bad;
+  const int i = blockIdx.x, t = t0 + i;
+  if (threadIdx.x == 0) {
+    s_b = -1;
+    s_bad = 0;
+  }
+  __syncthreads();
+  for (int b = threadIdx.x; b < a.B; b += blockDim.x) {
+    const int lo = a.tok_start[b], hi = a.tok_start[b + 1];
+    if (lo < 0 || hi < lo || hi > a.n_tok) set_status(MLA_ERR_BAD_INDEX);
+    else if (lo <= t && t < hi) atomicMax(&s_b, b);
+  }
+  __syncthreads();
+  const int b = s_b;
+  if (b >= 0) {
+    const int np = sequence_pages(a, b);
+    if (np < 0 && threadIdx.x == 0) s_bad = 1;
+    gm::PageEntry e;
+    for (int k = threadIdx.x; k < np; k += blockDim.x)
+      if (!page_at(a, b, k, &e)) s_bad = 1;
+  }
+  __syncthreads();
+  const int st = b < 0 ? kNone : (s_bad ? kBad : kLive);
+  if (threadIdx.x == 0) {
+    state[i] = st;
+    rot_pos[i] = 0;
+    if (st == kBad) set_status(MLA_ERR_BAD_INDEX);
+  }
+  for (int k = threadIdx.x; k < a.max_pages; k += blockDim.x)
+    table[(size_t)i * a.max_pages + k] =
+        st == kLive ? a.block_table[(size_t)b * a.max_pages + k] : 0;
+  for (int k = threadIdx.x; k < a.max_segs; k += blockDim.x)
+    segs[(size_t)i * a.max_segs + k] =
+        st == kLive ? a.segs[(size_t)b * a.max_segs + k] : mla_seg_t{0, 0, 0, 0};
+  const T* q = static_cast<const T*>(a.q) + (size_t)t * a.H * (a.d_n + a.d_r);
+  for (int k = threadIdx.x; k < a.H * a.d_n; k += blockDim.x)
+    q_nope[(size_t)i * a.H * a.d_n + k] = q[(size_t)(k / a.d_n) * (a.d_n + a.d_r) + k % a.d_n];
+  for (int k = threadIdx.x; k < a.H * a.d_r; k += blockDim.x)
+    q_rope[(size_t)i * a.H * a.d_r + k] =
+        q[(size_t)(k / a.d_r) * (a.d_n + a.d_r) + a.d_n + k % a.d_r];
+}
+
+// Results of those tokens in the storage type; tokens of no sequence keep
+// what their rows held.
+template <typename T>
+__global__ void __launch_bounds__(256) chunk_store_kernel(int t0, int H, int d_v, const int* state,
+                                                          const float* v, const float* lse_in,
+                                                          T* out, float* lse) {
+  const int i = blockIdx.x, st = state[i];
+  if (st == kNone) return;
+  const size_t row = (size_t)(t0 + i) * H;
+  for (int k = threadIdx.x; k < H * d_v; k += blockDim.x)
+    out[row * d_v + k] = from_f<T>(st == kBad ? kNaN : v[(size_t)i * H * d_v + k]);
+  if (lse)
+    for (int k = threadIdx.x; k < H; k += blockDim.x)
+      lse[row + k] = st == kBad ? kNaN : lse_in[(size_t)i * H + k];
+}
+
+// ------------------------------------------------------------ host
+size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
+
+bool expandable(const mla_dims_t* d) {
+  return d->dtype == MLA_BF16 && d->d_c == ck::kDc && d->d_r == ck::kDr && d->d_n == ck::kDn &&
+         d->d_v == ck::kDv;
+}
+
+struct Layout {
+  bool expanded;
+  // expanded
+  int cap, heads, groups;      // page entries; heads per launch; launches
+  long long rows_cap;
+  size_t plan, seq, items, pages, kr, k, v;
+  // absorbed
+  int slab;
+  size_t table, segs, q_nope, q_rope, rot, state, q_abs, o_lat, lse, vf, ws, ws_bytes;
+  size_t total;
+};
+
+// Expanded when its estimated time is the lower one.  A row's expansion costs
+// 2 * 512 * 256 flops a head at about 1.1 PFLOP/s; a query, row and head
+// 2 * 320 flops at about 0.7 PFLOP/s expanded (in query tiles of 128, so a
+// sequence's tokens round up) and 2 * 1088 at about 0.45 PFLOP/s absorbed.
+bool chunk_route(const mla_dims_t* d, int B, int n_tok, long long max_rows) {
+  if (!expandable(d)) return false;
+  const double rows = (double)max_rows, per = std::ceil((double)n_tok / B);
+  const double e = rows * 262144.0 / 1.1e15 + rows * std::ceil(per / 128) * 128 * 640.0 / 0.7e15;
+  const double s = rows * per * 2176.0 / 0.45e15;
+  return e < s;
+}
+
+bool make_layout(const mla_dims_t* d, int B, int n_tok, int n_ver, int max_pages, int max_segs,
+                 long long max_rows, Layout* l) {
+  *l = Layout{};
+  size_t at = 0;
+  auto take = [&](size_t bytes) {
+    const size_t here = at;
+    at = up256(at + bytes);
+    return here;
+  };
+  l->expanded = chunk_route(d, B, n_tok, max_rows);
+  const size_t es = d->dtype == MLA_BF16 ? 2 : 4;
+  if (l->expanded) {
+    // an even number of pages a sequence
+    const long long cap = ((max_rows + kPage - 1) / kPage + B + 3) / 4 * 4;
+    l->rows_cap = cap * kPage;
+    const size_t head = (size_t)l->rows_cap * (ck::kDn + ck::kDv) * 2;
+    int hg = (int)std::min<size_t>(d->H, std::max<size_t>(1, ((size_t)1 << 30) / head));
+    l->groups = (d->H + hg - 1) / hg;
+    l->heads = (d->H + l->groups - 1) / l->groups;
+    if (l->rows_cap * l->heads + 4 * kPage > INT32_MAX) return false;
+    l->cap = (int)cap;
+    l->plan = take(sizeof(ck::Plan));
+    l->seq = take(sizeof(int) * (3 * (size_t)B + 2));
+    l->items = take(sizeof(ck::Item) * ((size_t)n_tok / ck::kItemTokens + B));
+    l->pages = take(sizeof(gm::PageEntry) * (size_t)cap);
+    l->kr = take((size_t)l->rows_cap * ck::kDr * 2);
+    l->k = take((size_t)l->rows_cap * l->heads * ck::kDn * 2);
+    l->v = take((size_t)l->rows_cap * l->heads * ck::kDv * 2);
+  } else {
+    // tokens per pass: 32768 query rows of heads, which bounds the workspace
+    l->slab = std::min(n_tok, std::max(1, 32768 / d->H));
+    const size_t n = l->slab, row = d->d_c + d->d_r;
+    l->table = take(n * max_pages * 4);
+    l->segs = take(n * max_segs * sizeof(mla_seg_t));
+    l->q_nope = take(n * d->H * d->d_n * es);
+    l->q_rope = take(n * d->H * d->d_r * es);
+    l->rot = take(n * 4);
+    l->state = take(n * 4);
+    l->q_abs = take(n * n_ver * d->H * row * es);
+    l->o_lat = take(n * d->H * d->d_c * 4);
+    l->lse = take(n * d->H * 4);
+    l->vf = take(n * d->H * d->d_v * 4);
+    l->ws_bytes = mla_decode_workspace_size(d, l->slab, 1, n_ver, d->H);
+    if (l->ws_bytes == 0) return false;
+    l->ws = take(l->ws_bytes);
+  }
+  l->total = at;
+  return true;
+}
+
+bool chunk_dims_ok(const mla_dims_t* d) {
+  return d && d->H > 0 && d->d_c > 0 && d->d_r > 0 && d->d_r % 2 == 0 && d->d_n > 0 &&
+         d->d_v > 0 && (d->dtype == MLA_F32 || d->dtype == MLA_BF16) && std::isfinite(d->scale) &&
+         d->scale > 0.f && d->rope_base > 0.0;
+}
+
+mla_status_t run_expanded(const mla_dims_t* d, const ChunkArgs& a, const Layout& l, uint8_t* ws,
+                          const void* w_uk, const void* w_uv, void* v, float* lse, cudaStream_t st) {
+  const int sms = current_sms();
+  if (!sms) return MLA_ERR_CUDA;
+  ck::Plan* plan = reinterpret_cast<ck::Plan*>(ws + l.plan);
+  ck::Item* items = reinterpret_cast<ck::Item*>(ws + l.items);
+  gm::PageEntry* pages = reinterpret_cast<gm::PageEntry*>(ws + l.pages);
+  __nv_bfloat16* kr = reinterpret_cast<__nv_bfloat16*>(ws + l.kr);
+  const uint64_t cache_rows = (uint64_t)a.n_pages * kPage;
+
+  CUtensorMap tc;
+  ck::Maps mp;
+  const uint64_t q_ext[3] = {64, (uint64_t)a.n_tok, 3ull * d->H};
+  const uint64_t q_str[2] = {(uint64_t)d->H * (ck::kDn + ck::kDr) * 2, 128};
+  const uint32_t q_box[3] = {64, ck::kQTile, 3};
+  const uint64_t s_ext[3] = {64, (uint64_t)l.rows_cap * l.heads, 2};
+  const uint64_t s_str[2] = {(uint64_t)ck::kDn * 2, 128};
+  const uint32_t s_box[3] = {64, ck::kKTile, 1};
+  if (!map_rows(&tc, a.cache, ck::kDc, cache_rows, ck::kDc + ck::kDr, kPage) ||
+      !map_bf16(&mp.q, a.q, 3, q_ext, q_str, q_box) ||
+      !map_bf16(&mp.k, ws + l.k, 3, s_ext, s_str, s_box) ||
+      !map_bf16(&mp.v, ws + l.v, 3, s_ext, s_str, s_box) ||
+      !map_rows(&mp.kr, kr, ck::kDr, (uint64_t)l.rows_cap, ck::kDr, ck::kKTile))
+    return MLA_ERR_CUDA;
+  if (cudaFuncSetAttribute(gm::gemm_kernel<gm::kExpand>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           gm::kSmemMax) != cudaSuccess ||
+      cudaFuncSetAttribute(ck::chunk_attn_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           ck::kSmemBytes) != cudaSuccess)
+    return MLA_ERR_CUDA;
+
+  chunk_plan_kernel<<<1, kPlanThreads, 0, st>>>(a, l.cap, plan, reinterpret_cast<int*>(ws + l.seq),
+                                                items, pages);
+  if (cudaGetLastError() != cudaSuccess) return MLA_ERR_CUDA;
+  if (launch_dependent(chunk_rotary_kernel, dim3(l.cap), dim3(256), 0, st, true, a,
+                       static_cast<const ck::Plan*>(plan),
+                       static_cast<const gm::PageEntry*>(pages), kr) != cudaSuccess)
+    return MLA_ERR_CUDA;
+
+  gm::Params g = {};
+  g.k_steps = ck::kDc / gm::kKStep;
+  g.BN = ck::kDn + ck::kDv;
+  const int stage = gm::kABytes + g.BN / 2 * 128;
+  g.stages = (gm::kSmemMax - gm::kBarBytes - 1024) / stage;
+  g.pages = pages;
+  g.n_tiles = &plan->n_row_tiles;
+  g.rows_cap = l.rows_cap;
+  g.k_out = reinterpret_cast<__nv_bfloat16*>(ws + l.k);
+  g.v_out = reinterpret_cast<__nv_bfloat16*>(ws + l.v);
+  ck::Params p;
+  p.plan = plan;
+  p.items = items;
+  p.pages = pages;
+  p.q_pos = a.q_pos;
+  p.H = d->H;
+  p.rows_cap = l.rows_cap;
+  p.scale = d->scale;
+  p.scale_log2 = d->scale * ck::kLog2e;
+  p.v = static_cast<__nv_bfloat16*>(v);
+  p.lse = lse;
+  const int max_items = a.n_tok / ck::kItemTokens + a.B;
+  for (int h0 = 0; h0 < d->H; h0 += l.heads) {
+    const int nh = std::min(l.heads, d->H - h0);
+    CUtensorMap tk, tv;
+    const uint64_t w_rows = (uint64_t)nh * ck::kDn;
+    if (!map_rows(&tk, static_cast<const __nv_bfloat16*>(w_uk) + (size_t)h0 * ck::kDn * ck::kDc,
+                  ck::kDc, w_rows, ck::kDc, 128) ||
+        !map_rows(&tv, static_cast<const __nv_bfloat16*>(w_uv) + (size_t)h0 * ck::kDv * ck::kDc,
+                  ck::kDc, w_rows, ck::kDc, 128))
+      return MLA_ERR_CUDA;
+    g.n_heads = nh;
+    const long long tiles = (long long)l.cap / 4 * nh;
+    const int grid = 2 * (int)std::min<long long>(tiles, sms / 2 > 0 ? sms / 2 : 1);
+    if (launch_dependent(gm::gemm_kernel<gm::kExpand>, dim3(grid), dim3(gm::kThreads),
+                         g.stages * stage + gm::kBarBytes + 1024, st, true, g, tc, tk, tv) !=
+        cudaSuccess)
+      return MLA_ERR_CUDA;
+    p.h0 = h0;
+    p.n_heads = nh;
+    if (launch_dependent(ck::chunk_attn_kernel, dim3(max_items, nh), dim3(ck::kThreads),
+                         ck::kSmemBytes, st, true, p, mp) != cudaSuccess)
+      return MLA_ERR_CUDA;
+  }
+  return MLA_OK;
+}
+
+template <typename T>
+mla_status_t run_absorbed(const mla_dims_t* d, const ChunkArgs& a, const Layout& l, uint8_t* ws,
+                          const void* w_uk, const void* w_uv, void* v, float* lse, cudaStream_t st) {
+  int32_t* table = reinterpret_cast<int32_t*>(ws + l.table);
+  mla_seg_t* segs = reinterpret_cast<mla_seg_t*>(ws + l.segs);
+  T* q_nope = reinterpret_cast<T*>(ws + l.q_nope);
+  T* q_rope = reinterpret_cast<T*>(ws + l.q_rope);
+  int32_t* rot = reinterpret_cast<int32_t*>(ws + l.rot);
+  int* state = reinterpret_cast<int*>(ws + l.state);
+  float* o_lat = reinterpret_cast<float*>(ws + l.o_lat);
+  float* lse_t = reinterpret_cast<float*>(ws + l.lse);
+  float* vf = reinterpret_cast<float*>(ws + l.vf);
+  mla_stream_t ms = reinterpret_cast<mla_stream_t>(st);
+  for (int t0 = 0; t0 < a.n_tok; t0 += l.slab) {
+    const int n = std::min(l.slab, a.n_tok - t0);
+    chunk_spread_kernel<T><<<n, 256, 0, st>>>(a, t0, table, segs, q_nope, q_rope, rot, state);
+    if (cudaGetLastError() != cudaSuccess) return MLA_ERR_CUDA;
+    mla_status_t rc = mla_absorb_q(d, n, q_nope, q_rope, rot, a.delta, a.n_ver, w_uk, ws + l.q_abs, ms);
+    if (rc != MLA_OK) return rc;
+    rc = mla_decode(d, n, 1, ws + l.q_abs, a.n_ver, nullptr, d->H, a.cache, a.n_pages, table,
+                    a.max_pages, segs, a.max_segs, nullptr, nullptr, 0, a.q_pos + t0, o_lat, lse_t,
+                    ws + l.ws, l.ws_bytes, ms);
+    if (rc != MLA_OK) return rc;
+    rc = mla_out_proj(d, n, o_lat, w_uv, nullptr, vf, nullptr, ms);
+    if (rc != MLA_OK) return rc;
+    chunk_store_kernel<T><<<n, 256, 0, st>>>(t0, d->H, d->d_v, state, vf, lse_t,
+                                             static_cast<T*>(v), lse);
+    if (cudaGetLastError() != cudaSuccess) return MLA_ERR_CUDA;
+  }
+  return MLA_OK;
+}
+
+}  // namespace
+
+int chunk_take_status() { return take_module_status(); }
+
+}  // namespace mla
+
+using namespace mla;
+
+extern "C" size_t mla_chunk_workspace_size(const mla_dims_t* dims, int32_t B, int32_t n_tok,
+                                           int32_t n_ver, int32_t max_pages, int32_t max_segs,
+                                           int64_t max_rows) {
+  if (!chunk_dims_ok(dims) || B < 1 || n_tok < 1 || n_ver < 1 || n_ver > kMaxVersions ||
+      max_pages < 1 || max_segs < 1 || max_rows < 0 || max_rows > INT32_MAX)
+    return 0;
+  Layout l;
+  return make_layout(dims, B, n_tok, n_ver, max_pages, max_segs, max_rows, &l) ? l.total : 0;
+}
+
+extern "C" mla_status_t mla_chunk_attn(const mla_dims_t* dims, int32_t B, int32_t n_tok,
+                                       const void* q, const int32_t* tok_start,
+                                       const int32_t* q_pos, const void* w_uk, const void* w_uv,
+                                       const void* cache, int64_t n_pages,
+                                       const int32_t* block_table, int32_t max_pages,
+                                       const mla_seg_t* segs, int32_t max_segs,
+                                       const int32_t* delta, int32_t n_ver, int64_t max_rows,
+                                       void* v, float* lse, void* workspace, size_t ws_bytes,
+                                       mla_stream_t stream) {
+  if (!chunk_dims_ok(dims) || B < 0 || n_tok < 0 || n_ver < 1 || !delta || n_pages < 1 ||
+      max_pages < 1 || max_segs < 1 || max_rows < 0)
+    return MLA_ERR_INVALID_ARG;
+  if (dims->page_size != kPage || n_ver > kMaxVersions || n_pages * kPage + 2 * kPage > INT32_MAX ||
+      (long long)max_pages * kPage > INT32_MAX || max_rows > INT32_MAX)
+    return MLA_ERR_UNSUPPORTED;
+  if (B == 0 || n_tok == 0) return MLA_OK;
+  if (!q || !tok_start || !q_pos || !w_uk || !w_uv || !cache || !block_table || !segs || !v ||
+      !ptr_aligned(cache, 256) || !ptr_aligned(q, 16) || !ptr_aligned(w_uk, 16) ||
+      !ptr_aligned(w_uv, 16) || !ptr_aligned(v, 16) || !ptr_aligned(lse, 4))
+    return MLA_ERR_INVALID_ARG;
+  Layout l;
+  if (!make_layout(dims, B, n_tok, n_ver, max_pages, max_segs, max_rows, &l))
+    return MLA_ERR_UNSUPPORTED;
+  if (!workspace || ws_bytes < l.total) return MLA_ERR_WORKSPACE;
+  if (!ptr_aligned(workspace, 256)) return MLA_ERR_INVALID_ARG;
+  ChunkArgs a;
+  a.B = B;
+  a.n_tok = n_tok;
+  a.H = dims->H;
+  a.d_n = dims->d_n;
+  a.d_r = dims->d_r;
+  a.d_v = dims->d_v;
+  a.n_ver = n_ver;
+  a.max_pages = max_pages;
+  a.max_segs = max_segs;
+  a.n_pages = n_pages;
+  a.rope_base = dims->rope_base;
+  for (int i = 0; i < kMaxVersions; ++i) a.delta[i] = i < n_ver ? delta[i] : 0;
+  a.q = q;
+  a.tok_start = tok_start;
+  a.q_pos = q_pos;
+  a.cache = cache;
+  a.block_table = block_table;
+  a.segs = segs;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  if (l.expanded) return run_expanded(dims, a, l, ws, w_uk, w_uv, v, lse, st);
+  if (dims->dtype == MLA_BF16)
+    return run_absorbed<__nv_bfloat16>(dims, a, l, ws, w_uk, w_uv, v, lse, st);
+  return run_absorbed<float>(dims, a, l, ws, w_uk, w_uv, v, lse, st);
+}

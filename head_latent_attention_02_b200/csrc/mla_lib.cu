@@ -1,5 +1,5 @@
 // mla_lib.cu -- the C ABI of libmla (include/mla.h): argument validation,
-// TMA descriptor set-up and kernel launches.  Single translation unit.
+// TMA descriptor set-up and kernel launches of the decode step.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -12,13 +12,18 @@
 #include "mla.h"
 #include "common.cuh"
 #include "ptx.cuh"
+#include "host_tma.cuh"
 #include "kernels_simt.cuh"
 #include "kernels_lowbit.cuh"
 #include "decode_tc.cuh"
 #include "wgemm.cuh"
 
 namespace mla {
-int append_take_status();   // the cache writer's module (mla_append.cu)
+// the other modules' status words
+int append_take_status();   // mla_append.cu
+int tokens_take_status();   // mla_tokens.cu
+int linear_take_status();   // mla_linear.cu
+int chunk_take_status();    // mla_chunk.cu
 }
 using namespace mla;
 
@@ -89,34 +94,13 @@ bool tc_eligible(const mla_dims_t* d) {
   return d->dtype == MLA_BF16 && d->d_c == tc::kDc && d->d_r == tc::kDr;
 }
 
-// cuTensorMapEncodeTiled, fetched from the driver at run time so that the
-// library loads on machines without a driver.
-typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
-                                  const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
-                                  const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiledFn encode_fn() {
-  static EncodeTiledFn fn = nullptr;
-  static std::once_flag once;
-  std::call_once(once, [] {
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) ==
-            cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<EncodeTiledFn>(p);
-  });
-  return fn;
-}
-
 // Tensor map over a [rows, 576] bf16 matrix (row pitch 1152 B) with 64-column
 // boxes and 128-byte swizzle.  rank 2: (col, row), box {64, h}.  rank 3:
 // (col, row, 64-column panel), box {64, h, panels}: each box row is 128 *
 // panels contiguous bytes, landing as `panels` planes of h x 128 bytes.
 bool make_map_576(CUtensorMap* m, const void* base, uint64_t rows, int rank, uint32_t h,
                   uint32_t panels = 9) {
-  EncodeTiledFn fn = encode_fn();
+  EncodeTiledFn fn = encode_tiled();
   if (!fn) return false;
   cuuint64_t dims[3] = {64, (cuuint64_t)rows, 9};
   cuuint64_t strides[2] = {(cuuint64_t)tc::kRow * 2, 128};
@@ -133,7 +117,7 @@ bool make_map_576(CUtensorMap* m, const void* base, uint64_t rows, int rank, uin
 // (extent n_rows) and planes are query rows (stride plane_stride floats).
 bool make_map_out(CUtensorMap* m, float* base, uint64_t n_rows, uint64_t n_planes,
                   uint64_t plane_stride, int rank) {
-  EncodeTiledFn fn = encode_fn();
+  EncodeTiledFn fn = encode_tiled();
   if (!fn) return false;
   cuuint64_t dims[3] = {(cuuint64_t)tc::kDc, (cuuint64_t)n_rows, (cuuint64_t)n_planes};
   cuuint64_t strides[2] = {(cuuint64_t)tc::kDc * 4, (cuuint64_t)plane_stride * 4};
@@ -150,7 +134,7 @@ bool make_map_out(CUtensorMap* m, float* base, uint64_t n_rows, uint64_t n_plane
 // it is 128 * box_panels contiguous bytes of the matrix.
 bool make_map_panels(CUtensorMap* m, const void* base, uint64_t cols, uint64_t rows,
                      uint32_t box_rows, uint32_t box_panels) {
-  EncodeTiledFn fn = encode_fn();
+  EncodeTiledFn fn = encode_tiled();
   if (!fn) return false;
   cuuint64_t dims[3] = {64, (cuuint64_t)rows, (cuuint64_t)(cols / 64)};
   cuuint64_t strides[2] = {(cuuint64_t)cols * 2, 128};
@@ -303,8 +287,12 @@ mla_status_t mla_get_status(mla_stream_t stream) {
   if (cudaMemcpyFromSymbol(&v, g_status, sizeof(int)) != cudaSuccess) return MLA_ERR_CUDA;
   const int zero = 0;
   if (cudaMemcpyToSymbol(g_status, &zero, sizeof(int)) != cudaSuccess) return MLA_ERR_CUDA;
-  const int va = mla::append_take_status();
-  return static_cast<mla_status_t>(v ? v : va);
+  // every module is asked, so that each word is cleared
+  const int other[] = {mla::append_take_status(), mla::tokens_take_status(),
+                       mla::linear_take_status(), mla::chunk_take_status()};
+  for (int o : other)
+    if (!v) v = o;
+  return static_cast<mla_status_t>(v);
 }
 
 mla_status_t mla_absorb_q(const mla_dims_t* dims, int32_t n_q, const void* q_nope,

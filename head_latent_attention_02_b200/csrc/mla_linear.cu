@@ -1,0 +1,300 @@
+// mla_linear.cu -- out = act(x W^T + bias) + residual (mla_linear).
+//
+// The output projection of a prompt chunk (Day 27 tutorial "Move the Value
+// Expansion After the Weighted Sum": each head's value joins the shared W_O)
+// with the residual added where the product leaves the accumulator, and the
+// layer's other products.  bf16 operands whose rows take TMA (16-byte pitch
+// and base) run on the tensor cores (gemm_tc.cuh); fp32 and everything else
+// on the CUDA cores below.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "mla.h"
+#include "common.cuh"
+#include "ptx.cuh"
+#include "host_tma.cuh"
+#include "gemm_tc.cuh"
+
+namespace mla {
+namespace {
+
+// ------------------------------------------------------------ CUDA cores
+constexpr int kTK = 16;
+constexpr int kTN = 64;
+
+struct SimtArgs {
+  int M, N, K, act;
+  long long x_stride, w_stride, res_stride, out_stride;
+  const void* x;
+  const void* w;
+  const float* bias;
+  const void* residual;
+  void* out;
+};
+
+// A TM x 64 tile of the result per block of 256 threads, TM / 16 x 4 values a
+// thread; K in steps of 16 through shared memory, the next step's elements on
+// their way while this one's products run.  fp32 accumulation.
+template <typename T, int TM>
+__global__ void __launch_bounds__(256) linear_simt_kernel(const __grid_constant__ SimtArgs a) {
+  constexpr int R = TM / 16;
+  __shared__ float xs[kTK][TM + 4];
+  __shared__ float ws[kTK][kTN + 4];
+  const int m0 = blockIdx.y * TM, n0 = blockIdx.x * kTN;
+  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+  const T* x = static_cast<const T*>(a.x);
+  const T* w = static_cast<const T*>(a.w);
+  constexpr int XE = TM * kTK / 256, WE = kTN * kTK / 256;
+  float xr[XE], wr[WE];
+  auto fetch = [&](int k0) {
+#pragma unroll
+    for (int i = 0; i < XE; ++i) {
+      const int e = i * 256 + threadIdx.x, r = e / kTK, k = k0 + e % kTK;
+      xr[i] = m0 + r < a.M && k < a.K ? to_f(x[(long long)(m0 + r) * a.x_stride + k]) : 0.f;
+    }
+#pragma unroll
+    for (int i = 0; i < WE; ++i) {
+      const int e = i * 256 + threadIdx.x, r = e / kTK, k = k0 + e % kTK;
+      wr[i] = n0 + r < a.N && k < a.K ? to_f(w[(long long)(n0 + r) * a.w_stride + k]) : 0.f;
+    }
+  };
+  float acc[R][4] = {};
+  fetch(0);
+  for (int k0 = 0; k0 < a.K; k0 += kTK) {
+#pragma unroll
+    for (int i = 0; i < XE; ++i) {
+      const int e = i * 256 + threadIdx.x;
+      xs[e % kTK][e / kTK] = xr[i];
+    }
+#pragma unroll
+    for (int i = 0; i < WE; ++i) {
+      const int e = i * 256 + threadIdx.x;
+      ws[e % kTK][e / kTK] = wr[i];
+    }
+    __syncthreads();
+    if (k0 + kTK < a.K) fetch(k0 + kTK);
+#pragma unroll
+    for (int k = 0; k < kTK; ++k) {
+      float xv[R], wv[4];
+#pragma unroll
+      for (int u = 0; u < R; ++u) xv[u] = xs[k][ty * R + u];
+#pragma unroll
+      for (int v = 0; v < 4; ++v) wv[v] = ws[k][tx * 4 + v];
+#pragma unroll
+      for (int u = 0; u < R; ++u)
+#pragma unroll
+        for (int v = 0; v < 4; ++v) acc[u][v] = fmaf(xv[u], wv[v], acc[u][v]);
+    }
+    __syncthreads();
+  }
+#pragma unroll
+  for (int u = 0; u < R; ++u)
+#pragma unroll
+    for (int v = 0; v < 4; ++v) {
+      const int m = m0 + ty * R + u, n = n0 + tx * 4 + v;
+      if (m >= a.M || n >= a.N) continue;
+      float y = acc[u][v] + (a.bias ? a.bias[n] : 0.f);
+      if (a.act == gm::kSilu) y = y / (1.f + expf(-y));
+      if (a.act == gm::kGelu) y = 0.5f * y * (1.f + erff(y * 0.70710678118654752f));
+      if (a.residual) y += to_f(static_cast<const T*>(a.residual)[(long long)m * a.res_stride + n]);
+      static_cast<T*>(a.out)[(long long)m * a.out_stride + n] = from_f<T>(y);
+    }
+}
+
+template <typename T>
+void launch_simt(const SimtArgs& a, cudaStream_t st) {
+  const unsigned nb = (unsigned)((a.N + kTN - 1) / kTN);
+  // few rows: tiles of 16 rows, so that a short product has blocks for more SMs
+  if (a.M <= 512)
+    linear_simt_kernel<T, 16><<<dim3(nb, (unsigned)((a.M + 15) / 16)), 256, 0, st>>>(a);
+  else
+    linear_simt_kernel<T, 64><<<dim3(nb, (unsigned)((a.M + 63) / 64)), 256, 0, st>>>(a);
+}
+
+// ------------------------------------------------------------ tensor cores
+// Sum of a split tile's partials in the order of the pairs, and the epilogue.
+// grid (tiles, BN / 8); 256 threads, one row of the tile each, eight columns.
+__global__ void __launch_bounds__(256) linear_finish_kernel(const __grid_constant__ gm::Params p) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int t = blockIdx.x, c0 = blockIdx.y * 8, row = threadIdx.x;
+  const long long u0 = (long long)t * p.k_steps;
+  const int g0 = (int)(u0 / p.chunk), g1 = (int)((u0 + p.k_steps - 1) / p.chunk);
+  if (g0 == g1) return;                    // one pair made the whole tile
+  int mt, nt;
+  gm::tile_at(p, t, &mt, &nt);
+  const int a = mt * gm::kPairRows + row, b = nt * p.BN + c0;    // operand rows
+  if (p.swapped ? (a >= p.N || b >= p.M) : (a >= p.M || b >= p.N)) return;
+  float v[8] = {};
+#pragma unroll 4
+  for (int g = g0; g <= g1; ++g) {
+    const int second = (long long)g * p.chunk < u0 ? 1 : 0;   // the tile starts inside the run
+    const float* s = p.partial + ((long long)(2 * g + second) * p.BN + c0) * gm::kPairRows + row;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] += s[(long long)j * gm::kPairRows];
+  }
+  if (!p.swapped) {
+    gm::finish8(p, a, b, v);
+    return;
+  }
+  const float bias = p.bias ? __ldg(p.bias + a) : 0.f;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    if (b + j >= p.M) break;
+    float y = gm::activate(v[j] + bias, p.act);
+    if (p.residual) y += __bfloat162float(p.residual[(long long)(b + j) * p.res_stride + a]);
+    p.out[(long long)(b + j) * p.out_stride + a] = __float2bfloat16_rn(y);
+  }
+}
+
+struct TilePlan {
+  int swapped, BN, n_mt, n_nt, k_steps, stages, chunk, grid;
+  size_t ws;
+};
+
+// Which operand takes the tile's 256 rows, how wide the tile is, and whether K
+// is split.  Few rows of x: W takes the rows (its stream is what the call
+// costs) and the tile is as wide as x is high, in runs of units of equal
+// length.  Otherwise the width with the least estimated time: a pair's step
+// costs the larger of the MMA (2 BN clocks) and its operand loads at about 60
+// bytes a clock and SM.
+TilePlan plan_tiles(int M, int N, int K, int sms) {
+  TilePlan t = {};
+  const int pairs = sms / 2 > 0 ? sms / 2 : 1;
+  t.k_steps = (K + gm::kKStep - 1) / gm::kKStep;
+  t.swapped = M <= 128;
+  double best = 0;
+  const int rows = t.swapped ? N : M, cols = t.swapped ? M : N;
+  t.n_mt = (rows + gm::kPairRows - 1) / gm::kPairRows;
+  for (int bn = 32; bn <= gm::kMaxBN; bn += 32) {
+    if (t.swapped ? (bn != (cols + 31) / 32 * 32) : (bn < 64 && cols > bn)) continue;
+    const long long n_nt = (cols + bn - 1) / bn, tiles = (long long)t.n_mt * n_nt;
+    const double load = (gm::kRows + bn / 2) * 128 / 60.0;
+    const double step = 2.0 * bn > load ? 2.0 * bn : load;
+    const long long units = tiles * t.k_steps;
+    // a run of at least eight steps, so that a partial sum is worth its trip
+    long long run = (units + pairs - 1) / pairs;
+    if (run < 8) run = 8 < t.k_steps ? 8 : t.k_steps;
+    const double whole = (double)((tiles + pairs - 1) / pairs) * t.k_steps * step;
+    const double split = (double)run * step + 6000;
+    const bool use_split = split < whole;
+    const double cost = (use_split ? split : whole) + 4.0 * bn;
+    if (best == 0 || cost < best) {
+      best = cost;
+      t.BN = bn;
+      t.n_nt = (int)n_nt;
+      t.chunk = use_split ? (int)run : 0;
+      const long long g = use_split ? (units + run - 1) / run : (tiles < pairs ? tiles : pairs);
+      t.grid = 2 * (int)g;
+      t.ws = use_split ? (size_t)(2 * g) * bn * gm::kPairRows * sizeof(float) : 0;
+    }
+  }
+  const int stage = gm::kABytes + t.BN / 2 * 128;
+  t.stages = (gm::kSmemMax - gm::kBarBytes - 1024) / stage;
+  if (t.stages > gm::kMaxStages) t.stages = gm::kMaxStages;
+  return t;
+}
+
+bool tc_shape(int dtype, int M, int N, int K) {
+  return dtype == MLA_BF16 && M > 0 && N > 0 && K > 0;
+}
+
+}  // namespace
+
+int linear_take_status() { return take_module_status(); }
+
+}  // namespace mla
+
+using namespace mla;
+
+extern "C" size_t mla_linear_workspace_size(int32_t dtype, int32_t M, int32_t N, int32_t K) {
+  if (!tc_shape(dtype, M, N, K)) return 0;
+  const int sms = current_sms();
+  return sms ? plan_tiles(M, N, K, sms).ws : 0;
+}
+
+extern "C" mla_status_t mla_linear(int32_t dtype, int32_t M, int32_t N, int32_t K, const void* x,
+                                   int64_t x_stride, const void* w, int64_t w_stride,
+                                   const float* bias, int32_t act, const void* residual,
+                                   int64_t res_stride, void* out, int64_t out_stride,
+                                   void* workspace, size_t ws_bytes, mla_stream_t stream) {
+  if ((dtype != MLA_F32 && dtype != MLA_BF16) || M < 0 || N < 0 || K < 1 || act < gm::kNone ||
+      act > gm::kGelu || x_stride < K || w_stride < K || out_stride < N ||
+      (residual && res_stride < N))
+    return MLA_ERR_INVALID_ARG;
+  if (M == 0 || N == 0) return MLA_OK;
+  const size_t es = dtype == MLA_BF16 ? 2 : 4;
+  if (!x || !w || !out || !ptr_aligned(x, es) || !ptr_aligned(w, es) || !ptr_aligned(out, es) ||
+      !ptr_aligned(residual, es) || !ptr_aligned(bias, 4))
+    return MLA_ERR_INVALID_ARG;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  const bool tma = dtype == MLA_BF16 && ptr_aligned(x, 16) && ptr_aligned(w, 16) &&
+                   x_stride % 8 == 0 && w_stride % 8 == 0 && x_stride < (1ll << 38) &&
+                   w_stride < (1ll << 38);
+  if (!tma) {
+    if (((long long)M + 63) / 64 > 65535) return MLA_ERR_UNSUPPORTED;   // grid limit
+    SimtArgs a;
+    a.M = M;
+    a.N = N;
+    a.K = K;
+    a.act = act;
+    a.x_stride = x_stride;
+    a.w_stride = w_stride;
+    a.res_stride = res_stride;
+    a.out_stride = out_stride;
+    a.x = x;
+    a.w = w;
+    a.bias = bias;
+    a.residual = residual;
+    a.out = out;
+    if (dtype == MLA_BF16) launch_simt<__nv_bfloat16>(a, st);
+    else launch_simt<float>(a, st);
+    return cudaGetLastError() == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
+  }
+  const int sms = current_sms();
+  if (!sms) return MLA_ERR_CUDA;
+  const TilePlan t = plan_tiles(M, N, K, sms);
+  if ((long long)t.n_mt * t.n_nt > INT32_MAX) return MLA_ERR_UNSUPPORTED;
+  if (t.ws && (!workspace || ws_bytes < t.ws)) return MLA_ERR_WORKSPACE;
+  if (t.ws && !ptr_aligned(workspace, 256)) return MLA_ERR_INVALID_ARG;
+  gm::Params p = {};
+  p.k_steps = t.k_steps;
+  p.n_mt = t.n_mt;
+  p.n_nt = t.n_nt;
+  p.BN = t.BN;
+  p.stages = t.stages;
+  p.chunk = t.chunk;
+  p.swapped = t.swapped;
+  p.M = M;
+  p.N = N;
+  p.act = act;
+  p.res_stride = res_stride;
+  p.out_stride = out_stride;
+  p.bias = bias;
+  p.residual = static_cast<const __nv_bfloat16*>(residual);
+  p.out = static_cast<__nv_bfloat16*>(out);
+  p.partial = static_cast<float*>(workspace);
+  p.vec = ptr_aligned(out, 16) && out_stride % 8 == 0 &&
+          (!residual || (ptr_aligned(residual, 16) && res_stride % 8 == 0));
+  CUtensorMap ta, tb;
+  const void* a = t.swapped ? w : x;
+  const void* b = t.swapped ? x : w;
+  const uint64_t ar = t.swapped ? N : M, br = t.swapped ? M : N;
+  if (!map_rows(&ta, a, K, ar, t.swapped ? w_stride : x_stride, gm::kRows) ||
+      !map_rows(&tb, b, K, br, t.swapped ? x_stride : w_stride, t.BN / 2))
+    return MLA_ERR_CUDA;
+  const int smem = t.stages * (gm::kABytes + t.BN / 2 * 128) + gm::kBarBytes + 1024;
+  if (cudaFuncSetAttribute(gm::gemm_kernel<gm::kLinear>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           gm::kSmemMax) != cudaSuccess)
+    return MLA_ERR_CUDA;
+  if (launch_dependent(gm::gemm_kernel<gm::kLinear>, dim3(t.grid), dim3(gm::kThreads), smem, st,
+                       false, p, ta, tb, tb) != cudaSuccess)
+    return MLA_ERR_CUDA;
+  if (t.chunk &&
+      launch_dependent(linear_finish_kernel, dim3(t.n_mt * t.n_nt, t.BN / 8), dim3(256), 0, st,
+                       true, p) != cudaSuccess)
+    return MLA_ERR_CUDA;
+  return MLA_OK;
+}

@@ -1,0 +1,445 @@
+// mla_tokens.cu -- the token side of a prompt chunk: rotary positions with
+// several axes (mla_rope_axes) and the append of a ragged chunk to the paged
+// latent cache (mla_append_tokens).
+//
+// Rotation (Day 27 tutorial "Multi-Head Latent Attention", section "Position
+// Rotations Complicate the Absorption", with one position per axis): the
+// d_r / 2 pairs of a vector are cut into n_axes runs of sections[a] pairs; pair
+// i of run a turns by pos[a][token] * base^(-2i / d_r), i counted over the
+// whole vector, so that equal positions on every axis are the one-axis
+// rotation.  Angles, sines and cosines are computed in double (a float angle
+// at position 10^6 is off by 0.03 rad).
+//
+// Append: token i of sequence b becomes the cache row of logical row
+// row0[b] + i: [c * w / sqrt(mean(c^2) + eps) | R(pos) k] from the raw row
+// [c | k] of the down-projection, rounded to the storage type; a low-bit
+// pool gets the codes of that rounded row.
+//
+// Both are bound by memory for long chunks and by the latency of one chain of
+// loads for a few tokens.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <cstdint>
+
+#include "mla.h"
+#include "common.cuh"
+
+namespace mla {
+namespace {
+
+constexpr int kMaxPairs = 128;      // d_r <= 256
+constexpr int kMaxAxes = 4;
+constexpr int kRopeThreads = 256;
+constexpr int kRopeUnroll = 4;
+constexpr int kTokThreads = 256;    // append: a warp per token
+
+// Frequencies of the pairs, and the first pair of each axis' run.
+struct Axes {
+  int n, half;
+  int first[kMaxAxes + 1];
+  double theta[kMaxPairs];
+  __device__ int axis_of(int pair) const {
+    int x = 0;
+#pragma unroll
+    for (int i = 1; i < kMaxAxes; ++i) x += (i < n && pair >= first[i]) ? 1 : 0;
+    return x;
+  }
+};
+
+bool make_axes(const mla_dims_t* d, int n_axes, const int32_t* sections, Axes* ax) {
+  ax->n = n_axes;
+  ax->half = d->d_r / 2;
+  int sum = 0;
+  for (int i = 0; i < n_axes; ++i) {
+    ax->first[i] = sum;
+    if (sections[i] < 0 || sections[i] > ax->half - sum) return false;
+    sum += sections[i];
+  }
+  for (int i = n_axes; i <= kMaxAxes; ++i) ax->first[i] = sum;
+  for (int i = 0; i < ax->half; ++i) ax->theta[i] = std::pow(d->rope_base, -2.0 * i / d->d_r);
+  return sum == ax->half;
+}
+
+// Eight consecutive elements as floats; 16-byte accesses.
+__device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&v)[8]) {
+  const uint4 u = *reinterpret_cast<const uint4*>(p);
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = __uint_as_float(w[i] << 16);
+    v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  }
+}
+__device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
+  const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
+  v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+  v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+}
+__device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&v)[8]) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __nv_bfloat162 t = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+    w[i] = *reinterpret_cast<const uint32_t*>(&t);
+  }
+  *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+}
+__device__ __forceinline__ void store8(float* p, const float (&v)[8]) {
+  *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+  *reinterpret_cast<float4*>(p + 4) = make_float4(v[4], v[5], v[6], v[7]);
+}
+
+// The turned pair.  fp32 rows are computed in double and rounded once; bf16
+// rows in float, whose error (2^-23 of the pair's length) is far below the
+// rounding to bf16.
+template <typename T> struct Trig;
+template <> struct Trig<float> { using type = double2; };
+template <> struct Trig<__nv_bfloat16> { using type = float2; };
+__device__ __forceinline__ void turn(double2 cs, float x0, float x1, float& y0, float& y1) {
+  y0 = (float)((double)x0 * cs.x - (double)x1 * cs.y);
+  y1 = (float)((double)x0 * cs.y + (double)x1 * cs.x);
+}
+__device__ __forceinline__ void turn(float2 cs, float x0, float x1, float& y0, float& y1) {
+  y0 = x0 * cs.x - x1 * cs.y;
+  y1 = x0 * cs.y + x1 * cs.x;
+}
+
+// ---------------------------------------------------------------------------
+struct RopeArgs {
+  int n_tok, n_heads, heads_per_block;
+  int inverse;
+  long long x_tok, x_head, o_tok, o_head;   // strides in elements
+  const int32_t* pos;                       // [n_axes, n_tok]
+  const void* x;
+  void* out;
+};
+
+// grid (n_tok, head blocks).  The block computes its token's sines and cosines
+// once, in shared memory, while the vectors it will turn are on their way:
+// a thread issues its loads before it waits for the table.  kVec: 16-byte
+// accesses (d_r, strides and pointers are multiples of eight elements).
+template <typename T, bool kVec>
+__global__ void __launch_bounds__(kRopeThreads) rope_axes_kernel(const __grid_constant__ RopeArgs a,
+                                                                 const __grid_constant__ Axes ax) {
+  using CS = typename Trig<T>::type;
+  __shared__ CS cs[kMaxPairs];
+  const int t = blockIdx.x;
+  const int h0 = blockIdx.y * a.heads_per_block;
+  const int nh = min(a.heads_per_block, a.n_heads - h0);
+  const T* x = static_cast<const T*>(a.x) + (long long)t * a.x_tok + (long long)h0 * a.x_head;
+  T* out = static_cast<T*>(a.out) + (long long)t * a.o_tok + (long long)h0 * a.o_head;
+  const int per = kVec ? ax.half / 4 : ax.half;      // work items of a head
+  const int n = nh * per;
+  auto table = [&] {
+    for (int i = threadIdx.x; i < ax.half; i += kRopeThreads) {
+      double sn, c;
+      sincos((double)a.pos[(size_t)ax.axis_of(i) * a.n_tok + t] * ax.theta[i], &sn, &c);
+      if (a.inverse) sn = -sn;
+      cs[i].x = c;
+      cs[i].y = sn;
+    }
+    __syncthreads();
+  };
+  if constexpr (kVec) {
+    for (int base = 0; base < n; base += kRopeThreads * kRopeUnroll) {
+      float v[kRopeUnroll][8];
+#pragma unroll
+      for (int u = 0; u < kRopeUnroll; ++u) {
+        const int i = base + u * kRopeThreads + threadIdx.x;
+        if (i < n) load8(x + (long long)(i / per) * a.x_head + (i % per) * 8, v[u]);
+      }
+      if (base == 0) table();
+#pragma unroll
+      for (int u = 0; u < kRopeUnroll; ++u) {
+        const int i = base + u * kRopeThreads + threadIdx.x;
+        if (i >= n) break;
+        const int p0 = (i % per) * 4;
+        float y[8];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          turn(cs[p0 + j], v[u][2 * j], v[u][2 * j + 1], y[2 * j], y[2 * j + 1]);
+        store8(out + (long long)(i / per) * a.o_head + p0 * 2, y);
+      }
+    }
+  } else {
+    table();
+    for (int i = threadIdx.x; i < n; i += kRopeThreads) {
+      const int p = i % per;
+      const T* s = x + (long long)(i / per) * a.x_head + 2 * p;
+      T* d = out + (long long)(i / per) * a.o_head + 2 * p;
+      float y0, y1;
+      turn(cs[p], to_f(s[0]), to_f(s[1]), y0, y1);
+      d[0] = from_f<T>(y0);
+      d[1] = from_f<T>(y1);
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+struct AppendTokArgs {
+  int B, n_tok, d_c, d_r, max_pages, bits_c;   // bits_c 0: rows of the storage type
+  long long n_pages, kv_stride;
+  const void* kv;
+  const int32_t* tok_start;   // [B + 1]
+  const int32_t* row0;        // [B]
+  const int32_t* pos;         // [n_axes, n_tok]
+  const float* norm_w;        // [d_c] or null
+  float eps;
+  const float* scale_c;
+  const float* scale_r;
+  void* cache;
+  const int32_t* block_table;
+};
+
+// The sequence that token t belongs to, by the whole warp: the number of
+// starts at or before t, less one (the loads of a batch of 32 sequences are
+// independent of one another, where a binary search chains them).  -1: the
+// token lies behind the last sequence; -2: the starts are not in order.
+__device__ __forceinline__ int owner_of(const int32_t* tok_start, int B, int t, int lane) {
+  int n = 0;
+  for (int j = 0; j <= B; j += 32)
+    n += __popc(__ballot_sync(0xffffffffu, j + lane <= B && tok_start[min(j + lane, B)] <= t));
+  if (n == B + 1) return -1;
+  if (n == 0 || tok_start[n - 1] > t || tok_start[n] <= t) return -2;
+  return n - 1;
+}
+
+template <typename T>
+__device__ __forceinline__ void load_group(const T* p, bool vec, int n, float (&v)[8]) {
+  if (vec) {
+    load8(p, v);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = j < n ? to_f(p[j]) : 0.f;
+  }
+}
+
+__device__ __forceinline__ uint32_t code_of(float x, float scale, int bits) {
+  const int lo = -(1 << (bits - 1)), hi = (1 << (bits - 1)) - 1;
+  return (uint32_t)min(hi, max(lo, (int)rintf(x / scale))) & ((1u << bits) - 1u);
+}
+
+// A warp per token; lane l holds the latent groups of eight channels l, l + 32,
+// ... and the rotary pairs l, l + 32, ...  A is the type of the norm's sum and
+// product: float for rows of the storage type; double for a low-bit pool, where
+// one rounding of a value next to the border of two codes moves it by a
+// whole step.
+template <typename T, typename A>
+__global__ void __launch_bounds__(kTokThreads) append_tokens_kernel(
+    const __grid_constant__ AppendTokArgs a, const __grid_constant__ Axes ax) {
+  const long long gw = (long long)blockIdx.x * (kTokThreads / 32) + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31;
+  if (gw >= a.n_tok) return;
+  const int t = (int)gw;
+  const int b = owner_of(a.tok_start, a.B, t, lane);
+  if (b == -1) return;
+  int page = -1, slot = 0;
+  if (b >= 0) {
+    const long long r = (long long)a.row0[b] + (t - a.tok_start[b]);
+    if (r >= 0 && r / kPage < a.max_pages) {
+      page = a.block_table[(size_t)b * a.max_pages + r / kPage];
+      slot = (int)(r % kPage);
+    }
+  }
+  if (page < 0 || page >= a.n_pages) {
+    if (lane == 0) set_status(MLA_ERR_BAD_INDEX);
+    return;
+  }
+  const T* src = static_cast<const T*>(a.kv) + (long long)t * a.kv_stride;
+  const int groups = (a.d_c + 7) / 8;
+  const bool vec_in = a.d_c % 8 == 0 && (reinterpret_cast<uintptr_t>(src) & 15) == 0;
+  A inv = (A)1;
+  if (a.norm_w) {
+    A ss = (A)0;
+    for (int g = lane; g < groups; g += 32) {
+      float v[8];
+      load_group(src + 8 * g, vec_in, a.d_c - 8 * g, v);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) ss += (A)v[j] * (A)v[j];
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+    inv = (A)1 / sqrt(ss / (A)a.d_c + (A)a.eps);
+  }
+  const size_t row = (size_t)page * kPage + slot;
+  const int row_bytes = a.bits_c ? (a.d_c * a.bits_c + a.d_r * 4) / 8
+                                 : (a.d_c + a.d_r) * (int)sizeof(T);
+  uint8_t* dst = static_cast<uint8_t*>(a.cache) + row * row_bytes;
+  T* dst_t = reinterpret_cast<T*>(dst);
+  const bool vec_out = a.d_c % 8 == 0 && (reinterpret_cast<uintptr_t>(dst) & 15) == 0;
+  for (int g = lane; g < groups; g += 32) {
+    const int n = min(8, a.d_c - 8 * g);
+    float v[8];
+    load_group(src + 8 * g, vec_in, n, v);
+    if (a.norm_w) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (j < n) v[j] = (float)((A)v[j] * inv * (A)a.norm_w[8 * g + j]);
+    }
+    if (!a.bits_c) {
+      if (vec_out) {
+        store8(dst_t + 8 * g, v);
+      } else {
+        for (int j = 0; j < n; ++j) dst_t[8 * g + j] = from_f<T>(v[j]);
+      }
+    } else {
+      uint32_t word = 0;
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        word |= code_of(to_f(from_f<T>(v[j])), a.scale_c[8 * g + j], a.bits_c) << (a.bits_c * j);
+      if (a.bits_c == 4) reinterpret_cast<uint32_t*>(dst)[g] = word;
+      else reinterpret_cast<uint16_t*>(dst)[g] = (uint16_t)word;
+    }
+  }
+  const T* k = src + a.d_c;
+  for (int i = lane; i < ax.half; i += 32) {
+    double2 cs;
+    sincos((double)a.pos[(size_t)ax.axis_of(i) * a.n_tok + t] * ax.theta[i], &cs.y, &cs.x);
+    float y0, y1;
+    turn(cs, to_f(k[2 * i]), to_f(k[2 * i + 1]), y0, y1);
+    if (!a.bits_c) {
+      dst_t[a.d_c + 2 * i] = from_f<T>(y0);
+      dst_t[a.d_c + 2 * i + 1] = from_f<T>(y1);
+    } else {
+      dst[a.d_c * a.bits_c / 8 + i] =
+          (uint8_t)(code_of(to_f(from_f<T>(y0)), a.scale_r[2 * i], 4) |
+                    code_of(to_f(from_f<T>(y1)), a.scale_r[2 * i + 1], 4) << 4);
+    }
+  }
+}
+
+bool aligned_to(const void* p, uintptr_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
+
+bool rotary_dims_ok(const mla_dims_t* d) {
+  return d && d->d_r > 0 && d->d_r % 2 == 0 && d->rope_base > 0.0 &&
+         (d->dtype == MLA_F32 || d->dtype == MLA_BF16);
+}
+
+}  // namespace
+
+// Reads and clears this module's status word (mla_get_status calls it after
+// synchronising the stream).
+int tokens_take_status() { return take_module_status(); }
+
+}  // namespace mla
+
+using namespace mla;
+
+extern "C" mla_status_t mla_rope_axes(const mla_dims_t* dims, int32_t n_tok, int32_t n_heads,
+                                      const void* x, int64_t x_tok_stride, int64_t x_head_stride,
+                                      const int32_t* pos, int32_t n_axes, const int32_t* sections,
+                                      int32_t inverse, void* out, int64_t out_tok_stride,
+                                      int64_t out_head_stride, mla_stream_t stream) {
+  if (!rotary_dims_ok(dims) || n_tok < 0 || n_heads < 1 || n_axes < 1 || !sections ||
+      (inverse != 0 && inverse != 1))
+    return MLA_ERR_INVALID_ARG;
+  if (n_axes > kMaxAxes || dims->d_r > 2 * kMaxPairs) return MLA_ERR_UNSUPPORTED;
+  Axes ax;
+  if (!make_axes(dims, n_axes, sections, &ax)) return MLA_ERR_INVALID_ARG;
+  if (n_tok == 0) return MLA_OK;
+  const size_t es = dims->dtype == MLA_BF16 ? 2 : 4;
+  if (!x || !pos || !out || !aligned_to(x, es) || !aligned_to(out, es) || !aligned_to(pos, 4))
+    return MLA_ERR_INVALID_ARG;
+  // vectors of one tensor must not overlap: a head's d_r elements lie within
+  // its stride, or a token's heads are the outer axis
+  const int64_t d_r = dims->d_r;
+  auto apart = [&](int64_t tok, int64_t head) {
+    return (head >= d_r && (n_tok == 1 || tok >= head * (n_heads - 1) + d_r)) ||
+           (tok >= d_r && (n_heads == 1 || head >= tok * (n_tok - 1) + d_r));
+  };
+  if (x_tok_stride < 0 || x_head_stride < 0 ||
+      (!apart(out_tok_stride, out_head_stride) && (n_tok > 1 || n_heads > 1)))
+    return MLA_ERR_INVALID_ARG;
+  RopeArgs a;
+  a.n_tok = n_tok;
+  a.n_heads = n_heads;
+  a.inverse = inverse;
+  a.x_tok = x_tok_stride;
+  a.x_head = x_head_stride;
+  a.o_tok = out_tok_stride;
+  a.o_head = out_head_stride;
+  a.pos = pos;
+  a.x = x;
+  a.out = out;
+  const bool vec = dims->d_r % 8 == 0 && aligned_to(x, 16) && aligned_to(out, 16) &&
+                   x_tok_stride % 8 == 0 && x_head_stride % 8 == 0 && out_tok_stride % 8 == 0 &&
+                   out_head_stride % 8 == 0;
+  const int per = vec ? ax.half / 4 : ax.half;
+  // one batch of loads a thread; for few tokens one load a thread, so that the
+  // heads of a token spread over several SMs
+  const int items = kRopeThreads * (n_tok >= 1024 ? kRopeUnroll : 1);
+  int hpb = items / per > 0 ? items / per : 1;
+  if (hpb > n_heads) hpb = n_heads;
+  if ((n_heads + hpb - 1) / hpb > 65535) hpb = (n_heads + 65534) / 65535;
+  a.heads_per_block = hpb;
+  const dim3 grid(n_tok, (n_heads + hpb - 1) / hpb);
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  if (dims->dtype == MLA_BF16) {
+    if (vec) rope_axes_kernel<__nv_bfloat16, true><<<grid, kRopeThreads, 0, st>>>(a, ax);
+    else rope_axes_kernel<__nv_bfloat16, false><<<grid, kRopeThreads, 0, st>>>(a, ax);
+  } else {
+    if (vec) rope_axes_kernel<float, true><<<grid, kRopeThreads, 0, st>>>(a, ax);
+    else rope_axes_kernel<float, false><<<grid, kRopeThreads, 0, st>>>(a, ax);
+  }
+  return cudaGetLastError() == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
+}
+
+extern "C" mla_status_t mla_append_tokens(const mla_dims_t* dims, int32_t B, int32_t n_tok,
+                                          const void* kv, int64_t kv_stride,
+                                          const int32_t* tok_start, const int32_t* row0,
+                                          const int32_t* pos, int32_t n_axes,
+                                          const int32_t* sections, const float* norm_weight,
+                                          float norm_eps, int32_t bits_c, int32_t bits_r,
+                                          const float* scale_c, const float* scale_r, void* cache,
+                                          int64_t n_pages, const int32_t* block_table,
+                                          int32_t max_pages, mla_stream_t stream) {
+  if (!rotary_dims_ok(dims) || dims->d_c < 1 || B < 0 || n_tok < 0 || n_axes < 1 || !sections ||
+      n_pages < 1 || max_pages < 1 || kv_stride < dims->d_c + dims->d_r)
+    return MLA_ERR_INVALID_ARG;
+  if (norm_weight && !(norm_eps >= 0.f)) return MLA_ERR_INVALID_ARG;
+  if (dims->page_size != kPage || n_axes > kMaxAxes || dims->d_r > 2 * kMaxPairs)
+    return MLA_ERR_UNSUPPORTED;
+  const bool low = bits_c != 0 || bits_r != 0;
+  if (low && (!((bits_c == 4 || bits_c == 2) && bits_r == 4) || (dims->d_c * bits_c) % 32 != 0 ||
+              (dims->d_r * bits_r) % 32 != 0))
+    return MLA_ERR_UNSUPPORTED;
+  if (low != (scale_c != nullptr) || low != (scale_r != nullptr)) return MLA_ERR_INVALID_ARG;
+  Axes ax;
+  if (!make_axes(dims, n_axes, sections, &ax)) return MLA_ERR_INVALID_ARG;
+  if (n_tok == 0 || B == 0) return MLA_OK;
+  const size_t es = dims->dtype == MLA_BF16 ? 2 : 4;
+  if (!kv || !tok_start || !row0 || !pos || !cache || !block_table || !aligned_to(kv, es) ||
+      !aligned_to(cache, low ? 4 : es))
+    return MLA_ERR_INVALID_ARG;
+  AppendTokArgs a;
+  a.B = B;
+  a.n_tok = n_tok;
+  a.d_c = dims->d_c;
+  a.d_r = dims->d_r;
+  a.max_pages = max_pages;
+  a.bits_c = bits_c;
+  a.n_pages = n_pages;
+  a.kv_stride = kv_stride;
+  a.kv = kv;
+  a.tok_start = tok_start;
+  a.row0 = row0;
+  a.pos = pos;
+  a.norm_w = norm_weight;
+  a.eps = norm_eps;
+  a.scale_c = scale_c;
+  a.scale_r = scale_r;
+  a.cache = cache;
+  a.block_table = block_table;
+  const unsigned blocks = (unsigned)(((long long)n_tok * 32 + kTokThreads - 1) / kTokThreads);
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  if (dims->dtype == MLA_BF16) {
+    if (low) append_tokens_kernel<__nv_bfloat16, double><<<blocks, kTokThreads, 0, st>>>(a, ax);
+    else append_tokens_kernel<__nv_bfloat16, float><<<blocks, kTokThreads, 0, st>>>(a, ax);
+  } else {
+    if (low) append_tokens_kernel<float, double><<<blocks, kTokThreads, 0, st>>>(a, ax);
+    else append_tokens_kernel<float, float><<<blocks, kTokThreads, 0, st>>>(a, ax);
+  }
+  return cudaGetLastError() == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
+}

@@ -37,6 +37,7 @@ class Dims(ctypes.Structure):
 
 _lib = None
 _vp, _i32, _i64, _sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
+_pi32 = ctypes.POINTER(_i32)
 _SIGS = {
     "mla_abi_version": ([], _i32),
     "mla_status_str": ([_i32], ctypes.c_char_p),
@@ -68,6 +69,17 @@ _SIGS = {
                               _vp, _vp, _sz, _vp, _sz, _vp], _i32),
     "mla_decode_qknorm": ([ctypes.POINTER(Dims), _i32, _i32, _vp, _i32, _vp, _i32, _vp, _vp, _i64,
                            _vp, _i32, _vp, _i32, _vp, _vp, _vp, _vp, _sz, _vp], _i32),
+    "mla_rope_axes": ([ctypes.POINTER(Dims), _i32, _i32, _vp, _i64, _i64, _vp, _i32, _pi32, _i32,
+                       _vp, _i64, _i64, _vp], _i32),
+    "mla_append_tokens": ([ctypes.POINTER(Dims), _i32, _i32, _vp, _i64, _vp, _vp, _vp, _i32, _pi32,
+                           _vp, ctypes.c_float, _i32, _i32, _vp, _vp, _vp, _i64, _vp, _i32, _vp],
+                          _i32),
+    "mla_chunk_attn": ([ctypes.POINTER(Dims), _i32, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _vp,
+                        _i32, _vp, _i32, _pi32, _i32, _i64, _vp, _vp, _vp, _sz, _vp], _i32),
+    "mla_chunk_workspace_size": ([ctypes.POINTER(Dims), _i32, _i32, _i32, _i32, _i32, _i64], _sz),
+    "mla_linear": ([_i32, _i32, _i32, _i32, _vp, _i64, _vp, _i64, _vp, _i32, _vp, _i64, _vp, _i64,
+                    _vp, _sz, _vp], _i32),
+    "mla_linear_workspace_size": ([_i32, _i32, _i32, _i32], _sz),
 }
 
 
@@ -258,3 +270,134 @@ def decode_lowbit_tc(dims, bits_c, bits_r, B, s_q, q_abs, n_ver, head_ids, n_h, 
         block_table.shape[1], _p(segs), segs.shape[1], _p(gather_rows), _p(n_gather),
         max_gather, _p(q_pos), _p(o_lat), _p(lse), _p(dequant), dq_bytes, _p(workspace),
         ws_bytes, _s(stream)))
+
+
+# ------------------------------------------------------------------ prompt chunks
+ACTIVATIONS = {"none": 0, "silu": 1, "gelu": 2}
+_TORCH_DTYPE = {MLA_F32: torch.float32, MLA_BF16: torch.bfloat16}
+
+
+def _ints(values: Sequence[int]):
+    return (_i32 * len(values))(*[int(v) for v in values])
+
+
+def _bytes(t: Optional[torch.Tensor]) -> int:
+    return 0 if t is None else t.numel() * t.element_size()
+
+
+def _want(t: Optional[torch.Tensor], name: str, dtype, shape=None):
+    """Raises unless t (None passes) has the dtype and the sizes of ``shape`` (None: any)."""
+    if t is None:
+        return
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if shape is not None and (t.dim() != len(shape) or
+                              any(w is not None and w != n for w, n in zip(shape, t.shape))):
+        raise ValueError(f"{name} must have sizes {tuple(shape)}, got {tuple(t.shape)}")
+
+
+def _rows(t: Optional[torch.Tensor], name: str) -> int:
+    """Stride between the rows of a matrix whose last axis is contiguous."""
+    if t is None:
+        return 0
+    if t.shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name}: the last axis must be contiguous")
+    return max(t.stride(0), t.shape[1]) if t.shape[0] <= 1 else t.stride(0)
+
+
+def rope_axes(dims: Dims, x, pos, sections: Sequence[int], out, inverse: bool = False, stream=None):
+    """mla_rope_axes: x, out [n_tok, n_heads, d_r] views (any token and head strides), pos
+    [len(sections), n_tok] int32; ``out`` may be ``x``."""
+    n_tok, n_heads, d_r = x.shape
+    dt = _TORCH_DTYPE.get(dims.dtype)
+    _want(x, "x", dt, (None, None, dims.d_r))
+    _want(out, "out", dt, (n_tok, n_heads, d_r))
+    _want(pos, "pos", torch.int32, (len(sections), n_tok))
+    if x.stride(2) != 1 or out.stride(2) != 1:
+        raise ValueError("the last axis of x and out must be contiguous")
+    _check("mla_rope_axes", lib().mla_rope_axes(
+        ctypes.byref(dims), n_tok, n_heads, x.data_ptr(), x.stride(0), x.stride(1), _p(pos),
+        len(sections), _ints(sections), int(inverse), out.data_ptr(), out.stride(0), out.stride(1),
+        _s(stream)))
+
+
+def append_tokens(dims: Dims, kv, tok_start, row0, pos, sections: Sequence[int], cache, block_table,
+                  norm_weight=None, norm_eps: float = 0.0, bits: Optional[Sequence[int]] = None,
+                  scale_c=None, scale_r=None, stream=None):
+    """mla_append_tokens: kv [n_tok, d_c + d_r] rows (any row stride) into the pages of sequences
+    tok_start describes; ``bits`` (bits_c, bits_r) for a packed pool, else rows of the dtype."""
+    n_tok, B = kv.shape[0], row0.shape[0]
+    _want(kv, "kv", _TORCH_DTYPE.get(dims.dtype), (None, dims.d_c + dims.d_r))
+    _want(tok_start, "tok_start", torch.int32, (B + 1,))
+    _want(row0, "row0", torch.int32, (B,))
+    _want(pos, "pos", torch.int32, (len(sections), n_tok))
+    _want(block_table, "block_table", torch.int32, (B, None))
+    _want(norm_weight, "norm_weight", torch.float32, (dims.d_c,))
+    _want(scale_c, "scale_c", torch.float32, (dims.d_c,))
+    _want(scale_r, "scale_r", torch.float32, (dims.d_r,))
+    bits_c, bits_r = bits if bits else (0, 0)
+    if bits:
+        _want(cache, "cache", torch.uint8, (None, 64, (dims.d_c * bits_c + dims.d_r * bits_r) // 8))
+    else:
+        _want(cache, "cache", _TORCH_DTYPE.get(dims.dtype), (None, 64, dims.d_c + dims.d_r))
+    _check("mla_append_tokens", lib().mla_append_tokens(
+        ctypes.byref(dims), B, n_tok, kv.data_ptr(), _rows(kv, "kv"), _p(tok_start), _p(row0),
+        _p(pos), len(sections), _ints(sections), _p(norm_weight), norm_eps, bits_c, bits_r,
+        _p(scale_c), _p(scale_r), _p(cache), cache.shape[0], _p(block_table), block_table.shape[1],
+        _s(stream)))
+
+
+def chunk_workspace_size(dims: Dims, B: int, n_tok: int, n_ver: int, max_pages: int, max_segs: int,
+                         max_rows: int) -> int:
+    return int(lib().mla_chunk_workspace_size(ctypes.byref(dims), B, n_tok, n_ver, max_pages,
+                                              max_segs, max_rows))
+
+
+def chunk_attn(dims: Dims, q, tok_start, q_pos, w_uk, w_uv, cache, block_table, segs,
+               deltas: Sequence[int], max_rows: int, v, workspace, lse=None, stream=None):
+    """mla_chunk_attn: q [n_tok, H, d_n + d_r] (rotary part rotated) over the cached rows of the
+    sequences tok_start describes -> v [n_tok, H, d_v]; lse [n_tok, H] or None."""
+    n_tok, B = q.shape[0], tok_start.shape[0] - 1
+    dt = _TORCH_DTYPE.get(dims.dtype)
+    _want(q, "q", dt, (None, dims.H, dims.d_n + dims.d_r))
+    _want(tok_start, "tok_start", torch.int32, (B + 1,))
+    _want(q_pos, "q_pos", torch.int32, (n_tok,))
+    _want(w_uk, "w_uk", dt, (dims.H, dims.d_n, dims.d_c))
+    _want(w_uv, "w_uv", dt, (dims.H, dims.d_v, dims.d_c))
+    _want(cache, "cache", dt, (None, 64, dims.d_c + dims.d_r))
+    _want(block_table, "block_table", torch.int32, (B, None))
+    _want(segs, "segs", torch.int32, (B, None, 4))
+    _want(v, "v", dt, (n_tok, dims.H, dims.d_v))
+    _want(lse, "lse", torch.float32, (n_tok, dims.H))
+    _check("mla_chunk_attn", lib().mla_chunk_attn(
+        ctypes.byref(dims), B, n_tok, _p(q), _p(tok_start), _p(q_pos), _p(w_uk), _p(w_uv), _p(cache),
+        cache.shape[0], _p(block_table), block_table.shape[1], _p(segs), segs.shape[1],
+        _ints(deltas), len(deltas), max_rows, _p(v), _p(lse), _p(workspace), _bytes(workspace),
+        _s(stream)))
+
+
+def linear_workspace_size(x, w) -> int:
+    """Bytes of workspace for linear(x, w, ...)."""
+    dt = MLA_BF16 if x.dtype == torch.bfloat16 else MLA_F32
+    return int(lib().mla_linear_workspace_size(dt, x.shape[0], w.shape[0], x.shape[1]))
+
+
+def linear(x, w, out, bias=None, act: str = "none", residual=None, workspace=None, stream=None):
+    """mla_linear: out [M, N] = act(x [M, K] w [N, K]^T + bias [N]) + residual [M, N]; matrices may
+    have any row stride; ``out`` may be ``residual``."""
+    if x.dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError(f"x must be float32 or bfloat16, got {x.dtype}")
+    if x.dim() != 2 or w.dim() != 2:
+        raise ValueError("x and w must be matrices")
+    (M, K), N = x.shape, w.shape[0]
+    _want(w, "w", x.dtype, (N, K))
+    _want(out, "out", x.dtype, (M, N))
+    _want(bias, "bias", torch.float32, (N,))
+    _want(residual, "residual", x.dtype, (M, N))
+    if act not in ACTIVATIONS:
+        raise ValueError(f"act must be one of {sorted(ACTIVATIONS)}")
+    _check("mla_linear", lib().mla_linear(
+        MLA_BF16 if x.dtype == torch.bfloat16 else MLA_F32, M, N, K, x.data_ptr(), _rows(x, "x"),
+        w.data_ptr(), _rows(w, "w"), _p(bias), ACTIVATIONS[act],
+        None if residual is None else residual.data_ptr(), _rows(residual, "residual"),
+        out.data_ptr(), _rows(out, "out"), _p(workspace), _bytes(workspace), _s(stream)))

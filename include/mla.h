@@ -24,7 +24,8 @@
  *     never traps.  mla_get_status() reads and clears that word.
  *   - Storage types: dims.dtype == MLA_BF16 means q_nope, q_rope, q_abs, the
  *     cache, W_UK, W_UV and W_O hold bfloat16; MLA_F32 means they hold float.
- *     Accumulation is always fp32; o_lat, lse, v and out are always float.
+ *     Accumulation is always fp32; o_lat, lse, v and out are always float
+ *     (mla_chunk_attn's v and mla_linear's out have the storage type).
  *   - Layouts are dense row-major in the index order written in brackets.
  *   - No C++ exception crosses this interface.
  */
@@ -430,6 +431,130 @@ mla_status_t mla_decode_qknorm(const mla_dims_t* dims, int32_t B, int32_t s_q,
                                const mla_seg_t* segs, int32_t max_segs, const int32_t* q_pos,
                                float* o_lat, float* lse, void* workspace, size_t ws_bytes,
                                mla_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * A chunk of new tokens per sequence (prompt processing), the counterpart of
+ * the decode step: mla_rope_axes on the projected queries, mla_append_tokens
+ * to write the tokens into the cache, mla_chunk_attn over the cached rows and
+ * mla_linear for the output projection onto the residual.
+ *
+ * Tokens of all sequences are rows of one array; sequence b owns the tokens
+ * [tok_start[b], tok_start[b + 1]) (tok_start [B + 1], int32, device,
+ * ascending from >= 0 to <= n_tok; equal neighbours: no new token).  Tokens
+ * outside every range (a padded batch) are left out and their output rows keep
+ * what they held.
+ *
+ * mla_rope_axes -- rotary positions with several axes (time, height, width of
+ * images and video; one axis for text).  [T27] "Position Rotations Complicate
+ * the Absorption", with the d_r / 2 pairs cut into n_axes runs of sections[a]
+ * pairs: pair i, in run a, turns by pos[a][token] * rope_base^(-2i/d_r) (i
+ * counted over the whole vector, adjacent pairs as in mla_absorb_q), or by the
+ * opposite angle with `inverse` (which is also the gradient with respect to
+ * x).  Angles are computed in double; the result is rounded to dtype once.
+ *   x, out     [n_tok, n_heads, d_r] (dtype) with strides of *_tok_stride and
+ *              *_head_stride elements (>= 0), the last axis contiguous: the
+ *              rotary slice of a [n_tok, H, d_n + d_r] query is passed as it
+ *              is.  out may be x itself with the same strides; no other overlap.
+ *              x may be broadcast (stride 0); out's vectors must not overlap.
+ *   pos        [n_axes, n_tok] int32 positions (any value, also negative)
+ *   sections   [n_axes] HOST, each >= 0, sum d_r / 2; 1 <= n_axes <= 4
+ * Reads d_r, rope_base and dtype of dims.  Errors: INVALID_ARG; UNSUPPORTED
+ * (n_axes > 4, d_r > 256). */
+mla_status_t mla_rope_axes(const mla_dims_t* dims, int32_t n_tok, int32_t n_heads, const void* x,
+                           int64_t x_tok_stride, int64_t x_head_stride, const int32_t* pos,
+                           int32_t n_axes, const int32_t* sections, int32_t inverse, void* out,
+                           int64_t out_tok_stride, int64_t out_head_stride, mla_stream_t stream);
+
+/* mla_append_tokens -- append a ragged chunk to the paged cache.  Token
+ * tok_start[b] + i of sequence b becomes the cache row of logical row row0[b] + i
+ * (page block_table[b][row / page_size], slot row % page_size):
+ *     [ c * norm_weight / sqrt(mean(c^2) + norm_eps) | R(pos) k ]
+ * from the raw row [c (d_c) | k (d_r)] of the down-projection, rounded to
+ * dtype once (sums in fp32, angles in double); [RK]: a document cached on its own takes
+ * positions from 0.
+ *   kv           [n_tok, >= d_c + d_r] rows of kv_stride elements (dtype)
+ *   row0         [B] int32 first logical row of each sequence's new tokens
+ *   pos, sections as mla_rope_axes
+ *   norm_weight  [d_c] float RMSNorm weight of the latent, or NULL: c as it is
+ *   norm_eps     >= 0 (read with norm_weight only)
+ *   bits_c, bits_r  0, 0: cache [n_pages, page_size, d_c + d_r] of dtype; (4, 4)
+ *                or (2, 4): a pool of packed rows as mla_pack_rows writes them
+ *                (4-byte aligned), the codes of the rounded row by scale_c
+ *                [d_c] and scale_r [d_r] (float; NULL exactly for plain rows).
+ *                What decides a code is computed in double.
+ * Only the addressed rows change.  Two tokens naming one row race.
+ * A token whose row or page id is out of range, or whose tok_start
+ * is out of order, is skipped and records BAD_INDEX.  Errors: INVALID_ARG;
+ * UNSUPPORTED (page_size != 64, other bit pairs or widths, n_axes > 4,
+ * d_r > 256). */
+mla_status_t mla_append_tokens(const mla_dims_t* dims, int32_t B, int32_t n_tok, const void* kv,
+                               int64_t kv_stride, const int32_t* tok_start, const int32_t* row0,
+                               const int32_t* pos, int32_t n_axes, const int32_t* sections,
+                               const float* norm_weight, float norm_eps, int32_t bits_c,
+                               int32_t bits_r, const float* scale_c, const float* scale_r,
+                               void* cache, int64_t n_pages, const int32_t* block_table,
+                               int32_t max_pages, mla_stream_t stream);
+
+/* mla_chunk_attn -- attention of every token of a ragged chunk over its
+ * sequence's cached rows (the new tokens' own rows are appended first).
+ * [T27] "The Direct Form Explains the Meaning": score(t) = scale * (q_nope .
+ * W_UK[h] c_t + q_rope . k_rope_t), masked where key_pos(t) > q_pos, softmaxed;
+ * v = sum_t a_t W_UV[h] c_t.
+ *   q            [n_tok, H, d_n + d_r] (dtype), rotary part already rotated at
+ *                the token's position(s) (mla_rope_axes); 16-byte aligned
+ *   tok_start    [B + 1], see above
+ *   q_pos        [n_tok] int32 request positions: the mask, not a rotation
+ *   w_uk, w_uv   [H, d_n, d_c], [H, d_v, d_c] (dtype), 16-byte aligned
+ *   cache, block_table, segs   as mla_decode (segs [B, max_segs])
+ *   delta        [n_ver] HOST relocation offsets of the segments' versions, as
+ *                given to mla_absorb_q ([RK]); every axis is shifted by delta
+ *   max_rows     bound on the rows of all sequences, each segment rounded up
+ *                to whole pages; a sequence that exceeds it is invalid
+ *   v            [n_tok, H, d_v] out (dtype), 16-byte aligned: mla_linear's x
+ *   lse          [n_tok, H] out (float) or NULL: natural-log sum of exp of the
+ *                scaled visible scores
+ *   workspace    ws_bytes >= mla_chunk_workspace_size(...) for the same
+ *                arguments, 256-byte aligned, contents need not be initialised
+ * A token that sees no row gets v = 0 and lse = -inf.  A row whose position is
+ * past a token's does not reach it, whatever it holds.  A sequence with an
+ * invalid segment table, page id or too many rows records BAD_INDEX and its
+ * tokens get NaN; one whose tok_start is out of order records BAD_INDEX and
+ * is left out.  bf16: products round their operands (expanded keys and values,
+ * weights of the softmax) to bf16, sums and statistics are fp32.
+ * Errors: INVALID_ARG (scale must be > 0), UNSUPPORTED (page_size != 64,
+ * n_ver > 8, row counts beyond 2^31 - 1), WORKSPACE. */
+mla_status_t mla_chunk_attn(const mla_dims_t* dims, int32_t B, int32_t n_tok, const void* q,
+                            const int32_t* tok_start, const int32_t* q_pos, const void* w_uk,
+                            const void* w_uv, const void* cache, int64_t n_pages,
+                            const int32_t* block_table, int32_t max_pages, const mla_seg_t* segs,
+                            int32_t max_segs, const int32_t* delta, int32_t n_ver,
+                            int64_t max_rows, void* v, float* lse, void* workspace,
+                            size_t ws_bytes, mla_stream_t stream);
+
+/* Bytes of workspace mla_chunk_attn needs on the current device (0 if the
+ * arguments are invalid or the device cannot be queried). */
+size_t mla_chunk_workspace_size(const mla_dims_t* dims, int32_t B, int32_t n_tok, int32_t n_ver,
+                                int32_t max_pages, int32_t max_segs, int64_t max_rows);
+
+/* mla_linear -- out = act(x W^T + bias) + residual: a layer's projection with
+ * its epilogue, e.g. the output projection W_O of a chunk's values onto the
+ * residual stream ([T27] "Move the Value Expansion After the Weighted Sum").
+ *   x [M, K], w [N, K], residual [M, N] or NULL, out [M, N] (dtype), rows of
+ *   the given strides (elements, >= the row); bias [N] (float) or NULL;
+ *   act 0 none, 1 SiLU, 2 GELU (erf).  Sums, bias, activation and residual are
+ *   added in fp32 and rounded once.  out may be residual itself (same stride).
+ * bf16 operands with 16-byte aligned rows run on the tensor cores; others on
+ * the CUDA cores.  workspace: ws_bytes >= mla_linear_workspace_size (0 bytes:
+ * may be NULL), 256-byte aligned.  Results do not depend on timing.
+ * Errors: INVALID_ARG, UNSUPPORTED (sizes past the launch limits), WORKSPACE. */
+mla_status_t mla_linear(int32_t dtype, int32_t M, int32_t N, int32_t K, const void* x,
+                        int64_t x_stride, const void* w, int64_t w_stride, const float* bias,
+                        int32_t act, const void* residual, int64_t res_stride, void* out,
+                        int64_t out_stride, void* workspace, size_t ws_bytes, mla_stream_t stream);
+
+/* Bytes of workspace mla_linear needs on the current device (often 0; 0 too
+ * if the arguments are invalid or the device cannot be queried). */
+size_t mla_linear_workspace_size(int32_t dtype, int32_t M, int32_t N, int32_t K);
 
 #ifdef __cplusplus
 }  /* extern "C" */
