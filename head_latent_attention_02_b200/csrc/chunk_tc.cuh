@@ -44,9 +44,11 @@ constexpr int kQTile = 128, kKTile = 128;
 constexpr int kItemTokens = 2 * kQTile;
 constexpr int kPanel = 128 * 128;            // 128 rows x 64 bf16: 16 KB
 constexpr int kQBytes = 3 * kPanel;          // a query tile: two nope panels, one rope panel
-constexpr int kRing = 8;                     // panels in flight: a tile's keys take 3, its values 2
+constexpr int kSlot = 2 * kPanel;            // a tile's keys (without the rotary part) or its values
+constexpr int kSlots = 3, kRotSlots = 2;
 constexpr int kOffRing = 2 * kQBytes;
-constexpr int kOffBar = kOffRing + kRing * kPanel;
+constexpr int kOffRot = kOffRing + kSlots * kSlot;
+constexpr int kOffBar = kOffRot + kRotSlots * kPanel;
 constexpr int kSmemBytes = kOffBar + 512 + 1024;
 constexpr int kThreads = 320;
 constexpr int kTmemCols = 512;
@@ -82,7 +84,8 @@ struct Params {
 
 // Tensor maps (64 columns, 128-byte swizzle):
 //   q   (column, token, panel) over q [n_tok, H x 192], box {64, 128, 3}
-//   k,v (column, row, panel) over the scratch [heads x rows_cap, 128], box {64, 128, 2}
+//   k,v (column, row, panel) over the scratch [heads x rows_cap, 128], box
+//       {64, 128, 2}: two 64-column panels of 16 KB
 //   kr  (column, row) over the rotary scratch [rows_cap, 64], box {64, 128}
 struct Maps {
   CUtensorMap q, k, v, kr;
@@ -90,15 +93,23 @@ struct Maps {
 
 struct Bars {
   uint64_t q_full[2];
-  uint64_t full[kRing], empty[kRing];
+  uint64_t full[kSlots], empty[kSlots];        // keys of tile 0, values of tile 0, keys of tile 1, ...
+  uint64_t rot_full[kRotSlots], rot_empty[kRotSlots];
   uint64_t s_full[2], p_full[2], o_full[2];
   uint32_t tmem_base;
   int n_tiles[2];
-  int q_max[2];
+  int q_max[2], q_min[2];
+  int n_full[2];               // leading tiles that every query of the tile sees whole
 };
 static_assert(sizeof(Bars) <= 512, "barrier block too large");
 
-__device__ __forceinline__ float exp2_fast(float x) { return ex2_approx(x); }
+// max that keeps NaN (fmaxf drops it): a NaN score makes the row's maximum, and
+// with it the whole row, NaN.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float y;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+  return y;
+}
 
 // Visible rows of one page: those with data whose position is not past qp.
 __device__ __forceinline__ int visible(const gm::PageEntry& e, int qp) {
@@ -139,24 +150,39 @@ chunk_attn_kernel(const __grid_constant__ Params p, const __grid_constant__ Maps
       mbar_init(&bar->o_full[t], 1);
       bar->n_tiles[t] = 0;
       bar->q_max[t] = INT32_MIN;
+      bar->q_min[t] = INT32_MAX;
+      bar->n_full[t] = INT32_MAX;
     }
-    for (int i = 0; i < kRing; ++i) {
+    for (int i = 0; i < kSlots; ++i) {
       mbar_init(&bar->full[i], 1);
       mbar_init(&bar->empty[i], 1);
+    }
+    for (int i = 0; i < kRotSlots; ++i) {
+      mbar_init(&bar->rot_full[i], 1);
+      mbar_init(&bar->rot_empty[i], 1);
     }
     fence_mbar_init();
   }
   if (warp == 1) tmem_alloc(&bar->tmem_base, kTmemCols);
   __syncthreads();
-  // the last tile that each query tile sees: no query's position lies before it
-  if (threadIdx.x < it.n) atomicMax(&bar->q_max[threadIdx.x >> 7], p.q_pos[it.tok0 + threadIdx.x]);
+  // the tiles that each query tile needs (up to the last one that any of its
+  // queries sees) and the leading ones that need no mask
+  if (threadIdx.x < it.n) {
+    const int qp = p.q_pos[it.tok0 + threadIdx.x];
+    atomicMax(&bar->q_max[threadIdx.x >> 7], qp);
+    atomicMin(&bar->q_min[threadIdx.x >> 7], qp);
+  }
   __syncthreads();
   for (int j = threadIdx.x; j < it.tiles; j += kThreads) {
     const gm::PageEntry e0 = p.pages[it.entry + 2 * j], e1 = p.pages[it.entry + 2 * j + 1];
 #pragma unroll
-    for (int t = 0; t < 2; ++t)
-      if (t * kQTile < it.n && (visible(e0, bar->q_max[t]) > 0 || visible(e1, bar->q_max[t]) > 0))
+    for (int t = 0; t < 2; ++t) {
+      if (t * kQTile >= it.n) continue;
+      if (visible(e0, bar->q_max[t]) > 0 || visible(e1, bar->q_max[t]) > 0)
         atomicMax(&bar->n_tiles[t], j + 1);
+      if (visible(e0, bar->q_min[t]) < kPage || visible(e1, bar->q_min[t]) < kPage)
+        atomicMin(&bar->n_full[t], j);
+    }
   }
   tc_fence_before();
   __syncthreads();
@@ -177,29 +203,30 @@ chunk_attn_kernel(const __grid_constant__ Params p, const __grid_constant__ Maps
         mbar_arrive_expect_tx(&bar->q_full[t], kQBytes);
         tma_load_3d(smem + t * kQBytes, &mp.q, &bar->q_full[t], 0, it.tok0 + t * kQTile, 3 * h);
       };
-      int n = 0;
       bool ok = true;
-      // panel i of tile j: i 0, 1 the keys' panels, 2 the rotary keys, 3, 4 the values'
-      auto load = [&](int j, int i) {
-        const int slot = n % kRing;
-        if (!mbar_wait(&bar->empty[slot], ((n / kRing) & 1) ^ 1)) {
+      auto wait = [&](uint64_t* b, int use) {      // the slot's use-th filling may start
+        if (!mbar_wait(b, (use & 1) ^ 1)) {
           set_status(MLA_ERR_TIMEOUT);
-          return false;
+          ok = false;
         }
-        uint8_t* dst = smem + kOffRing + slot * kPanel;
-        mbar_arrive_expect_tx(&bar->full[slot], kPanel);
-        if (i < 2) tma_load_3d(dst, &mp.k, &bar->full[slot], 0, krow + j * kKTile, i);
-        else if (i == 2) tma_load_2d(dst, &mp.kr, &bar->full[slot], 0, it.entry * kPage + j * kKTile);
-        else tma_load_3d(dst, &mp.v, &bar->full[slot], 0, krow + j * kKTile, i - 3);
-        ++n;
-        return true;
+        return ok;
+      };
+      auto load = [&](const CUtensorMap* map, int n, int row) {
+        const int slot = n % kSlots;
+        if (!wait(&bar->empty[slot], n / kSlots)) return;
+        mbar_arrive_expect_tx(&bar->full[slot], kSlot);
+        tma_load_3d(smem + kOffRing + slot * kSlot, map, &bar->full[slot], 0, row, 0);
       };
       if (nt0 > 0) load_q(0);
       for (int j = 0; ok && j < nt; ++j) {
-        for (int i = 0; ok && i < 5; ++i) {
-          ok = load(j, i);
-          if (j == 0 && i == 2 && nt1 > 0) load_q(1);
-        }
+        load(&mp.k, 2 * j, krow + j * kKTile);
+        const int rs = j % kRotSlots;
+        if (!ok || !wait(&bar->rot_empty[rs], j / kRotSlots)) break;
+        mbar_arrive_expect_tx(&bar->rot_full[rs], kPanel);
+        tma_load_2d(smem + kOffRot + rs * kPanel, &mp.kr, &bar->rot_full[rs], 0,
+                    it.entry * kPage + j * kKTile);
+        if (j == 0 && nt1 > 0) load_q(1);
+        load(&mp.v, 2 * j + 1, krow + j * kKTile);
       }
     }
   } else if (warp == 1) {
@@ -207,7 +234,15 @@ chunk_attn_kernel(const __grid_constant__ Params p, const __grid_constant__ Maps
     if (lane == 0 && nt > 0) {
       constexpr uint32_t idesc_s = idesc_bf16_f32(kQTile, kKTile, false, false);
       constexpr uint32_t idesc_o = idesc_bf16_f32(kQTile, kDv, false, true);
-      const uint32_t ring = smem_u32(smem + kOffRing);
+      // Descriptors of the first panels; a panel, a slot or a K step further is
+      // an addition (16-byte units) that never leaves the address field.  The
+      // issuing thread shares its scheduler with softmax warps: building each
+      // descriptor anew cost it 1400 clocks for the eight MMAs of a P V.
+      const uint64_t dq = smem_desc_sw128(smem_u32(smem), 16, 1024);
+      const uint64_t dk = smem_desc_sw128(smem_u32(smem + kOffRing), 16, 1024);
+      const uint64_t dr = smem_desc_sw128(smem_u32(smem + kOffRot), 16, 1024);
+      // values: 16 rows of both 64-column panels per step, rows outermost
+      const uint64_t dv = smem_desc_sw128(smem_u32(smem + kOffRing), kPanel, 1024);
       bool ok = true;
       auto wait = [&](uint64_t* b, uint32_t parity) {
         if (ok && !mbar_wait(b, parity)) {
@@ -215,18 +250,13 @@ chunk_attn_kernel(const __grid_constant__ Params p, const __grid_constant__ Maps
           ok = false;
         }
       };
-      // panel n of the stream of panels: tile j's keys are 5 j .. 5 j + 2, its
-      // values 5 j + 3 and 5 j + 4
-      auto wait_panels = [&](int n, int count) {
-        for (int i = n; i < n + count; ++i) wait(&bar->full[i % kRing], (i / kRing) & 1);
-        tc_fence_after();
-      };
-      auto free_panels = [&](int n, int count) {
-        for (int i = n; i < n + count; ++i) mma_commit(&bar->empty[i % kRing]);
-      };
       for (int j = 0; ok && j <= nt; ++j) {
-        if (j > 0) wait_panels(5 * (j - 1) + 3, 2);
-        if (j < nt) wait_panels(5 * j, 3);
+        const int kn = 2 * j, vn = 2 * j - 1;      // their places in the stream of slots
+        const int ks_n = kn % kSlots, vs_n = vn < 0 ? 0 : vn % kSlots;   // and their slots
+        if (j > 0) wait(&bar->full[vs_n], (vn / kSlots) & 1);
+        if (!ok) break;
+        const uint64_t kd = dk + ks_n * (kSlot >> 4), vd = dv + vs_n * (kSlot >> 4);
+        const uint64_t rd = dr + (j % kRotSlots) * (kPanel >> 4);
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
           const int mine = t ? nt1 : nt0;
@@ -235,44 +265,39 @@ chunk_attn_kernel(const __grid_constant__ Params p, const __grid_constant__ Maps
             wait(&bar->p_full[t], (j - 1) & 1);
             tc_fence_after();
             if (!ok) break;
-            // 16 rows of both 64-column value panels per step, rows outermost
-            const int n0 = 5 * (j - 1) + 3;
-            const uint32_t v0 = ring + (n0 % kRing) * kPanel, v1 = ring + ((n0 + 1) % kRing) * kPanel;
-            // the panels' distance; the ring may put the second one first
 #pragma unroll
-            for (int ks = 0; ks < 8; ++ks) {
-              if (v1 > v0) {
-                mma_bf16_ts(o_col, s_col + 8 * ks, smem_desc_sw128(v0 + ks * 2048, v1 - v0, 1024),
-                            idesc_o, (j > 1 || ks > 0) ? 1u : 0u);
-              } else {
-                constexpr uint32_t idesc_h = idesc_bf16_f32(kQTile, 64, false, true);
-                mma_bf16_ts(o_col, s_col + 8 * ks, smem_desc_sw128(v0 + ks * 2048, kPanel, 1024),
-                            idesc_h, (j > 1 || ks > 0) ? 1u : 0u);
-                mma_bf16_ts(o_col + 64, s_col + 8 * ks,
-                            smem_desc_sw128(v1 + ks * 2048, kPanel, 1024), idesc_h,
-                            (j > 1 || ks > 0) ? 1u : 0u);
-              }
-            }
+            for (int ks = 0; ks < 8; ++ks)
+              mma_bf16_ts(o_col, s_col + 8 * ks, vd + ks * (2048 >> 4), idesc_o,
+                          (j > 1 || ks > 0) ? 1u : 0u);
             if (j == mine) mma_commit(&bar->o_full[t]);
           }
+          // both query tiles are done with the values: their slot takes the
+          // keys of the next step, whose load needs all the time it can get
+          if (t == 1 && j > 0) mma_commit(&bar->empty[vs_n]);
           if (j < mine) {
-            wait(&bar->q_full[t], 0);
-            if (!ok) break;
-            const uint32_t q0 = smem_u32(smem + t * kQBytes);
-#pragma unroll
-            for (int pn = 0; pn < 3; ++pn) {
-              const uint32_t kb = ring + ((5 * j + pn) % kRing) * kPanel;
-#pragma unroll
-              for (int ks = 0; ks < 4; ++ks)
-                mma_bf16_ss(s_col, smem_desc_sw128(q0 + pn * kPanel + ks * 32, 16, 1024),
-                            smem_desc_sw128(kb + ks * 32, 16, 1024), idesc_s,
-                            (pn | ks) ? 1u : 0u);
+            if (t == 0 || nt0 <= j) {      // the first query tile of the step
+              wait(&bar->full[ks_n], (kn / kSlots) & 1);
+              wait(&bar->rot_full[j % kRotSlots], (j / kRotSlots) & 1);
             }
+            if (j == 0) wait(&bar->q_full[t], 0);
+            tc_fence_after();
+            if (!ok) break;
+            const uint64_t qd = dq + t * (kQBytes >> 4);
+#pragma unroll
+            for (int ks = 0; ks < 8; ++ks) {
+              const uint32_t at = (ks >> 2) * (kPanel >> 4) + (ks & 3) * 2;
+              mma_bf16_ss(s_col, qd + at, kd + at, idesc_s, ks ? 1u : 0u);
+            }
+#pragma unroll
+            for (int ks = 0; ks < 4; ++ks)
+              mma_bf16_ss(s_col, qd + 2 * (kPanel >> 4) + ks * 2, rd + ks * 2, idesc_s, 1u);
             mma_commit(&bar->s_full[t]);
           }
         }
-        if (j > 0) free_panels(5 * (j - 1) + 3, 2);
-        if (j < nt) free_panels(5 * j, 3);
+        if (j < nt) {
+          mma_commit(&bar->empty[ks_n]);
+          mma_commit(&bar->rot_empty[j % kRotSlots]);
+        }
       }
     }
   } else {
@@ -290,14 +315,14 @@ chunk_attn_kernel(const __grid_constant__ Params p, const __grid_constant__ Maps
     bool ok = true;
     if (mine > 0) {
       const gm::PageEntry* pe = p.pages + it.entry;
-      gm::PageEntry e0 = pe[0], e1 = pe[1];
+      const int n_full = bar->n_full[t];
       for (int j = 0; j < mine; ++j) {
-        const int v0 = visible(e0, qp), v1 = visible(e1, qp);
-        if (j + 1 < mine) {
-          e0 = pe[2 * j + 2];
-          e1 = pe[2 * j + 3];
+        int v0 = kPage, v1 = kPage;
+        if (j >= n_full) {
+          v0 = visible(pe[2 * j], qp);
+          v1 = visible(pe[2 * j + 1], qp);
         }
-        const bool all = __all_sync(0xffffffffu, v0 == kPage && v1 == kPage);
+        const bool all = j < n_full || __all_sync(0xffffffffu, v0 == kPage && v1 == kPage);
         if (!__all_sync(0xffffffffu, mbar_wait(&bar->s_full[t], j & 1))) {
           if (lane == 0) set_status(MLA_ERR_TIMEOUT);
           ok = false;
@@ -316,16 +341,16 @@ chunk_attn_kernel(const __grid_constant__ Params p, const __grid_constant__ Maps
         float mx[4];
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-          mx[c] = fmaxf(s[c][0], s[c][1]);
+          mx[c] = max_nan(s[c][0], s[c][1]);
 #pragma unroll
-          for (int i = 2; i < 32; i += 2) mx[c] = fmaxf(mx[c], fmaxf(s[c][i], s[c][i + 1]));
+          for (int i = 2; i < 32; i += 2) mx[c] = max_nan(mx[c], max_nan(s[c][i], s[c][i + 1]));
         }
-        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-        const bool raise = top * p.scale_log2 > m * p.scale_log2 + kMargin;
+        const float top = max_nan(max_nan(mx[0], mx[1]), max_nan(mx[2], mx[3]));
+        const bool raise = !(top * p.scale_log2 <= m * p.scale_log2 + kMargin);   // or NaN
         if (__any_sync(0xffffffffu, raise)) {
           const float m_new = raise ? top : m;
           // nothing seen so far (m = -inf): sums and O are zero whatever the factor
-          const float f = m_new == m ? 1.f : exp2_fast((m - m_new) * p.scale_log2);
+          const float f = m_new == m ? 1.f : ex2_approx((m - m_new) * p.scale_log2);
           l *= f;
           m = m_new;
           if (j > 0) {
@@ -347,8 +372,9 @@ chunk_attn_kernel(const __grid_constant__ Params p, const __grid_constant__ Maps
 #pragma unroll
           for (int i = 0; i < 32; ++i) {
             const int c0 = 2 * c + i / 16, i0 = 2 * (i % 16);
-            const float a = exp2_fast(fmaf(s[c0][i0], p.scale_log2, off));
-            const float b = exp2_fast(fmaf(s[c0][i0 + 1], p.scale_log2, off));
+            const float x = fmaf(s[c0][i0], p.scale_log2, off);
+            const float y = fmaf(s[c0][i0 + 1], p.scale_log2, off);
+            const float a = ex2_approx(x), b = ex2_approx(y);
             sum[i & 3] += a + b;
             w[i] = __uint_as_float(gm::pack2(a, b));
           }

@@ -59,6 +59,7 @@ struct PageEntry {
 
 struct Params {
   int k_steps, n_mt, n_nt, BN, stages;
+  int P;                     // 64-K panels of a stage; > 1: three-axis maps over whole panels
   int chunk;                 // split: units of a pair's run; 0: whole tiles
   // linear: the M x N result; swapped: A holds W's rows and B x's
   int swapped, M, N, act;
@@ -162,7 +163,9 @@ __device__ __forceinline__ void finish8(const Params& p, int m, int n, const flo
 
 enum Mode : int { kLinear = 0, kExpand = 1 };
 
-// linear: ta over A, box {64, 128}; tb over B, box {64, BN / 2}.  expand: ta
+// linear: ta over A, box {64, 128}; tb over B, box {64, BN / 2}; with P > 1 both
+// as (64-column offset, row, panel), P panels deep, so that a box row is 128 P
+// contiguous bytes.  expand: ta
 // over the cache rows, box {64, 64}; tb / tv over W_UK / W_UV seen as
 // [heads x 128, 512], box {64, 128}: the first CTA's half of B is W_UK[h],
 // the second's W_UV[h], so columns 0 .. 127 of the tile are keys and the rest
@@ -175,8 +178,10 @@ gemm_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtensorMa
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int S = p.stages;
-  const int b_bytes = p.BN / 2 * 128;
-  const int stage = kABytes + b_bytes;
+  const int P = kMode == kExpand ? 1 : p.P;
+  const int b_panel = p.BN / 2 * 128;
+  const int a_bytes = P * kABytes;
+  const int stage = a_bytes + P * b_panel;
   Bars* bar = reinterpret_cast<Bars*>(smem + S * stage);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
@@ -237,8 +242,14 @@ gemm_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtensorMa
             tma_load_2d_pair(dst + kABytes / 2, &ta, fb, k * kKStep, y1);
             tma_load_2d_pair(dst + kABytes, rank ? &tv : &tb, fb, k * kKStep, nt * 128);
           } else {
-            tma_load_2d_pair(dst, &ta, fb, k * kKStep, mt * kPairRows + (int)rank * kRows);
-            tma_load_2d_pair(dst + kABytes, &tb, fb, k * kKStep, nt * p.BN + (int)rank * (p.BN / 2));
+            const int ra = mt * kPairRows + (int)rank * kRows, rb = nt * p.BN + (int)rank * (p.BN / 2);
+            if (P == 1) {
+              tma_load_2d_pair(dst, &ta, fb, k * kKStep, ra);
+              tma_load_2d_pair(dst + a_bytes, &tb, fb, k * kKStep, rb);
+            } else {
+              tma_load_3d_pair(dst, &ta, fb, 0, ra, k * P);
+              tma_load_3d_pair(dst + a_bytes, &tb, fb, 0, rb, k * P);
+            }
           }
         }
       }
@@ -264,12 +275,14 @@ gemm_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtensorMa
             break;
           }
           tc_fence_after();
-          const uint32_t a0 = smem_u32(smem + slot * stage), b0 = a0 + kABytes;
+          const uint32_t a0 = smem_u32(smem + slot * stage), b0 = a0 + a_bytes;
+          for (int pn = 0; pn < P; ++pn)
 #pragma unroll
-          for (int ks = 0; ks < 4; ++ks)
-            mma_pair_bf16_ss(tmem + ab * kMaxBN, smem_desc_sw128(a0 + ks * 32, 16, 1024),
-                             smem_desc_sw128(b0 + ks * 32, 16, 1024), idesc,
-                             (k == s.k0 && ks == 0) ? 0u : 1u);
+            for (int ks = 0; ks < 4; ++ks)
+              mma_pair_bf16_ss(tmem + ab * kMaxBN,
+                               smem_desc_sw128(a0 + pn * kABytes + ks * 32, 16, 1024),
+                               smem_desc_sw128(b0 + pn * b_panel + ks * 32, 16, 1024), idesc,
+                               (k == s.k0 && (pn | ks) == 0) ? 0u : 1u);
           mma_pair_commit_both(&bar->empty[slot]);
         }
         if (ok) mma_pair_commit_both(&bar->acc_full[ab]);

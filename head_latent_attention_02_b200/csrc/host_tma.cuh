@@ -61,6 +61,16 @@ static inline bool map_rows(CUtensorMap* m, const void* base, uint64_t cols, uin
   return map_bf16(m, base, 2, extent, stride, box);
 }
 
+// The same matrix as (64-column offset, row, 64-column panel) in boxes of 64 x
+// box_rows x panels: a box row is 128 * panels contiguous bytes, which the
+// memory serves better than single 128-byte pieces.  cols is a multiple of 64.
+static inline bool map_panels(CUtensorMap* m, const void* base, uint64_t cols, uint64_t rows,
+                              uint64_t pitch, uint32_t box_rows, uint32_t panels) {
+  const uint64_t extent[3] = {64, rows, cols / 64}, stride[2] = {pitch * 2, 128};
+  const uint32_t box[3] = {64, box_rows, panels};
+  return map_bf16(m, base, 3, extent, stride, box);
+}
+
 // SMs of the current device; 0 when it cannot be queried.
 static inline int current_sms() {
   int dev = 0, sms = 0;

@@ -418,7 +418,7 @@ mla_status_t run_expanded(const mla_dims_t* d, const ChunkArgs& a, const Layout&
   const uint32_t q_box[3] = {64, ck::kQTile, 3};
   const uint64_t s_ext[3] = {64, (uint64_t)l.rows_cap * l.heads, 2};
   const uint64_t s_str[2] = {(uint64_t)ck::kDn * 2, 128};
-  const uint32_t s_box[3] = {64, ck::kKTile, 1};
+  const uint32_t s_box[3] = {64, ck::kKTile, 2};
   if (!map_rows(&tc, a.cache, ck::kDc, cache_rows, ck::kDc + ck::kDr, kPage) ||
       !map_bf16(&mp.q, a.q, 3, q_ext, q_str, q_box) ||
       !map_bf16(&mp.k, ws + l.k, 3, s_ext, s_str, s_box) ||

@@ -150,7 +150,7 @@ __global__ void __launch_bounds__(256) linear_finish_kernel(const __grid_constan
 }
 
 struct TilePlan {
-  int swapped, BN, n_mt, n_nt, k_steps, stages, chunk, grid;
+  int swapped, BN, n_mt, n_nt, P, k_steps, stages, chunk, grid;
   size_t ws;
 };
 
@@ -163,8 +163,11 @@ struct TilePlan {
 TilePlan plan_tiles(int M, int N, int K, int sms) {
   TilePlan t = {};
   const int pairs = sms / 2 > 0 ? sms / 2 : 1;
-  t.k_steps = (K + gm::kKStep - 1) / gm::kKStep;
   t.swapped = M <= 128;
+  // panels of a stage: long box rows where W is streamed once
+  t.P = K % 64 == 0 && t.swapped ? (M <= 32 ? 4 : 2) : 1;
+  const int step_k = gm::kKStep * t.P;
+  t.k_steps = (K + step_k - 1) / step_k;
   double best = 0;
   const int rows = t.swapped ? N : M, cols = t.swapped ? M : N;
   t.n_mt = (rows + gm::kPairRows - 1) / gm::kPairRows;
@@ -172,11 +175,11 @@ TilePlan plan_tiles(int M, int N, int K, int sms) {
     if (t.swapped ? (bn != (cols + 31) / 32 * 32) : (bn < 64 && cols > bn)) continue;
     const long long n_nt = (cols + bn - 1) / bn, tiles = (long long)t.n_mt * n_nt;
     const double load = (gm::kRows + bn / 2) * 128 / 60.0;
-    const double step = 2.0 * bn > load ? 2.0 * bn : load;
+    const double step = t.P * (2.0 * bn > load ? 2.0 * bn : load);
     const long long units = tiles * t.k_steps;
     // a run of at least eight steps, so that a partial sum is worth its trip
     long long run = (units + pairs - 1) / pairs;
-    if (run < 8) run = 8 < t.k_steps ? 8 : t.k_steps;
+    if (run * t.P < 8) run = (8 + t.P - 1) / t.P < t.k_steps ? (8 + t.P - 1) / t.P : t.k_steps;
     const double whole = (double)((tiles + pairs - 1) / pairs) * t.k_steps * step;
     const double split = (double)run * step + 6000;
     const bool use_split = split < whole;
@@ -191,7 +194,7 @@ TilePlan plan_tiles(int M, int N, int K, int sms) {
       t.ws = use_split ? (size_t)(2 * g) * bn * gm::kPairRows * sizeof(float) : 0;
     }
   }
-  const int stage = gm::kABytes + t.BN / 2 * 128;
+  const int stage = t.P * (gm::kABytes + t.BN / 2 * 128);
   t.stages = (gm::kSmemMax - gm::kBarBytes - 1024) / stage;
   if (t.stages > gm::kMaxStages) t.stages = gm::kMaxStages;
   return t;
@@ -265,6 +268,7 @@ extern "C" mla_status_t mla_linear(int32_t dtype, int32_t M, int32_t N, int32_t 
   p.n_nt = t.n_nt;
   p.BN = t.BN;
   p.stages = t.stages;
+  p.P = t.P;
   p.chunk = t.chunk;
   p.swapped = t.swapped;
   p.M = M;
@@ -282,10 +286,13 @@ extern "C" mla_status_t mla_linear(int32_t dtype, int32_t M, int32_t N, int32_t 
   const void* a = t.swapped ? w : x;
   const void* b = t.swapped ? x : w;
   const uint64_t ar = t.swapped ? N : M, br = t.swapped ? M : N;
-  if (!map_rows(&ta, a, K, ar, t.swapped ? w_stride : x_stride, gm::kRows) ||
-      !map_rows(&tb, b, K, br, t.swapped ? x_stride : w_stride, t.BN / 2))
-    return MLA_ERR_CUDA;
-  const int smem = t.stages * (gm::kABytes + t.BN / 2 * 128) + gm::kBarBytes + 1024;
+  const uint64_t as = t.swapped ? w_stride : x_stride, bs = t.swapped ? x_stride : w_stride;
+  const bool mapped = t.P == 1 ? map_rows(&ta, a, K, ar, as, gm::kRows) &&
+                                     map_rows(&tb, b, K, br, bs, t.BN / 2)
+                               : map_panels(&ta, a, K, ar, as, gm::kRows, t.P) &&
+                                     map_panels(&tb, b, K, br, bs, t.BN / 2, t.P);
+  if (!mapped) return MLA_ERR_CUDA;
+  const int smem = t.stages * t.P * (gm::kABytes + t.BN / 2 * 128) + gm::kBarBytes + 1024;
   if (cudaFuncSetAttribute(gm::gemm_kernel<gm::kLinear>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            gm::kSmemMax) != cudaSuccess)
     return MLA_ERR_CUDA;

@@ -29,10 +29,11 @@
 namespace mla {
 namespace {
 
-constexpr int kMaxPairs = 128;      // d_r <= 256
+constexpr int kMaxPairs = 64;       // d_r <= 128
 constexpr int kMaxAxes = 4;
 constexpr int kRopeThreads = 256;
 constexpr int kRopeUnroll = 4;
+constexpr int kRopeTokens = 8;      // tokens of a block at most
 constexpr int kTokThreads = 256;    // append: a warp per token
 
 // Frequencies of the pairs, and the first pair of each axis' run.
@@ -58,7 +59,12 @@ bool make_axes(const mla_dims_t* d, int n_axes, const int32_t* sections, Axes* a
     sum += sections[i];
   }
   for (int i = n_axes; i <= kMaxAxes; ++i) ax->first[i] = sum;
-  for (int i = 0; i < ax->half; ++i) ax->theta[i] = std::pow(d->rope_base, -2.0 * i / d->d_r);
+  // base^(-2i / d_r) as powers of one ratio: 128 products in 80-bit arithmetic
+  // stay far below half a unit of the double they are rounded to, and cost the
+  // host 0.1 us where as many calls of pow take 2 us of a 4 us launch
+  const long double ratio = powl((long double)d->rope_base, -2.0L / d->d_r);
+  long double th = 1.0L;
+  for (int i = 0; i < ax->half; ++i, th *= ratio) ax->theta[i] = (double)th;
   return sum == ax->half;
 }
 
@@ -108,7 +114,7 @@ __device__ __forceinline__ void turn(float2 cs, float x0, float x1, float& y0, f
 
 // ---------------------------------------------------------------------------
 struct RopeArgs {
-  int n_tok, n_heads, heads_per_block;
+  int n_tok, n_heads, heads_per_block, tok_per_block;
   int inverse;
   long long x_tok, x_head, o_tok, o_head;   // strides in elements
   const int32_t* pos;                       // [n_axes, n_tok]
@@ -116,26 +122,26 @@ struct RopeArgs {
   void* out;
 };
 
-// grid (n_tok, head blocks).  The block computes its token's sines and cosines
-// once, in shared memory, while the vectors it will turn are on their way:
-// a thread issues its loads before it waits for the table.  kVec: 16-byte
-// accesses (d_r, strides and pointers are multiples of eight elements).
+// grid (token blocks, head blocks).  A block computes the sines and cosines of
+// its tokens once, in shared memory, while the vectors they turn are on their
+// way: a thread issues its loads before it waits for the table.  kVec:
+// 16-byte accesses (d_r, strides and pointers are multiples of eight elements).
 template <typename T, bool kVec>
 __global__ void __launch_bounds__(kRopeThreads) rope_axes_kernel(const __grid_constant__ RopeArgs a,
                                                                  const __grid_constant__ Axes ax) {
   using CS = typename Trig<T>::type;
-  __shared__ CS cs[kMaxPairs];
-  const int t = blockIdx.x;
-  const int h0 = blockIdx.y * a.heads_per_block;
-  const int nh = min(a.heads_per_block, a.n_heads - h0);
-  const T* x = static_cast<const T*>(a.x) + (long long)t * a.x_tok + (long long)h0 * a.x_head;
-  T* out = static_cast<T*>(a.out) + (long long)t * a.o_tok + (long long)h0 * a.o_head;
+  __shared__ CS cs[kRopeTokens * kMaxPairs];
+  const int t0 = blockIdx.x * a.tok_per_block, nt = min(a.tok_per_block, a.n_tok - t0);
+  const int h0 = blockIdx.y * a.heads_per_block, nh = min(a.heads_per_block, a.n_heads - h0);
+  const T* x = static_cast<const T*>(a.x) + (long long)t0 * a.x_tok + (long long)h0 * a.x_head;
+  T* out = static_cast<T*>(a.out) + (long long)t0 * a.o_tok + (long long)h0 * a.o_head;
   const int per = kVec ? ax.half / 4 : ax.half;      // work items of a head
-  const int n = nh * per;
+  const int n = nt * nh * per;
   auto table = [&] {
-    for (int i = threadIdx.x; i < ax.half; i += kRopeThreads) {
+    for (int i = threadIdx.x; i < nt * ax.half; i += kRopeThreads) {
+      const int t = i / ax.half, p = i % ax.half;
       double sn, c;
-      sincos((double)a.pos[(size_t)ax.axis_of(i) * a.n_tok + t] * ax.theta[i], &sn, &c);
+      sincos((double)a.pos[(size_t)ax.axis_of(p) * a.n_tok + t0 + t] * ax.theta[p], &sn, &c);
       if (a.inverse) sn = -sn;
       cs[i].x = c;
       cs[i].y = sn;
@@ -145,32 +151,34 @@ __global__ void __launch_bounds__(kRopeThreads) rope_axes_kernel(const __grid_co
   if constexpr (kVec) {
     for (int base = 0; base < n; base += kRopeThreads * kRopeUnroll) {
       float v[kRopeUnroll][8];
+      int t[kRopeUnroll], h[kRopeUnroll], p0[kRopeUnroll];
 #pragma unroll
       for (int u = 0; u < kRopeUnroll; ++u) {
         const int i = base + u * kRopeThreads + threadIdx.x;
-        if (i < n) load8(x + (long long)(i / per) * a.x_head + (i % per) * 8, v[u]);
+        p0[u] = i % per * 4;
+        h[u] = i / per % nh;
+        t[u] = i / per / nh;
+        if (i < n) load8(x + t[u] * a.x_tok + h[u] * a.x_head + p0[u] * 2, v[u]);
       }
       if (base == 0) table();
 #pragma unroll
       for (int u = 0; u < kRopeUnroll; ++u) {
-        const int i = base + u * kRopeThreads + threadIdx.x;
-        if (i >= n) break;
-        const int p0 = (i % per) * 4;
+        if (base + u * kRopeThreads + (int)threadIdx.x >= n) break;
+        const CS* c = cs + t[u] * ax.half + p0[u];
         float y[8];
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-          turn(cs[p0 + j], v[u][2 * j], v[u][2 * j + 1], y[2 * j], y[2 * j + 1]);
-        store8(out + (long long)(i / per) * a.o_head + p0 * 2, y);
+        for (int j = 0; j < 4; ++j) turn(c[j], v[u][2 * j], v[u][2 * j + 1], y[2 * j], y[2 * j + 1]);
+        store8(out + t[u] * a.o_tok + h[u] * a.o_head + p0[u] * 2, y);
       }
     }
   } else {
     table();
     for (int i = threadIdx.x; i < n; i += kRopeThreads) {
-      const int p = i % per;
-      const T* s = x + (long long)(i / per) * a.x_head + 2 * p;
-      T* d = out + (long long)(i / per) * a.o_head + 2 * p;
+      const int p = i % per, h = i / per % nh, t = i / per / nh;
+      const T* s = x + t * a.x_tok + h * a.x_head + 2 * p;
+      T* d = out + t * a.o_tok + h * a.o_head + 2 * p;
       float y0, y1;
-      turn(cs[p], to_f(s[0]), to_f(s[1]), y0, y1);
+      turn(cs[t * ax.half + p], to_f(s[0]), to_f(s[1]), y0, y1);
       d[0] = from_f<T>(y0);
       d[1] = from_f<T>(y1);
     }
@@ -367,14 +375,21 @@ extern "C" mla_status_t mla_rope_axes(const mla_dims_t* dims, int32_t n_tok, int
                    x_tok_stride % 8 == 0 && x_head_stride % 8 == 0 && out_tok_stride % 8 == 0 &&
                    out_head_stride % 8 == 0;
   const int per = vec ? ax.half / 4 : ax.half;
-  // one batch of loads a thread; for few tokens one load a thread, so that the
-  // heads of a token spread over several SMs
-  const int items = kRopeThreads * (n_tok >= 1024 ? kRopeUnroll : 1);
-  int hpb = items / per > 0 ? items / per : 1;
+  // One batch of loads a thread: as many tokens as fill it, heads split when
+  // one token holds more.  Few tokens: one load a thread, so that the heads
+  // of a token spread over several SMs.
+  const int items = kRopeThreads * (n_tok >= 512 ? kRopeUnroll : 1);
+  int hpb = items / per > 0 ? items / per : 1, tpb = 1;
   if (hpb > n_heads) hpb = n_heads;
   if ((n_heads + hpb - 1) / hpb > 65535) hpb = (n_heads + 65534) / 65535;
+  if (hpb == n_heads && n_tok >= 512) {
+    tpb = items / (per * n_heads);
+    if (tpb < 1) tpb = 1;
+    if (tpb > kRopeTokens) tpb = kRopeTokens;
+  }
   a.heads_per_block = hpb;
-  const dim3 grid(n_tok, (n_heads + hpb - 1) / hpb);
+  a.tok_per_block = tpb;
+  const dim3 grid((n_tok + tpb - 1) / tpb, (n_heads + hpb - 1) / hpb);
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   if (dims->dtype == MLA_BF16) {
     if (vec) rope_axes_kernel<__nv_bfloat16, true><<<grid, kRopeThreads, 0, st>>>(a, ax);

@@ -277,48 +277,85 @@ ACTIVATIONS = {"none": 0, "silu": 1, "gelu": 2}
 _TORCH_DTYPE = {MLA_F32: torch.float32, MLA_BF16: torch.bfloat16}
 
 
+_arrays: dict = {}
+
+
 def _ints(values: Sequence[int]):
-    return (_i32 * len(values))(*[int(v) for v in values])
+    """A host int32 array of the values (kept: the same few lists come with every call)."""
+    key = tuple(values)
+    arr = _arrays.get(key)
+    if arr is None:
+        if len(_arrays) > 256:
+            _arrays.clear()
+        arr = _arrays[key] = (_i32 * len(key))(*[int(v) for v in key])
+    return arr
 
 
 def _bytes(t: Optional[torch.Tensor]) -> int:
     return 0 if t is None else t.numel() * t.element_size()
 
 
-def _want(t: Optional[torch.Tensor], name: str, dtype, shape=None):
-    """Raises unless t (None passes) has the dtype and the sizes of ``shape`` (None: any)."""
+def _at(t, name: str, dtype, shape: tuple, dev: int) -> Optional[int]:
+    """Address of a contiguous tensor of this dtype, shape and device (None: null); raises otherwise."""
     if t is None:
-        return
-    if t.dtype != dtype:
-        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if shape is not None and (t.dim() != len(shape) or
-                              any(w is not None and w != n for w, n in zip(shape, t.shape))):
-        raise ValueError(f"{name} must have sizes {tuple(shape)}, got {tuple(t.shape)}")
+        return None
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != dev or not t.is_contiguous():
+        _refuse(t, name, dtype, shape, dev)
+    return t.data_ptr()
 
 
-def _rows(t: Optional[torch.Tensor], name: str) -> int:
-    """Stride between the rows of a matrix whose last axis is contiguous."""
+def _view(t, name: str, dtype, shape: tuple, dev: int) -> Optional[tuple]:
+    """Strides of a view of this dtype, shape and device whose last axis is contiguous."""
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != dev:
+        _refuse(t, name, dtype, shape, dev)
+    strides = t.stride()
+    if strides[-1] != 1 and shape[-1] > 1:
+        raise ValueError(f"{name}: the last axis must be contiguous")
+    return strides
+
+
+def _pitch(t, name: str, dtype, shape: tuple, dev: int) -> int:
+    """Elements between the rows of a matrix of this dtype, shape and device (0 for None)."""
     if t is None:
         return 0
-    if t.shape[1] > 1 and t.stride(1) != 1:
-        raise ValueError(f"{name}: the last axis must be contiguous")
-    return max(t.stride(0), t.shape[1]) if t.shape[0] <= 1 else t.stride(0)
+    pitch = _view(t, name, dtype, shape, dev)[0]
+    return pitch if shape[0] > 1 else max(pitch, shape[1])
+
+
+def _refuse(t, name, dtype, shape, dev):
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be on the current CUDA device (cuda:{dev}), got {t.device}")
+    if t.dtype is not dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have sizes {tuple(shape)}, got {tuple(t.shape)}")
+    raise ValueError(f"{name} must be contiguous")
+
+
+def _call(name: str, dev: int, stream, *args):
+    """The C call on ``stream``, or on the current stream of the current device."""
+    s = _raw_stream(dev) if stream is None else _s(stream)
+    code = getattr(lib(), name)(*args, s)
+    if code:
+        raise MLAError(name, code)
+
+
+def _raw_stream(dev: int) -> int:
+    return torch._C._cuda_getCurrentRawStream(dev)
 
 
 def rope_axes(dims: Dims, x, pos, sections: Sequence[int], out, inverse: bool = False, stream=None):
     """mla_rope_axes: x, out [n_tok, n_heads, d_r] views (any token and head strides), pos
     [len(sections), n_tok] int32; ``out`` may be ``x``."""
-    n_tok, n_heads, d_r = x.shape
+    dev = torch.cuda.current_device()
+    n_tok, n_heads, _ = shape = x.shape
     dt = _TORCH_DTYPE.get(dims.dtype)
-    _want(x, "x", dt, (None, None, dims.d_r))
-    _want(out, "out", dt, (n_tok, n_heads, d_r))
-    _want(pos, "pos", torch.int32, (len(sections), n_tok))
-    if x.stride(2) != 1 or out.stride(2) != 1:
-        raise ValueError("the last axis of x and out must be contiguous")
-    _check("mla_rope_axes", lib().mla_rope_axes(
-        ctypes.byref(dims), n_tok, n_heads, x.data_ptr(), x.stride(0), x.stride(1), _p(pos),
-        len(sections), _ints(sections), int(inverse), out.data_ptr(), out.stride(0), out.stride(1),
-        _s(stream)))
+    xs = _view(x, "x", dt, (n_tok, n_heads, dims.d_r), dev)
+    os_ = _view(out, "out", dt, shape, dev)
+    n_axes = len(sections)
+    _call("mla_rope_axes", dev, stream, ctypes.byref(dims), n_tok, n_heads, x.data_ptr(), xs[0],
+          xs[1], _at(pos, "pos", torch.int32, (n_axes, n_tok), dev), n_axes, _ints(sections),
+          int(inverse), out.data_ptr(), os_[0], os_[1])
 
 
 def append_tokens(dims: Dims, kv, tok_start, row0, pos, sections: Sequence[int], cache, block_table,
@@ -326,25 +363,22 @@ def append_tokens(dims: Dims, kv, tok_start, row0, pos, sections: Sequence[int],
                   scale_c=None, scale_r=None, stream=None):
     """mla_append_tokens: kv [n_tok, d_c + d_r] rows (any row stride) into the pages of sequences
     tok_start describes; ``bits`` (bits_c, bits_r) for a packed pool, else rows of the dtype."""
-    n_tok, B = kv.shape[0], row0.shape[0]
-    _want(kv, "kv", _TORCH_DTYPE.get(dims.dtype), (None, dims.d_c + dims.d_r))
-    _want(tok_start, "tok_start", torch.int32, (B + 1,))
-    _want(row0, "row0", torch.int32, (B,))
-    _want(pos, "pos", torch.int32, (len(sections), n_tok))
-    _want(block_table, "block_table", torch.int32, (B, None))
-    _want(norm_weight, "norm_weight", torch.float32, (dims.d_c,))
-    _want(scale_c, "scale_c", torch.float32, (dims.d_c,))
-    _want(scale_r, "scale_r", torch.float32, (dims.d_r,))
+    dev = torch.cuda.current_device()
+    n_tok, B, i32, f32 = kv.shape[0], row0.shape[0], torch.int32, torch.float32
+    d_c, d_r, dt = dims.d_c, dims.d_r, _TORCH_DTYPE.get(dims.dtype)
+    n_pages, max_pages, n_axes = cache.shape[0], block_table.shape[1], len(sections)
     bits_c, bits_r = bits if bits else (0, 0)
     if bits:
-        _want(cache, "cache", torch.uint8, (None, 64, (dims.d_c * bits_c + dims.d_r * bits_r) // 8))
+        pool = _at(cache, "cache", torch.uint8, (n_pages, 64, (d_c * bits_c + d_r * bits_r) // 8), dev)
     else:
-        _want(cache, "cache", _TORCH_DTYPE.get(dims.dtype), (None, 64, dims.d_c + dims.d_r))
-    _check("mla_append_tokens", lib().mla_append_tokens(
-        ctypes.byref(dims), B, n_tok, kv.data_ptr(), _rows(kv, "kv"), _p(tok_start), _p(row0),
-        _p(pos), len(sections), _ints(sections), _p(norm_weight), norm_eps, bits_c, bits_r,
-        _p(scale_c), _p(scale_r), _p(cache), cache.shape[0], _p(block_table), block_table.shape[1],
-        _s(stream)))
+        pool = _at(cache, "cache", dt, (n_pages, 64, d_c + d_r), dev)
+    _call("mla_append_tokens", dev, stream, ctypes.byref(dims), B, n_tok, kv.data_ptr(),
+          _pitch(kv, "kv", dt, (n_tok, d_c + d_r), dev),
+          _at(tok_start, "tok_start", i32, (B + 1,), dev), _at(row0, "row0", i32, (B,), dev),
+          _at(pos, "pos", i32, (n_axes, n_tok), dev), n_axes, _ints(sections),
+          _at(norm_weight, "norm_weight", f32, (d_c,), dev), norm_eps, bits_c, bits_r,
+          _at(scale_c, "scale_c", f32, (d_c,), dev), _at(scale_r, "scale_r", f32, (d_r,), dev), pool,
+          n_pages, _at(block_table, "block_table", i32, (B, max_pages), dev), max_pages)
 
 
 def chunk_workspace_size(dims: Dims, B: int, n_tok: int, n_ver: int, max_pages: int, max_segs: int,
@@ -357,23 +391,21 @@ def chunk_attn(dims: Dims, q, tok_start, q_pos, w_uk, w_uv, cache, block_table, 
                deltas: Sequence[int], max_rows: int, v, workspace, lse=None, stream=None):
     """mla_chunk_attn: q [n_tok, H, d_n + d_r] (rotary part rotated) over the cached rows of the
     sequences tok_start describes -> v [n_tok, H, d_v]; lse [n_tok, H] or None."""
-    n_tok, B = q.shape[0], tok_start.shape[0] - 1
-    dt = _TORCH_DTYPE.get(dims.dtype)
-    _want(q, "q", dt, (None, dims.H, dims.d_n + dims.d_r))
-    _want(tok_start, "tok_start", torch.int32, (B + 1,))
-    _want(q_pos, "q_pos", torch.int32, (n_tok,))
-    _want(w_uk, "w_uk", dt, (dims.H, dims.d_n, dims.d_c))
-    _want(w_uv, "w_uv", dt, (dims.H, dims.d_v, dims.d_c))
-    _want(cache, "cache", dt, (None, 64, dims.d_c + dims.d_r))
-    _want(block_table, "block_table", torch.int32, (B, None))
-    _want(segs, "segs", torch.int32, (B, None, 4))
-    _want(v, "v", dt, (n_tok, dims.H, dims.d_v))
-    _want(lse, "lse", torch.float32, (n_tok, dims.H))
-    _check("mla_chunk_attn", lib().mla_chunk_attn(
-        ctypes.byref(dims), B, n_tok, _p(q), _p(tok_start), _p(q_pos), _p(w_uk), _p(w_uv), _p(cache),
-        cache.shape[0], _p(block_table), block_table.shape[1], _p(segs), segs.shape[1],
-        _ints(deltas), len(deltas), max_rows, _p(v), _p(lse), _p(workspace), _bytes(workspace),
-        _s(stream)))
+    dev = torch.cuda.current_device()
+    n_tok, B, i32, H = q.shape[0], tok_start.shape[0] - 1, torch.int32, dims.H
+    d_c, d_r, d_n, d_v, dt = dims.d_c, dims.d_r, dims.d_n, dims.d_v, _TORCH_DTYPE.get(dims.dtype)
+    n_pages, max_pages, max_segs = cache.shape[0], block_table.shape[1], segs.shape[1]
+    if workspace is not None and workspace.get_device() != dev:
+        raise ValueError("workspace must be on the current CUDA device")
+    _call("mla_chunk_attn", dev, stream, ctypes.byref(dims), B, n_tok,
+          _at(q, "q", dt, (n_tok, H, d_n + d_r), dev),
+          _at(tok_start, "tok_start", i32, (B + 1,), dev), _at(q_pos, "q_pos", i32, (n_tok,), dev),
+          _at(w_uk, "w_uk", dt, (H, d_n, d_c), dev), _at(w_uv, "w_uv", dt, (H, d_v, d_c), dev),
+          _at(cache, "cache", dt, (n_pages, 64, d_c + d_r), dev), n_pages,
+          _at(block_table, "block_table", i32, (B, max_pages), dev), max_pages,
+          _at(segs, "segs", i32, (B, max_segs, 4), dev), max_segs, _ints(deltas), len(deltas),
+          max_rows, _at(v, "v", dt, (n_tok, H, d_v), dev),
+          _at(lse, "lse", torch.float32, (n_tok, H), dev), _p(workspace), _bytes(workspace))
 
 
 def linear_workspace_size(x, w) -> int:
@@ -385,19 +417,20 @@ def linear_workspace_size(x, w) -> int:
 def linear(x, w, out, bias=None, act: str = "none", residual=None, workspace=None, stream=None):
     """mla_linear: out [M, N] = act(x [M, K] w [N, K]^T + bias [N]) + residual [M, N]; matrices may
     have any row stride; ``out`` may be ``residual``."""
-    if x.dtype not in (torch.float32, torch.bfloat16):
-        raise ValueError(f"x must be float32 or bfloat16, got {x.dtype}")
+    dev = torch.cuda.current_device()
+    dt = x.dtype
+    if dt is not torch.bfloat16 and dt is not torch.float32:
+        raise ValueError(f"x must be float32 or bfloat16, got {dt}")
     if x.dim() != 2 or w.dim() != 2:
         raise ValueError("x and w must be matrices")
-    (M, K), N = x.shape, w.shape[0]
-    _want(w, "w", x.dtype, (N, K))
-    _want(out, "out", x.dtype, (M, N))
-    _want(bias, "bias", torch.float32, (N,))
-    _want(residual, "residual", x.dtype, (M, N))
     if act not in ACTIVATIONS:
         raise ValueError(f"act must be one of {sorted(ACTIVATIONS)}")
-    _check("mla_linear", lib().mla_linear(
-        MLA_BF16 if x.dtype == torch.bfloat16 else MLA_F32, M, N, K, x.data_ptr(), _rows(x, "x"),
-        w.data_ptr(), _rows(w, "w"), _p(bias), ACTIVATIONS[act],
-        None if residual is None else residual.data_ptr(), _rows(residual, "residual"),
-        out.data_ptr(), _rows(out, "out"), _p(workspace), _bytes(workspace), _s(stream)))
+    if workspace is not None and workspace.get_device() != dev:
+        raise ValueError("workspace must be on the current CUDA device")
+    (M, K), N = x.shape, w.shape[0]
+    _call("mla_linear", dev, stream, MLA_BF16 if dt is torch.bfloat16 else MLA_F32, M, N, K,
+          x.data_ptr(), _pitch(x, "x", dt, (M, K), dev), w.data_ptr(),
+          _pitch(w, "w", dt, (N, K), dev), _at(bias, "bias", torch.float32, (N,), dev),
+          ACTIVATIONS[act], None if residual is None else residual.data_ptr(),
+          _pitch(residual, "residual", dt, (M, N), dev), out.data_ptr(),
+          _pitch(out, "out", dt, (M, N), dev), _p(workspace), _bytes(workspace))

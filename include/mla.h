@@ -459,7 +459,7 @@ mla_status_t mla_decode_qknorm(const mla_dims_t* dims, int32_t B, int32_t s_q,
  *   pos        [n_axes, n_tok] int32 positions (any value, also negative)
  *   sections   [n_axes] HOST, each >= 0, sum d_r / 2; 1 <= n_axes <= 4
  * Reads d_r, rope_base and dtype of dims.  Errors: INVALID_ARG; UNSUPPORTED
- * (n_axes > 4, d_r > 256). */
+ * (n_axes > 4, d_r > 128). */
 mla_status_t mla_rope_axes(const mla_dims_t* dims, int32_t n_tok, int32_t n_heads, const void* x,
                            int64_t x_tok_stride, int64_t x_head_stride, const int32_t* pos,
                            int32_t n_axes, const int32_t* sections, int32_t inverse, void* out,
@@ -486,7 +486,7 @@ mla_status_t mla_rope_axes(const mla_dims_t* dims, int32_t n_tok, int32_t n_head
  * A token whose row or page id is out of range, or whose tok_start
  * is out of order, is skipped and records BAD_INDEX.  Errors: INVALID_ARG;
  * UNSUPPORTED (page_size != 64, other bit pairs or widths, n_axes > 4,
- * d_r > 256). */
+ * d_r > 128). */
 mla_status_t mla_append_tokens(const mla_dims_t* dims, int32_t B, int32_t n_tok, const void* kv,
                                int64_t kv_stride, const int32_t* tok_start, const int32_t* row0,
                                const int32_t* pos, int32_t n_axes, const int32_t* sections,
