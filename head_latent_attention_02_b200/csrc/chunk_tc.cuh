@@ -9,24 +9,28 @@
 // the absorbed form, so it is the cheaper one as soon as the expansion
 // (2 * 512 * 256 flops per row and head) is shared by enough queries.
 //
-// Decomposition.  A CTA takes 256 consecutive tokens of one sequence and one
-// head, as two query tiles of 128 rows, and walks the sequence's rows in tiles
-// of 128 (two pages of the list).  S and O of both query tiles fill the 512
-// tensor-memory columns; P (bf16) overwrites its S.  The tensor core works on
-// one query tile while the other one's softmax runs:
+// Decomposition.  A cluster of two CTAs takes 512 consecutive tokens of one
+// sequence and one head, as two query tiles of 256 rows (128 in each CTA), and
+// walks the sequence's rows in tiles of 128 (two pages of the list).  The MMAs
+// act on the pair (cta_group::2): each CTA holds half of a tile's keys (64
+// rows) and half of its values (64 columns) in shared memory and the tensor
+// cores read both halves, so a CTA loads 40 KB a tile instead of 80 KB.  With one
+// CTA per 256 tokens the ring held a tile and a half and its loads, 1.5 us
+// from issue to landing, stalled the products.  S and O of both query tiles
+// fill the 512 tensor-memory columns; P (bf16) overwrites its S.  The
+// tensor core works on one query tile while the other one's softmax runs:
 //     ... P0 V | S0 | P1 V | S1 | P0 V | S0 ...
 // At 192 + 128 columns a tile costs the tensor core 1280 clocks and its
-// exponentials the special-function units 1024, so the products bound the
-// loop as long as a tile's softmax finishes within the other tile's products.
+// exponentials the special-function units 1024.
 //
-// Roles (320 threads): warp 0 loads by TMA, warp 1 issues the MMAs, warps 2-5
-// and 6-9 run the softmax of query tiles 0 and 1 (a thread per query row, so
-// that row statistics need no exchange between threads).  The running maximum
-// is only raised when it grew by more than 2^8 (the weights then stay below
-// 2^8, harmless in fp32 sums and in bf16, whose precision is relative); O is
-// rescaled by the softmax threads in that rare case.  S of step j is issued
-// after P V of step j - 1 and its barrier covers both, so O is at rest while
-// a softmax thread holds S.
+// Roles (320 threads a CTA): warp 0 loads by TMA, warp 1 of the first CTA
+// issues the MMAs, warps 2-5 and 6-9 run the softmax of query tiles 0 and 1 (a
+// thread per query row, so that row statistics need no exchange between
+// threads).  The running maximum is only raised when it grew by more than
+// 2^8 (the weights then stay below 2^8, harmless in fp32 sums and in bf16,
+// whose precision is relative); O is rescaled by the softmax threads in that
+// rare case.  S of step j is issued after P V of step j - 1 and its barrier
+// covers both, so O is at rest while a softmax thread holds S.
 //
 // Every wait is bounded and records MLA_ERR_TIMEOUT when it gives up.
 #pragma once
@@ -41,14 +45,17 @@ namespace ck {
 
 constexpr int kDn = 128, kDr = 64, kDv = 128, kDc = 512;
 constexpr int kQTile = 128, kKTile = 128;
-constexpr int kItemTokens = 2 * kQTile;
+constexpr int kPairTile = 2 * kQTile;        // rows of a query tile, both CTAs
+constexpr int kItemTokens = 2 * kPairTile;
 constexpr int kPanel = 128 * 128;            // 128 rows x 64 bf16: 16 KB
 constexpr int kQBytes = 3 * kPanel;          // a query tile: two nope panels, one rope panel
-constexpr int kSlot = 2 * kPanel;            // a tile's keys (without the rotary part) or its values
-constexpr int kSlots = 3, kRotSlots = 2;
-constexpr int kOffRing = 2 * kQBytes;
-constexpr int kOffRot = kOffRing + kSlots * kSlot;
-constexpr int kOffBar = kOffRot + kRotSlots * kPanel;
+// a CTA's half of a tile's keys and of its values
+constexpr int kKeySlot = kPanel + kPanel / 2;   // 64 rows x two panels and the rotary panel
+constexpr int kValSlot = kPanel;                // 128 rows x one panel
+constexpr int kKeySlots = 3, kValSlots = 3;     // 120 KB: three tiles
+constexpr int kOffKeys = 2 * kQBytes;
+constexpr int kOffVals = kOffKeys + kKeySlots * kKeySlot;
+constexpr int kOffBar = kOffVals + kValSlots * kValSlot;
 constexpr int kSmemBytes = kOffBar + 512 + 1024;
 constexpr int kThreads = 320;
 constexpr int kTmemCols = 512;
@@ -59,7 +66,7 @@ static_assert(kSmemBytes <= 232448, "shared memory budget");
 
 struct Item {
   int b;         // sequence; its rows start at page entry `entry`
-  int tok0, n;   // tokens [tok0, tok0 + n), n <= 256
+  int tok0, n;   // tokens [tok0, tok0 + n), n <= 512
   int entry;     // first page entry of the sequence (even)
   int tiles;     // 128-row tiles of the sequence; -1: the sequence is invalid
 };
@@ -84,32 +91,24 @@ struct Params {
 
 // Tensor maps (64 columns, 128-byte swizzle):
 //   q   (column, token, panel) over q [n_tok, H x 192], box {64, 128, 3}
-//   k,v (column, row, panel) over the scratch [heads x rows_cap, 128], box
-//       {64, 128, 2}: two 64-column panels of 16 KB
-//   kr  (column, row) over the rotary scratch [rows_cap, 64], box {64, 128}
+//   k,v (column, row, panel) over the scratch [heads x rows_cap, 128], boxes
+//       {64, 64, 2} and {64, 128, 1}
+//   kr  (column, row) over the rotary scratch [rows_cap, 64], box {64, 64}
 struct Maps {
   CUtensorMap q, k, v, kr;
 };
 
 struct Bars {
   uint64_t q_full[2];
-  uint64_t full[kSlots], empty[kSlots];        // keys of tile 0, values of tile 0, keys of tile 1, ...
-  uint64_t rot_full[kRotSlots], rot_empty[kRotSlots];
-  uint64_t s_full[2], p_full[2], o_full[2];
+  uint64_t k_full[kKeySlots], k_empty[kKeySlots], v_full[kValSlots], v_empty[kValSlots];
+  uint64_t s_full[2], o_full[2];
+  uint64_t p_full[2][2];                       // query tile, half of the weights' columns
   uint32_t tmem_base;
   int n_tiles[2];
   int q_max[2], q_min[2];
   int n_full[2];               // leading tiles that every query of the tile sees whole
 };
 static_assert(sizeof(Bars) <= 512, "barrier block too large");
-
-// max that keeps NaN (fmaxf drops it): a NaN score makes the row's maximum, and
-// with it the whole row, NaN.
-__device__ __forceinline__ float max_nan(float a, float b) {
-  float y;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
-  return y;
-}
 
 // Visible rows of one page: those with data whose position is not past qp.
 __device__ __forceinline__ int visible(const gm::PageEntry& e, int qp) {
@@ -118,7 +117,7 @@ __device__ __forceinline__ int visible(const gm::PageEntry& e, int qp) {
   return d < e.n ? (int)d : e.n;
 }
 
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 chunk_attn_kernel(const __grid_constant__ Params p, const __grid_constant__ Maps mp) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
@@ -128,16 +127,18 @@ chunk_attn_kernel(const __grid_constant__ Params p, const __grid_constant__ Maps
 
   // the item list and the expanded rows are complete after this wait
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  if ((int)blockIdx.x >= p.plan->n_items) return;
-  const Item it = p.items[blockIdx.x];
+  const int item = blockIdx.x >> 1;
+  const int rank = (int)cluster_ctarank();
+  if (item >= p.plan->n_items) return;       // both CTAs of the pair
+  const Item it = p.items[item];
   const int hl = blockIdx.y, h = p.h0 + hl;
 
   if (it.tiles < 0) {      // invalid sequence: NaN
-    for (int i = threadIdx.x; i < it.n * kDv; i += kThreads)
+    for (int i = rank * kThreads + threadIdx.x; i < it.n * kDv; i += 2 * kThreads)
       p.v[((long long)(it.tok0 + i / kDv) * p.H + h) * kDv + i % kDv] =
           __float2bfloat16_rn(__int_as_float(0x7fc00000));
     if (p.lse)
-      for (int i = threadIdx.x; i < it.n; i += kThreads)
+      for (int i = rank * kThreads + threadIdx.x; i < it.n; i += 2 * kThreads)
         p.lse[(long long)(it.tok0 + i) * p.H + h] = __int_as_float(0x7fc00000);
     return;
   }
@@ -146,38 +147,39 @@ chunk_attn_kernel(const __grid_constant__ Params p, const __grid_constant__ Maps
     for (int t = 0; t < 2; ++t) {
       mbar_init(&bar->q_full[t], 1);
       mbar_init(&bar->s_full[t], 1);
-      mbar_init(&bar->p_full[t], 4);
+      mbar_init(&bar->p_full[t][0], 8);    // four softmax warps of each CTA
+      mbar_init(&bar->p_full[t][1], 8);
       mbar_init(&bar->o_full[t], 1);
       bar->n_tiles[t] = 0;
       bar->q_max[t] = INT32_MIN;
       bar->q_min[t] = INT32_MAX;
       bar->n_full[t] = INT32_MAX;
     }
-    for (int i = 0; i < kSlots; ++i) {
-      mbar_init(&bar->full[i], 1);
-      mbar_init(&bar->empty[i], 1);
+    for (int i = 0; i < kKeySlots; ++i) {
+      mbar_init(&bar->k_full[i], 1);
+      mbar_init(&bar->k_empty[i], 1);
     }
-    for (int i = 0; i < kRotSlots; ++i) {
-      mbar_init(&bar->rot_full[i], 1);
-      mbar_init(&bar->rot_empty[i], 1);
+    for (int i = 0; i < kValSlots; ++i) {
+      mbar_init(&bar->v_full[i], 1);
+      mbar_init(&bar->v_empty[i], 1);
     }
     fence_mbar_init();
   }
-  if (warp == 1) tmem_alloc(&bar->tmem_base, kTmemCols);
+  if (warp == 1) tmem_alloc_pair(&bar->tmem_base, kTmemCols);
   __syncthreads();
   // the tiles that each query tile needs (up to the last one that any of its
   // queries sees) and the leading ones that need no mask
-  if (threadIdx.x < it.n) {
-    const int qp = p.q_pos[it.tok0 + threadIdx.x];
-    atomicMax(&bar->q_max[threadIdx.x >> 7], qp);
-    atomicMin(&bar->q_min[threadIdx.x >> 7], qp);
+  for (int i = threadIdx.x; i < it.n; i += kThreads) {
+    const int qp = p.q_pos[it.tok0 + i];
+    atomicMax(&bar->q_max[i / kPairTile], qp);
+    atomicMin(&bar->q_min[i / kPairTile], qp);
   }
   __syncthreads();
   for (int j = threadIdx.x; j < it.tiles; j += kThreads) {
     const gm::PageEntry e0 = p.pages[it.entry + 2 * j], e1 = p.pages[it.entry + 2 * j + 1];
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
-      if (t * kQTile >= it.n) continue;
+      if (t * kPairTile >= it.n) continue;
       if (visible(e0, bar->q_max[t]) > 0 || visible(e1, bar->q_max[t]) > 0)
         atomicMax(&bar->n_tiles[t], j + 1);
       if (visible(e0, bar->q_min[t]) < kPage || visible(e1, bar->q_min[t]) < kPage)
@@ -186,6 +188,7 @@ chunk_attn_kernel(const __grid_constant__ Params p, const __grid_constant__ Maps
   }
   tc_fence_before();
   __syncthreads();
+  cluster_sync();       // the peer's barriers are ready
   tc_fence_after();
   const uint32_t tmem = bar->tmem_base;
   const int nt0 = bar->n_tiles[0], nt1 = bar->n_tiles[1];
@@ -199,9 +202,14 @@ chunk_attn_kernel(const __grid_constant__ Params p, const __grid_constant__ Maps
       prefetch_tmap(&mp.v);
       prefetch_tmap(&mp.kr);
       const int krow = (int)(hl * p.rows_cap) + it.entry * kPage;
+      // the pair's bytes are counted on the first CTA's barriers
+      auto expect = [&](uint64_t* b, int bytes) {
+        if (rank == 0) mbar_arrive_expect_tx(b, 2 * bytes);
+        return mapa(smem_u32(b), 0);
+      };
       auto load_q = [&](int t) {
-        mbar_arrive_expect_tx(&bar->q_full[t], kQBytes);
-        tma_load_3d(smem + t * kQBytes, &mp.q, &bar->q_full[t], 0, it.tok0 + t * kQTile, 3 * h);
+        const uint32_t b = expect(&bar->q_full[t], kQBytes);
+        tma_load_3d_pair(smem + t * kQBytes, &mp.q, b, 0, it.tok0 + t * kPairTile + rank * kQTile, 3 * h);
       };
       bool ok = true;
       auto wait = [&](uint64_t* b, int use) {      // the slot's use-th filling may start
@@ -211,93 +219,84 @@ chunk_attn_kernel(const __grid_constant__ Params p, const __grid_constant__ Maps
         }
         return ok;
       };
-      auto load = [&](const CUtensorMap* map, int n, int row) {
-        const int slot = n % kSlots;
-        if (!wait(&bar->empty[slot], n / kSlots)) return;
-        mbar_arrive_expect_tx(&bar->full[slot], kSlot);
-        tma_load_3d(smem + kOffRing + slot * kSlot, map, &bar->full[slot], 0, row, 0);
-      };
       if (nt0 > 0) load_q(0);
       for (int j = 0; ok && j < nt; ++j) {
-        load(&mp.k, 2 * j, krow + j * kKTile);
-        const int rs = j % kRotSlots;
-        if (!ok || !wait(&bar->rot_empty[rs], j / kRotSlots)) break;
-        mbar_arrive_expect_tx(&bar->rot_full[rs], kPanel);
-        tma_load_2d(smem + kOffRot + rs * kPanel, &mp.kr, &bar->rot_full[rs], 0,
-                    it.entry * kPage + j * kKTile);
+        const int ks = j % kKeySlots, vs = j % kValSlots;
+        if (!wait(&bar->k_empty[ks], j / kKeySlots)) break;
+        uint8_t* key = smem + kOffKeys + ks * kKeySlot;
+        uint32_t b = expect(&bar->k_full[ks], kKeySlot);
+        tma_load_3d_pair(key, &mp.k, b, 0, krow + j * kKTile + rank * 64, 0);
+        tma_load_2d_pair(key + kPanel, &mp.kr, b, 0, it.entry * kPage + j * kKTile + rank * 64);
         if (j == 0 && nt1 > 0) load_q(1);
-        load(&mp.v, 2 * j + 1, krow + j * kKTile);
+        if (!wait(&bar->v_empty[vs], j / kValSlots)) break;
+        b = expect(&bar->v_full[vs], kValSlot);
+        tma_load_3d_pair(smem + kOffVals + vs * kValSlot, &mp.v, b, 0, krow + j * kKTile, rank);
       }
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA
-    if (lane == 0 && nt > 0) {
-      constexpr uint32_t idesc_s = idesc_bf16_f32(kQTile, kKTile, false, false);
-      constexpr uint32_t idesc_o = idesc_bf16_f32(kQTile, kDv, false, true);
+    if (rank == 0 && nt > 0) {        // the whole warp, converged
+      constexpr uint32_t idesc_s = idesc_bf16_f32(kPairTile, kKTile, false, false);
+      constexpr uint32_t idesc_o = idesc_bf16_f32(kPairTile, kDv, false, true);
       // Descriptors of the first panels; a panel, a slot or a K step further is
       // an addition (16-byte units) that never leaves the address field.  The
-      // issuing thread shares its scheduler with softmax warps: building each
+      // issuing warp shares its scheduler with softmax warps: building each
       // descriptor anew cost it 1400 clocks for the eight MMAs of a P V.
       const uint64_t dq = smem_desc_sw128(smem_u32(smem), 16, 1024);
-      const uint64_t dk = smem_desc_sw128(smem_u32(smem + kOffRing), 16, 1024);
-      const uint64_t dr = smem_desc_sw128(smem_u32(smem + kOffRot), 16, 1024);
-      // values: 16 rows of both 64-column panels per step, rows outermost
-      const uint64_t dv = smem_desc_sw128(smem_u32(smem + kOffRing), kPanel, 1024);
+      const uint64_t dk = smem_desc_sw128(smem_u32(smem + kOffKeys), 16, 1024);
+      // values: 16 rows of the CTA's 64-column panel per step, rows outermost
+      const uint64_t dv = smem_desc_sw128(smem_u32(smem + kOffVals), kPanel, 1024);
       bool ok = true;
       auto wait = [&](uint64_t* b, uint32_t parity) {
-        if (ok && !mbar_wait(b, parity)) {
-          set_status(MLA_ERR_TIMEOUT);
+        if (ok && !__all_sync(0xffffffffu, mbar_wait(b, parity))) {
+          if (lane == 0) set_status(MLA_ERR_TIMEOUT);
           ok = false;
         }
       };
       for (int j = 0; ok && j <= nt; ++j) {
-        const int kn = 2 * j, vn = 2 * j - 1;      // their places in the stream of slots
-        const int ks_n = kn % kSlots, vs_n = vn < 0 ? 0 : vn % kSlots;   // and their slots
-        if (j > 0) wait(&bar->full[vs_n], (vn / kSlots) & 1);
+        // P V of step j - 1, then S of step j, for each query tile; what was
+        // loaded is waited for first, off the chain from weights to scores
+        const int ks_n = j % kKeySlots, vs_n = (j + kValSlots - 1) % kValSlots;
+        if (j < nt) wait(&bar->k_full[ks_n], (j / kKeySlots) & 1);
+        if (j > 0) wait(&bar->v_full[vs_n], ((j - 1) / kValSlots) & 1);
         if (!ok) break;
-        const uint64_t kd = dk + ks_n * (kSlot >> 4), vd = dv + vs_n * (kSlot >> 4);
-        const uint64_t rd = dr + (j % kRotSlots) * (kPanel >> 4);
+        const uint64_t kd = dk + ks_n * (kKeySlot >> 4), vd = dv + vs_n * (kValSlot >> 4);
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
           const int mine = t ? nt1 : nt0;
           const uint32_t s_col = tmem + kColS + t * kKTile, o_col = tmem + kColO + t * kDv;
           if (j > 0 && j - 1 < mine) {
-            wait(&bar->p_full[t], (j - 1) & 1);
-            tc_fence_after();
-            if (!ok) break;
 #pragma unroll
-            for (int ks = 0; ks < 8; ++ks)
-              mma_bf16_ts(o_col, s_col + 8 * ks, vd + ks * (2048 >> 4), idesc_o,
-                          (j > 1 || ks > 0) ? 1u : 0u);
-            if (j == mine) mma_commit(&bar->o_full[t]);
+            for (int half = 0; half < 2; ++half) {
+              wait(&bar->p_full[t][half], (j - 1) & 1);
+              tc_fence_after();
+              if (!ok) break;
+#pragma unroll
+              for (int ks = 4 * half; ks < 4 * half + 4; ++ks)
+                mma_pair_bf16_ts_elect(o_col, s_col + 8 * ks, vd + ks * (2048 >> 4), idesc_o,
+                                       (j > 1 || ks > 0) ? 1u : 0u);
+            }
+            if (!ok) break;
+            if (j == mine) mma_pair_commit_both_elect(&bar->o_full[t]);
           }
-          // both query tiles are done with the values: their slot takes the
-          // keys of the next step, whose load needs all the time it can get
-          if (t == 1 && j > 0) mma_commit(&bar->empty[vs_n]);
           if (j < mine) {
-            if (t == 0 || nt0 <= j) {      // the first query tile of the step
-              wait(&bar->full[ks_n], (kn / kSlots) & 1);
-              wait(&bar->rot_full[j % kRotSlots], (j / kRotSlots) & 1);
+            if (j == 0) {
+              wait(&bar->q_full[t], 0);
+              if (!ok) break;
             }
-            if (j == 0) wait(&bar->q_full[t], 0);
             tc_fence_after();
-            if (!ok) break;
             const uint64_t qd = dq + t * (kQBytes >> 4);
+            // query panels are 128 rows high, a CTA's key panels 64
 #pragma unroll
-            for (int ks = 0; ks < 8; ++ks) {
-              const uint32_t at = (ks >> 2) * (kPanel >> 4) + (ks & 3) * 2;
-              mma_bf16_ss(s_col, qd + at, kd + at, idesc_s, ks ? 1u : 0u);
-            }
-#pragma unroll
-            for (int ks = 0; ks < 4; ++ks)
-              mma_bf16_ss(s_col, qd + 2 * (kPanel >> 4) + ks * 2, rd + ks * 2, idesc_s, 1u);
-            mma_commit(&bar->s_full[t]);
+            for (int ks = 0; ks < 12; ++ks)
+              mma_pair_bf16_ss_elect(s_col, qd + (ks >> 2) * (kPanel >> 4) + (ks & 3) * 2,
+                                     kd + (ks >> 2) * (kPanel >> 5) + (ks & 3) * 2, idesc_s,
+                                     ks ? 1u : 0u);
+            mma_pair_commit_both_elect(&bar->s_full[t]);
           }
         }
-        if (j < nt) {
-          mma_commit(&bar->empty[ks_n]);
-          mma_commit(&bar->rot_empty[j % kRotSlots]);
-        }
+        if (j > 0) mma_pair_commit_both_elect(&bar->v_empty[vs_n]);
+        if (j < nt) mma_pair_commit_both_elect(&bar->k_empty[ks_n]);
       }
     }
   } else {
@@ -305,7 +304,7 @@ chunk_attn_kernel(const __grid_constant__ Params p, const __grid_constant__ Maps
     const int t = warp >= 6 ? 1 : 0;
     const int quad = warp & 3;
     const int row = quad * 32 + lane;                 // row of the query tile
-    const int tok = t * kQTile + row;                 // token of the item
+    const int tok = t * kPairTile + rank * kQTile + row;   // token of the item
     const int mine = t ? nt1 : nt0;
     const uint32_t lanes = (uint32_t)(quad * 32) << 16;
     const uint32_t s_col = tmem + kColS + t * kKTile + lanes;
@@ -341,12 +340,14 @@ chunk_attn_kernel(const __grid_constant__ Params p, const __grid_constant__ Maps
         float mx[4];
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-          mx[c] = max_nan(s[c][0], s[c][1]);
+          mx[c] = fmaxf(s[c][0], s[c][1]);
 #pragma unroll
-          for (int i = 2; i < 32; i += 2) mx[c] = max_nan(mx[c], max_nan(s[c][i], s[c][i + 1]));
+          for (int i = 2; i < 32; i += 2) mx[c] = fmaxf(mx[c], fmaxf(s[c][i], s[c][i + 1]));
         }
-        const float top = max_nan(max_nan(mx[0], mx[1]), max_nan(mx[2], mx[3]));
-        const bool raise = !(top * p.scale_log2 <= m * p.scale_log2 + kMargin);   // or NaN
+        // NaN scores are left out of the maximum; their weights are NaN, and so
+        // are the row's sum and its output
+        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+        const bool raise = !(top * p.scale_log2 <= m * p.scale_log2 + kMargin);
         if (__any_sync(0xffffffffu, raise)) {
           const float m_new = raise ? top : m;
           // nothing seen so far (m = -inf): sums and O are zero whatever the factor
@@ -365,26 +366,32 @@ chunk_attn_kernel(const __grid_constant__ Params p, const __grid_constant__ Maps
           }
         }
         const float off = m == kNegInf ? 0.f : -m * p.scale_log2;
-        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+        const uint64_t off2 = pack_f32x2(off, off), mul2 = pack_f32x2(p.scale_log2, p.scale_log2);
+        uint64_t sum[2] = {0ull, 0ull};
+        // the weights of 64 columns at a time, so that P V may start on the first
+        // half while the second one is computed
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
           float w[32];
 #pragma unroll
           for (int i = 0; i < 32; ++i) {
             const int c0 = 2 * c + i / 16, i0 = 2 * (i % 16);
-            const float x = fmaf(s[c0][i0], p.scale_log2, off);
-            const float y = fmaf(s[c0][i0 + 1], p.scale_log2, off);
-            const float a = ex2_approx(x), b = ex2_approx(y);
-            sum[i & 3] += a + b;
-            w[i] = __uint_as_float(gm::pack2(a, b));
+            float x, y;
+            unpack_f32x2(fma_f32x2(pack_f32x2(s[c0][i0], s[c0][i0 + 1]), mul2, off2), x, y);
+            x = ex2_approx(x);
+            y = ex2_approx(y);
+            sum[i & 1] = add_f32x2(sum[i & 1], pack_f32x2(x, y));
+            w[i] = __uint_as_float(gm::pack2(x, y));
           }
           tmem_st32(s_col + 32 * c, w);
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_pair(mapa(smem_u32(&bar->p_full[t][c]), 0));
         }
-        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-        tmem_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bar->p_full[t]);
+        float a0, a1;
+        unpack_f32x2(add_f32x2(sum[0], sum[1]), a0, a1);
+        l += a0 + a1;
       }
       if (ok && !__all_sync(0xffffffffu, mbar_wait(&bar->o_full[t], 0))) {
         if (lane == 0) set_status(MLA_ERR_TIMEOUT);
@@ -424,9 +431,10 @@ chunk_attn_kernel(const __grid_constant__ Params p, const __grid_constant__ Maps
 
   __syncwarp();
   __syncthreads();
+  cluster_sync();       // no CTA leaves while the pair's MMAs may read its shared memory
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(tmem, kTmemCols);
+    tmem_dealloc_pair(tmem, kTmemCols);
   }
 }
 

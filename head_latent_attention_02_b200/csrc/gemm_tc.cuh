@@ -228,7 +228,7 @@ gemm_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtensorMa
         }
         for (int k = s.k0; k < s.k1; ++k, ++n) {
           const int slot = n % S;
-          if (!mbar_wait_cluster(&bar->empty[slot], ((n / S) & 1) ^ 1)) {
+          if (!mbar_wait(&bar->empty[slot], ((n / S) & 1) ^ 1)) {
             set_status(MLA_ERR_TIMEOUT);
             ok = false;
             break;
@@ -256,36 +256,40 @@ gemm_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtensorMa
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA
-    if (rank == 0 && lane == 0) {
+    if (rank == 0) {        // the whole warp, converged
       const uint32_t idesc = idesc_bf16_f32(kPairRows, p.BN, false, false);
       bool ok = true;
       Seg s;
       for (int i = 0, n = 0; ok && segment(p, tiles, pair, pairs, i, &s); ++i) {
         const int ab = i & 1;
-        if (!mbar_wait_cluster(&bar->acc_empty[ab], ((i >> 1) & 1) ^ 1)) {
-          set_status(MLA_ERR_TIMEOUT);
+        if (!__all_sync(0xffffffffu, mbar_wait(&bar->acc_empty[ab], ((i >> 1) & 1) ^ 1))) {
+          if (lane == 0) set_status(MLA_ERR_TIMEOUT);
           break;
         }
         tc_fence_after();
         for (int k = s.k0; k < s.k1; ++k, ++n) {
           const int slot = n % S;
-          if (!mbar_wait_cluster(&bar->full[slot], (n / S) & 1)) {
-            set_status(MLA_ERR_TIMEOUT);
+          if (!__all_sync(0xffffffffu, mbar_wait(&bar->full[slot], (n / S) & 1))) {
+            if (lane == 0) set_status(MLA_ERR_TIMEOUT);
             ok = false;
             break;
           }
           tc_fence_after();
-          const uint32_t a0 = smem_u32(smem + slot * stage), b0 = a0 + a_bytes;
-          for (int pn = 0; pn < P; ++pn)
+          // descriptors of the stage; a panel or a K step further is an addition
+          // (16-byte units) that never leaves the address field
+          const uint32_t a0 = smem_u32(smem + slot * stage);
+          uint64_t ad = smem_desc_sw128(a0, 16, 1024), bd = smem_desc_sw128(a0 + a_bytes, 16, 1024);
+          for (int pn = 0; pn < P; ++pn) {
 #pragma unroll
             for (int ks = 0; ks < 4; ++ks)
-              mma_pair_bf16_ss(tmem + ab * kMaxBN,
-                               smem_desc_sw128(a0 + pn * kABytes + ks * 32, 16, 1024),
-                               smem_desc_sw128(b0 + pn * b_panel + ks * 32, 16, 1024), idesc,
-                               (k == s.k0 && (pn | ks) == 0) ? 0u : 1u);
-          mma_pair_commit_both(&bar->empty[slot]);
+              mma_pair_bf16_ss_elect(tmem + ab * kMaxBN, ad + 2 * ks, bd + 2 * ks, idesc,
+                                     (k == s.k0 && (pn | ks) == 0) ? 0u : 1u);
+            ad += kABytes >> 4;
+            bd += b_panel >> 4;
+          }
+          mma_pair_commit_both_elect(&bar->empty[slot]);
         }
-        if (ok) mma_pair_commit_both(&bar->acc_full[ab]);
+        if (ok) mma_pair_commit_both_elect(&bar->acc_full[ab]);
       }
     }
   } else {
@@ -305,7 +309,7 @@ gemm_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtensorMa
       } else {
         tile_at(p, s.tile, &mt, &nt);
       }
-      if (!__all_sync(0xffffffffu, mbar_wait_cluster(&bar->acc_full[ab], (i >> 1) & 1))) {
+      if (!__all_sync(0xffffffffu, mbar_wait(&bar->acc_full[ab], (i >> 1) & 1))) {
         if (lane == 0) set_status(MLA_ERR_TIMEOUT);
         break;
       }
@@ -391,7 +395,7 @@ gemm_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtensorMa
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive_cluster_addr(mapa(smem_u32(&bar->acc_empty[ab]), 0));
+      if (lane == 0) mbar_arrive_pair(mapa(smem_u32(&bar->acc_empty[ab]), 0));
     }
   }
 

@@ -128,7 +128,7 @@ __device__ __forceinline__ int last_at_most(const int* off, int n, int x) {
 
 // One CTA: validates the sequences, lists their pages (an even number each, so
 // that a 128-row tile belongs to one sequence; a multiple of four in all) and
-// their 256-token items.  seq: page offset [B + 1], item offset [B + 1], flag
+// their 512-token items.  seq: page offset [B + 1], item offset [B + 1], flag
 // [B].  A sequence that does not fit `cap` pages is invalid.
 __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(
     const __grid_constant__ ChunkArgs a, int cap, ck::Plan* plan, int* seq, ck::Item* items,
@@ -335,12 +335,12 @@ struct Layout {
 
 // Expanded when its estimated time is the lower one.  A row's expansion costs
 // 2 * 512 * 256 flops a head at about 1.1 PFLOP/s; a query, row and head
-// 2 * 320 flops at about 0.7 PFLOP/s expanded (in query tiles of 128, so a
+// 2 * 320 flops at about 0.7 PFLOP/s expanded (in query tiles of 256, so a
 // sequence's tokens round up) and 2 * 1088 at about 0.45 PFLOP/s absorbed.
 bool chunk_route(const mla_dims_t* d, int B, int n_tok, long long max_rows) {
   if (!expandable(d)) return false;
   const double rows = (double)max_rows, per = std::ceil((double)n_tok / B);
-  const double e = rows * 262144.0 / 1.1e15 + rows * std::ceil(per / 128) * 128 * 640.0 / 0.7e15;
+  const double e = rows * 262144.0 / 1.1e15 + rows * std::ceil(per / 256) * 256 * 640.0 / 0.7e15;
   const double s = rows * per * 2176.0 / 0.45e15;
   return e < s;
 }
@@ -418,12 +418,12 @@ mla_status_t run_expanded(const mla_dims_t* d, const ChunkArgs& a, const Layout&
   const uint32_t q_box[3] = {64, ck::kQTile, 3};
   const uint64_t s_ext[3] = {64, (uint64_t)l.rows_cap * l.heads, 2};
   const uint64_t s_str[2] = {(uint64_t)ck::kDn * 2, 128};
-  const uint32_t s_box[3] = {64, ck::kKTile, 2};
+  const uint32_t k_box[3] = {64, ck::kKTile / 2, 2}, v_box[3] = {64, ck::kKTile, 1};
   if (!map_rows(&tc, a.cache, ck::kDc, cache_rows, ck::kDc + ck::kDr, kPage) ||
       !map_bf16(&mp.q, a.q, 3, q_ext, q_str, q_box) ||
-      !map_bf16(&mp.k, ws + l.k, 3, s_ext, s_str, s_box) ||
-      !map_bf16(&mp.v, ws + l.v, 3, s_ext, s_str, s_box) ||
-      !map_rows(&mp.kr, kr, ck::kDr, (uint64_t)l.rows_cap, ck::kDr, ck::kKTile))
+      !map_bf16(&mp.k, ws + l.k, 3, s_ext, s_str, k_box) ||
+      !map_bf16(&mp.v, ws + l.v, 3, s_ext, s_str, v_box) ||
+      !map_rows(&mp.kr, kr, ck::kDr, (uint64_t)l.rows_cap, ck::kDr, ck::kKTile / 2))
     return MLA_ERR_CUDA;
   if (cudaFuncSetAttribute(gm::gemm_kernel<gm::kExpand>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            gm::kSmemMax) != cudaSuccess ||
@@ -479,7 +479,7 @@ mla_status_t run_expanded(const mla_dims_t* d, const ChunkArgs& a, const Layout&
       return MLA_ERR_CUDA;
     p.h0 = h0;
     p.n_heads = nh;
-    if (launch_dependent(ck::chunk_attn_kernel, dim3(max_items, nh), dim3(ck::kThreads),
+    if (launch_dependent(ck::chunk_attn_kernel, dim3(2 * max_items, nh), dim3(ck::kThreads),
                          ck::kSmemBytes, st, true, p, mp) != cudaSuccess)
       return MLA_ERR_CUDA;
   }

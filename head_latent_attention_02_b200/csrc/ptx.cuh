@@ -292,6 +292,26 @@ __device__ __forceinline__ void tmem_ld128_sync(uint32_t taddr, float (&v)[4][32
     for (int i = 0; i < 32; ++i) v[k][i] = __uint_as_float(r[32 * k + i]);
 }
 
+// Two floats in one 64-bit register pair: the FMA pipe's packed operations.
+__device__ __forceinline__ uint64_t pack_f32x2(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void unpack_f32x2(uint64_t v, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
 // 2^x on the special-function unit (flushes denormal results to zero).
 __device__ __forceinline__ float ex2_approx(float x) {
   float y;
@@ -369,6 +389,17 @@ __device__ __forceinline__ void mma_pair_bf16_ss(uint32_t d_tmem, uint64_t a_des
       "setp.ne.b32 p, %4, 0;\n\t"
       "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}"
       ::"r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate) : "memory");
+}
+
+// The pair's product with A read from tensor memory (each CTA's 128 rows from
+// its own) and B's columns from both CTAs' shared memory.
+__device__ __forceinline__ void mma_pair_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
+                                                 uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
+      ::"r"(d_tmem), "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate) : "memory");
 }
 
 // Arrive on the barrier at this shared-memory offset in both CTAs of the pair
@@ -489,6 +520,14 @@ __device__ __forceinline__ void mbar_arrive_expect_tx_cluster(uint32_t bar, uint
                ::"r"(bar), "r"(bytes) : "memory");
 }
 
+// Arrive on a barrier of another CTA (shared::cluster address) after tensor-
+// memory accesses: those are ordered by tcgen05.wait and
+// tcgen05.fence::before_thread_sync, so the arrival needs no cluster-scope
+// release of generic memory, which costs about 1000 clocks.
+__device__ __forceinline__ void mbar_arrive_pair(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+
 // Bulk copy of `bytes` from this CTA's shared memory into another CTA's
 // (shared::cluster destination); completion is counted on a barrier there.
 __device__ __forceinline__ void bulk_copy_to_cluster(uint32_t dst, const void* src, uint32_t bytes,
@@ -502,6 +541,40 @@ __device__ __forceinline__ void bulk_copy_to_cluster(uint32_t dst, const void* s
 }  // namespace mla
 
 namespace mla {
+// ------------------------------------------------------------------ elected forms
+// The pair's products and commits for a converged warp, issued by one elected
+// lane (the same one every time).  With the loop around them warp-uniform,
+// descriptors and addresses stay in uniform registers; inside a branch that
+// one lane takes, each operand is moved there first, which made the issue of
+// an MMA slower than its execution.
+__device__ __forceinline__ void mma_pair_bf16_ss_elect(uint32_t d_tmem, uint64_t a_desc,
+                                                       uint64_t b_desc, uint32_t idesc,
+                                                       uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "elect.sync _|q, 0xffffffff;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "@q tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+      ::"r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate) : "memory");
+}
+__device__ __forceinline__ void mma_pair_bf16_ts_elect(uint32_t d_tmem, uint32_t a_tmem,
+                                                       uint64_t b_desc, uint32_t idesc,
+                                                       uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "elect.sync _|q, 0xffffffff;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "@q tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
+      ::"r"(d_tmem), "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate) : "memory");
+}
+__device__ __forceinline__ void mma_pair_commit_both_elect(uint64_t* bar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t"
+      "elect.sync _|q, 0xffffffff;\n\t"
+      "@q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
+      " [%0], %1;\n\t}" ::"r"(smem_u32(bar)), "h"((uint16_t)0x3) : "memory");
+}
+
 // Plain 16-byte store into another CTA's shared memory (shared::cluster address).
 __device__ __forceinline__ void st_cluster_v4(uint32_t addr, uint4 v) {
   asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};"
