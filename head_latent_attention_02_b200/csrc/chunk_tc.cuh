@@ -23,8 +23,8 @@
 // At 192 + 128 columns a tile costs the tensor core 1280 clocks and its
 // exponentials the special-function units 1024.
 //
-// Roles (320 threads a CTA): warp 0 loads by TMA, warp 1 of the first CTA
-// issues the MMAs, warps 2-5 and 6-9 run the softmax of query tiles 0 and 1 (a
+// Roles (384 threads a CTA): warp 0 loads by TMA, warp 1 of the first CTA
+// issues the MMAs, warps 4-7 and 8-11 run the softmax of query tiles 0 and 1 (a
 // thread per query row, so that row statistics need no exchange between
 // threads).  The running maximum is only raised when it grew by more than
 // 2^8 (the weights then stay below 2^8, harmless in fp32 sums and in bf16,
@@ -38,7 +38,6 @@
 
 #include "common.cuh"
 #include "ptx.cuh"
-#include "gemm_tc.cuh"
 
 namespace mla {
 namespace ck {
@@ -57,7 +56,11 @@ constexpr int kOffKeys = 2 * kQBytes;
 constexpr int kOffVals = kOffKeys + kKeySlots * kKeySlot;
 constexpr int kOffBar = kOffVals + kValSlots * kValSlot;
 constexpr int kSmemBytes = kOffBar + 512 + 1024;
-constexpr int kThreads = 320;
+constexpr int kThreads = 384;
+// registers a thread: launched with 168, redistributed between the warpgroup
+// that loads and issues and the two that hold a row of scores each
+constexpr int kRegsIssue = 88, kRegsSoftmax = 208;
+static_assert(kRegsIssue + 2 * kRegsSoftmax == 3 * 168, "register split");
 constexpr int kTmemCols = 512;
 constexpr int kColS = 0, kColO = 256;
 constexpr float kLog2e = 1.4426950408889634f;
@@ -80,7 +83,7 @@ struct Plan {
 struct Params {
   const Plan* plan;
   const Item* items;
-  const gm::PageEntry* pages;
+  const PageEntry* pages;
   const int32_t* q_pos;
   int H, h0, n_heads;          // heads of the call; first head and heads of this launch
   long long rows_cap;          // rows per head of the key and value scratch
@@ -111,7 +114,7 @@ struct Bars {
 static_assert(sizeof(Bars) <= 512, "barrier block too large");
 
 // Visible rows of one page: those with data whose position is not past qp.
-__device__ __forceinline__ int visible(const gm::PageEntry& e, int qp) {
+__device__ __forceinline__ int visible(const PageEntry& e, int qp) {
   if (e.kpos > qp) return 0;
   const long long d = (long long)qp - e.kpos + 1;
   return d < e.n ? (int)d : e.n;
@@ -176,7 +179,7 @@ chunk_attn_kernel(const __grid_constant__ Params p, const __grid_constant__ Maps
   }
   __syncthreads();
   for (int j = threadIdx.x; j < it.tiles; j += kThreads) {
-    const gm::PageEntry e0 = p.pages[it.entry + 2 * j], e1 = p.pages[it.entry + 2 * j + 1];
+    const PageEntry e0 = p.pages[it.entry + 2 * j], e1 = p.pages[it.entry + 2 * j + 1];
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
       if (t * kPairTile >= it.n) continue;
@@ -194,114 +197,118 @@ chunk_attn_kernel(const __grid_constant__ Params p, const __grid_constant__ Maps
   const int nt0 = bar->n_tiles[0], nt1 = bar->n_tiles[1];
   const int nt = max(nt0, nt1);
 
-  if (warp == 0) {
-    // ------------------------------------------------------------ loads
-    if (lane == 0 && nt > 0) {
-      prefetch_tmap(&mp.q);
-      prefetch_tmap(&mp.k);
-      prefetch_tmap(&mp.v);
-      prefetch_tmap(&mp.kr);
-      const int krow = (int)(hl * p.rows_cap) + it.entry * kPage;
-      // the pair's bytes are counted on the first CTA's barriers
-      auto expect = [&](uint64_t* b, int bytes) {
-        if (rank == 0) mbar_arrive_expect_tx(b, 2 * bytes);
-        return mapa(smem_u32(b), 0);
-      };
-      auto load_q = [&](int t) {
-        const uint32_t b = expect(&bar->q_full[t], kQBytes);
-        tma_load_3d_pair(smem + t * kQBytes, &mp.q, b, 0, it.tok0 + t * kPairTile + rank * kQTile, 3 * h);
-      };
-      bool ok = true;
-      auto wait = [&](uint64_t* b, int use) {      // the slot's use-th filling may start
-        if (!mbar_wait(b, (use & 1) ^ 1)) {
-          set_status(MLA_ERR_TIMEOUT);
-          ok = false;
+  if (warp < 4) {
+    setmaxnreg_dec<kRegsIssue>();
+    if (warp == 0) {
+      // ------------------------------------------------------------ loads
+      if (lane == 0 && nt > 0) {
+        prefetch_tmap(&mp.q);
+        prefetch_tmap(&mp.k);
+        prefetch_tmap(&mp.v);
+        prefetch_tmap(&mp.kr);
+        const int krow = (int)(hl * p.rows_cap) + it.entry * kPage;
+        // the pair's bytes are counted on the first CTA's barriers
+        auto expect = [&](uint64_t* b, int bytes) {
+          if (rank == 0) mbar_arrive_expect_tx(b, 2 * bytes);
+          return mapa(smem_u32(b), 0);
+        };
+        auto load_q = [&](int t) {
+          const uint32_t b = expect(&bar->q_full[t], kQBytes);
+          tma_load_3d_pair(smem + t * kQBytes, &mp.q, b, 0, it.tok0 + t * kPairTile + rank * kQTile, 3 * h);
+        };
+        bool ok = true;
+        auto wait = [&](uint64_t* b, int use) {      // the slot's use-th filling may start
+          if (!mbar_wait(b, (use & 1) ^ 1)) {
+            set_status(MLA_ERR_TIMEOUT);
+            ok = false;
+          }
+          return ok;
+        };
+        if (nt0 > 0) load_q(0);
+        for (int j = 0; ok && j < nt; ++j) {
+          const int ks = j % kKeySlots, vs = j % kValSlots;
+          if (!wait(&bar->k_empty[ks], j / kKeySlots)) break;
+          uint8_t* key = smem + kOffKeys + ks * kKeySlot;
+          uint32_t b = expect(&bar->k_full[ks], kKeySlot);
+          tma_load_3d_pair(key, &mp.k, b, 0, krow + j * kKTile + rank * 64, 0);
+          tma_load_2d_pair(key + kPanel, &mp.kr, b, 0, it.entry * kPage + j * kKTile + rank * 64);
+          if (j == 0 && nt1 > 0) load_q(1);
+          if (!wait(&bar->v_empty[vs], j / kValSlots)) break;
+          b = expect(&bar->v_full[vs], kValSlot);
+          tma_load_3d_pair(smem + kOffVals + vs * kValSlot, &mp.v, b, 0, krow + j * kKTile, rank);
         }
-        return ok;
-      };
-      if (nt0 > 0) load_q(0);
-      for (int j = 0; ok && j < nt; ++j) {
-        const int ks = j % kKeySlots, vs = j % kValSlots;
-        if (!wait(&bar->k_empty[ks], j / kKeySlots)) break;
-        uint8_t* key = smem + kOffKeys + ks * kKeySlot;
-        uint32_t b = expect(&bar->k_full[ks], kKeySlot);
-        tma_load_3d_pair(key, &mp.k, b, 0, krow + j * kKTile + rank * 64, 0);
-        tma_load_2d_pair(key + kPanel, &mp.kr, b, 0, it.entry * kPage + j * kKTile + rank * 64);
-        if (j == 0 && nt1 > 0) load_q(1);
-        if (!wait(&bar->v_empty[vs], j / kValSlots)) break;
-        b = expect(&bar->v_full[vs], kValSlot);
-        tma_load_3d_pair(smem + kOffVals + vs * kValSlot, &mp.v, b, 0, krow + j * kKTile, rank);
       }
-    }
-  } else if (warp == 1) {
-    // ------------------------------------------------------------ MMA
-    if (rank == 0 && nt > 0) {        // the whole warp, converged
-      constexpr uint32_t idesc_s = idesc_bf16_f32(kPairTile, kKTile, false, false);
-      constexpr uint32_t idesc_o = idesc_bf16_f32(kPairTile, kDv, false, true);
-      // Descriptors of the first panels; a panel, a slot or a K step further is
-      // an addition (16-byte units) that never leaves the address field.  The
-      // issuing warp shares its scheduler with softmax warps: building each
-      // descriptor anew cost it 1400 clocks for the eight MMAs of a P V.
-      const uint64_t dq = smem_desc_sw128(smem_u32(smem), 16, 1024);
-      const uint64_t dk = smem_desc_sw128(smem_u32(smem + kOffKeys), 16, 1024);
-      // values: 16 rows of the CTA's 64-column panel per step, rows outermost
-      const uint64_t dv = smem_desc_sw128(smem_u32(smem + kOffVals), kPanel, 1024);
-      bool ok = true;
-      auto wait = [&](uint64_t* b, uint32_t parity) {
-        if (ok && !__all_sync(0xffffffffu, mbar_wait(b, parity))) {
-          if (lane == 0) set_status(MLA_ERR_TIMEOUT);
-          ok = false;
-        }
-      };
-      for (int j = 0; ok && j <= nt; ++j) {
-        // P V of step j - 1, then S of step j, for each query tile; what was
-        // loaded is waited for first, off the chain from weights to scores
-        const int ks_n = j % kKeySlots, vs_n = (j + kValSlots - 1) % kValSlots;
-        if (j < nt) wait(&bar->k_full[ks_n], (j / kKeySlots) & 1);
-        if (j > 0) wait(&bar->v_full[vs_n], ((j - 1) / kValSlots) & 1);
-        if (!ok) break;
-        const uint64_t kd = dk + ks_n * (kKeySlot >> 4), vd = dv + vs_n * (kValSlot >> 4);
+    } else if (warp == 1) {
+      // ------------------------------------------------------------ MMA
+      if (rank == 0 && nt > 0) {        // the whole warp, converged
+        constexpr uint32_t idesc_s = idesc_bf16_f32(kPairTile, kKTile, false, false);
+        constexpr uint32_t idesc_o = idesc_bf16_f32(kPairTile, kDv, false, true);
+        // Descriptors of the first panels; a panel, a slot or a K step further is
+        // an addition (16-byte units) that never leaves the address field.  The
+        // issuing warp shares its scheduler with softmax warps: building each
+        // descriptor anew cost it 1400 clocks for the eight MMAs of a P V.
+        const uint64_t dq = smem_desc_sw128(smem_u32(smem), 16, 1024);
+        const uint64_t dk = smem_desc_sw128(smem_u32(smem + kOffKeys), 16, 1024);
+        // values: 16 rows of the CTA's 64-column panel per step, rows outermost
+        const uint64_t dv = smem_desc_sw128(smem_u32(smem + kOffVals), kPanel, 1024);
+        bool ok = true;
+        auto wait = [&](uint64_t* b, uint32_t parity) {
+          if (ok && !__all_sync(0xffffffffu, mbar_wait(b, parity))) {
+            if (lane == 0) set_status(MLA_ERR_TIMEOUT);
+            ok = false;
+          }
+        };
+        for (int j = 0; ok && j <= nt; ++j) {
+          // P V of step j - 1, then S of step j, for each query tile; what was
+          // loaded is waited for first, off the chain from weights to scores
+          const int ks_n = j % kKeySlots, vs_n = (j + kValSlots - 1) % kValSlots;
+          if (j < nt) wait(&bar->k_full[ks_n], (j / kKeySlots) & 1);
+          if (j > 0) wait(&bar->v_full[vs_n], ((j - 1) / kValSlots) & 1);
+          if (!ok) break;
+          const uint64_t kd = dk + ks_n * (kKeySlot >> 4), vd = dv + vs_n * (kValSlot >> 4);
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          const int mine = t ? nt1 : nt0;
-          const uint32_t s_col = tmem + kColS + t * kKTile, o_col = tmem + kColO + t * kDv;
-          if (j > 0 && j - 1 < mine) {
+          for (int t = 0; t < 2; ++t) {
+            const int mine = t ? nt1 : nt0;
+            const uint32_t s_col = tmem + kColS + t * kKTile, o_col = tmem + kColO + t * kDv;
+            if (j > 0 && j - 1 < mine) {
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
-              wait(&bar->p_full[t][half], (j - 1) & 1);
+              for (int half = 0; half < 2; ++half) {
+                wait(&bar->p_full[t][half], (j - 1) & 1);
+                tc_fence_after();
+                if (!ok) break;
+#pragma unroll
+                for (int ks = 4 * half; ks < 4 * half + 4; ++ks)
+                  mma_pair_bf16_ts_elect(o_col, s_col + 8 * ks, vd + ks * (2048 >> 4), idesc_o,
+                                         (j > 1 || ks > 0) ? 1u : 0u);
+              }
+              if (!ok) break;
+              if (j == mine) mma_pair_commit_both_elect(&bar->o_full[t]);
+            }
+            if (j < mine) {
+              if (j == 0) {
+                wait(&bar->q_full[t], 0);
+                if (!ok) break;
+              }
               tc_fence_after();
-              if (!ok) break;
+              const uint64_t qd = dq + t * (kQBytes >> 4);
+              // query panels are 128 rows high, a CTA's key panels 64
 #pragma unroll
-              for (int ks = 4 * half; ks < 4 * half + 4; ++ks)
-                mma_pair_bf16_ts_elect(o_col, s_col + 8 * ks, vd + ks * (2048 >> 4), idesc_o,
-                                       (j > 1 || ks > 0) ? 1u : 0u);
+              for (int ks = 0; ks < 12; ++ks)
+                mma_pair_bf16_ss_elect(s_col, qd + (ks >> 2) * (kPanel >> 4) + (ks & 3) * 2,
+                                       kd + (ks >> 2) * (kPanel >> 5) + (ks & 3) * 2, idesc_s,
+                                       ks ? 1u : 0u);
+              mma_pair_commit_both_elect(&bar->s_full[t]);
             }
-            if (!ok) break;
-            if (j == mine) mma_pair_commit_both_elect(&bar->o_full[t]);
           }
-          if (j < mine) {
-            if (j == 0) {
-              wait(&bar->q_full[t], 0);
-              if (!ok) break;
-            }
-            tc_fence_after();
-            const uint64_t qd = dq + t * (kQBytes >> 4);
-            // query panels are 128 rows high, a CTA's key panels 64
-#pragma unroll
-            for (int ks = 0; ks < 12; ++ks)
-              mma_pair_bf16_ss_elect(s_col, qd + (ks >> 2) * (kPanel >> 4) + (ks & 3) * 2,
-                                     kd + (ks >> 2) * (kPanel >> 5) + (ks & 3) * 2, idesc_s,
-                                     ks ? 1u : 0u);
-            mma_pair_commit_both_elect(&bar->s_full[t]);
-          }
+          if (j > 0) mma_pair_commit_both_elect(&bar->v_empty[vs_n]);
+          if (j < nt) mma_pair_commit_both_elect(&bar->k_empty[ks_n]);
         }
-        if (j > 0) mma_pair_commit_both_elect(&bar->v_empty[vs_n]);
-        if (j < nt) mma_pair_commit_both_elect(&bar->k_empty[ks_n]);
       }
     }
   } else {
     // ------------------------------------------------------------ softmax
-    const int t = warp >= 6 ? 1 : 0;
+    setmaxnreg_inc<kRegsSoftmax>();
+    const int t = warp >= 8 ? 1 : 0;
     const int quad = warp & 3;
     const int row = quad * 32 + lane;                 // row of the query tile
     const int tok = t * kPairTile + rank * kQTile + row;   // token of the item
@@ -313,7 +320,7 @@ chunk_attn_kernel(const __grid_constant__ Params p, const __grid_constant__ Maps
     float m = kNegInf, l = 0.f;       // running maximum (unscaled scores), sum of weights
     bool ok = true;
     if (mine > 0) {
-      const gm::PageEntry* pe = p.pages + it.entry;
+      const PageEntry* pe = p.pages + it.entry;
       const int n_full = bar->n_full[t];
       for (int j = 0; j < mine; ++j) {
         int v0 = kPage, v1 = kPage;
@@ -381,7 +388,7 @@ chunk_attn_kernel(const __grid_constant__ Params p, const __grid_constant__ Maps
             x = ex2_approx(x);
             y = ex2_approx(y);
             sum[i & 1] = add_f32x2(sum[i & 1], pack_f32x2(x, y));
-            w[i] = __uint_as_float(gm::pack2(x, y));
+            w[i] = __uint_as_float(pack2(x, y));
           }
           tmem_st32(s_col + 32 * c, w);
           tmem_wait_st();
@@ -419,7 +426,7 @@ chunk_attn_kernel(const __grid_constant__ Params p, const __grid_constant__ Maps
           uint32_t w[4];
 #pragma unroll
           for (int k = 0; k < 4; ++k)
-            w[k] = none ? 0u : gm::pack2(a[8 * i + 2 * k] * inv, a[8 * i + 2 * k + 1] * inv);
+            w[k] = none ? 0u : pack2(a[8 * i + 2 * k] * inv, a[8 * i + 2 * k + 1] * inv);
           d[i] = make_uint4(w[0], w[1], w[2], w[3]);
         }
       }

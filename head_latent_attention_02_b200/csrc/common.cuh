@@ -42,9 +42,25 @@ __device__ __forceinline__ float round_bf16(float x) {
   return __bfloat162float(__float2bfloat16_rn(x));
 }
 
+// Two floats as a pair of bfloat16 (the first one in the low half), and back.
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  const __nv_bfloat162 t = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&t);
+}
+__device__ __forceinline__ float lo_f(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float hi_f(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+
 constexpr int kPage = 64;
 constexpr int kMaxVersions = 8;
 constexpr float kNegInf = -__builtin_huge_valf();
+
+// 64 rows of the paged cache that a chunk call attends (mla_chunk.cu).
+struct PageEntry {
+  int row;      // physical cache row of the page's first row; past the cache: no rows
+  int kpos;     // request position of that row
+  int n;        // rows that hold data (0 .. 64)
+  int ver;      // relocation version
+};
 
 // Description of one mla_decode call as the kernels see it.
 struct DecodeArgs {

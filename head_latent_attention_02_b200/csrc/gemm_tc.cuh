@@ -1,10 +1,7 @@
 // gemm_tc.cuh -- bf16 matrix products with fused epilogues on sm_100a tensor
 // cores: D[m, n] = sum_k A[m, k] B[n, k], both operands K-major, fp32
-// accumulation in tensor memory.
-//
-//   linear  out = act(x W^T + bias) + residual (mla_linear)
-//   expand  K_h = W_UK[h] c and V_h = W_UV[h] c for the cached latents c of a
-//           page list, per head (the key and value rows of mla_chunk_attn)
+// accumulation in tensor memory; out = act(x W^T + bias) + residual
+// (mla_linear).
 //
 // Tile.  A cluster of two CTAs computes 256 x BN (cta_group::2, BN <= 256):
 // each CTA holds 128 rows of A and half of B's rows in shared memory, and the
@@ -49,19 +46,11 @@ constexpr int kGroupM = 8;               // row tiles that share a pass over the
 
 enum Act : int { kNone = 0, kSilu = 1, kGelu = 2 };
 
-// 64 rows of the paged cache that a chunk call attends (mla_chunk.cu).
-struct PageEntry {
-  int row;      // physical cache row of the page's first row; past the cache: no rows
-  int kpos;     // request position of that row
-  int n;        // rows that hold data (0 .. 64)
-  int ver;      // relocation version
-};
-
 struct Params {
   int k_steps, n_mt, n_nt, BN, stages;
   int P;                     // 64-K panels of a stage; > 1: three-axis maps over whole panels
   int chunk;                 // split: units of a pair's run; 0: whole tiles
-  // linear: the M x N result; swapped: A holds W's rows and B x's
+  // the M x N result; swapped: A holds W's rows and B x's
   int swapped, M, N, act;
   long long res_stride, out_stride;
   const float* bias;
@@ -69,13 +58,6 @@ struct Params {
   __nv_bfloat16* out;
   float* partial;            // split: [2 x pairs][BN][256]
   int vec;                   // out and residual rows take 16-byte accesses
-  // expand
-  const PageEntry* pages;    // four entries a row tile
-  const int* n_tiles;        // device: row tiles in use
-  int n_heads;               // heads of this launch
-  long long rows_cap;        // rows per head of the key and value scratch
-  __nv_bfloat16* k_out;      // [n_heads][rows_cap][128]
-  __nv_bfloat16* v_out;
 };
 
 struct Bars {
@@ -127,13 +109,6 @@ __device__ __forceinline__ float activate(float x, int act) {
   return x;
 }
 
-__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
-  const __nv_bfloat162 t = __floats2bfloat162_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&t);
-}
-__device__ __forceinline__ float lo_f(uint32_t w) { return __uint_as_float(w << 16); }
-__device__ __forceinline__ float hi_f(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
-
 // Eight consecutive results of one row: out[m][n .. n + 8) = act(v + bias) +
 // residual.  Handles columns past N and rows that take no 16-byte access.
 __device__ __forceinline__ void finish8(const Params& p, int m, int n, const float* v) {
@@ -161,24 +136,17 @@ __device__ __forceinline__ void finish8(const Params& p, int m, int n, const flo
   }
 }
 
-enum Mode : int { kLinear = 0, kExpand = 1 };
-
-// linear: ta over A, box {64, 128}; tb over B, box {64, BN / 2}; with P > 1 both
-// as (64-column offset, row, panel), P panels deep, so that a box row is 128 P
-// contiguous bytes.  expand: ta
-// over the cache rows, box {64, 64}; tb / tv over W_UK / W_UV seen as
-// [heads x 128, 512], box {64, 128}: the first CTA's half of B is W_UK[h],
-// the second's W_UV[h], so columns 0 .. 127 of the tile are keys and the rest
-// values.
-template <int kMode>
+// ta over A, box {64, 128}; tb over B, box {64, BN / 2}; with P > 1 both as
+// (64-column offset, row, panel), P panels deep, so that a box row is 128 P
+// contiguous bytes.
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 gemm_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtensorMap ta,
-            const __grid_constant__ CUtensorMap tb, const __grid_constant__ CUtensorMap tv) {
+            const __grid_constant__ CUtensorMap tb) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int S = p.stages;
-  const int P = kMode == kExpand ? 1 : p.P;
+  const int P = p.P;
   const int b_panel = p.BN / 2 * 128;
   const int a_bytes = P * kABytes;
   const int stage = a_bytes + P * b_panel;
@@ -204,28 +172,19 @@ gemm_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtensorMa
   cluster_sync();
   tc_fence_after();
   const uint32_t tmem = bar->tmem_base;
-  // what this kernel reads of the launch before it (the page list, the
-  // attention's values) is complete after this wait
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int tiles = kMode == kExpand ? *p.n_tiles * p.n_heads : p.n_mt * p.n_nt;
+  const int tiles = p.n_mt * p.n_nt;
 
   if (warp == 0) {
     // ------------------------------------------------------------ loads
     if (lane == 0) {
       prefetch_tmap(&ta);
-      prefetch_tmap(rank && kMode == kExpand ? &tv : &tb);
+      prefetch_tmap(&tb);
       bool ok = true;
       Seg s;
       for (int i = 0, n = 0; ok && segment(p, tiles, pair, pairs, i, &s); ++i) {
-        int mt, nt, y0 = 0, y1 = 0;
-        if (kMode == kExpand) {
-          mt = s.tile / p.n_heads;
-          nt = s.tile % p.n_heads;
-          y0 = p.pages[4 * mt + 2 * rank].row;
-          y1 = p.pages[4 * mt + 2 * rank + 1].row;
-        } else {
-          tile_at(p, s.tile, &mt, &nt);
-        }
+        int mt, nt;
+        tile_at(p, s.tile, &mt, &nt);
+        const int ra = mt * kPairRows + (int)rank * kRows, rb = nt * p.BN + (int)rank * (p.BN / 2);
         for (int k = s.k0; k < s.k1; ++k, ++n) {
           const int slot = n % S;
           if (!mbar_wait(&bar->empty[slot], ((n / S) & 1) ^ 1)) {
@@ -237,19 +196,12 @@ gemm_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtensorMa
           if (rank == 0) mbar_arrive_expect_tx(&bar->full[slot], 2 * stage);
           const uint32_t fb = mapa(smem_u32(&bar->full[slot]), 0);
           uint8_t* dst = smem + slot * stage;
-          if (kMode == kExpand) {
-            tma_load_2d_pair(dst, &ta, fb, k * kKStep, y0);
-            tma_load_2d_pair(dst + kABytes / 2, &ta, fb, k * kKStep, y1);
-            tma_load_2d_pair(dst + kABytes, rank ? &tv : &tb, fb, k * kKStep, nt * 128);
+          if (P == 1) {
+            tma_load_2d_pair(dst, &ta, fb, k * kKStep, ra);
+            tma_load_2d_pair(dst + a_bytes, &tb, fb, k * kKStep, rb);
           } else {
-            const int ra = mt * kPairRows + (int)rank * kRows, rb = nt * p.BN + (int)rank * (p.BN / 2);
-            if (P == 1) {
-              tma_load_2d_pair(dst, &ta, fb, k * kKStep, ra);
-              tma_load_2d_pair(dst + a_bytes, &tb, fb, k * kKStep, rb);
-            } else {
-              tma_load_3d_pair(dst, &ta, fb, 0, ra, k * P);
-              tma_load_3d_pair(dst + a_bytes, &tb, fb, 0, rb, k * P);
-            }
+            tma_load_3d_pair(dst, &ta, fb, 0, ra, k * P);
+            tma_load_3d_pair(dst + a_bytes, &tb, fb, 0, rb, k * P);
           }
         }
       }
@@ -300,56 +252,14 @@ gemm_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtensorMa
     for (int i = 0; segment(p, tiles, pair, pairs, i, &s); ++i) {
       const int ab = i & 1;
       const uint32_t acc = tmem + ab * kMaxBN + ((uint32_t)(quad * 32) << 16);
-      PageEntry pe = {0, 0, 0, 0};
       int mt, nt;
-      if (kMode == kExpand) {
-        mt = s.tile / p.n_heads;
-        nt = s.tile % p.n_heads;
-        pe = p.pages[4 * mt + row / 64];
-      } else {
-        tile_at(p, s.tile, &mt, &nt);
-      }
+      tile_at(p, s.tile, &mt, &nt);
       if (!__all_sync(0xffffffffu, mbar_wait(&bar->acc_full[ab], (i >> 1) & 1))) {
         if (lane == 0) set_status(MLA_ERR_TIMEOUT);
         break;
       }
       tc_fence_after();
-      if constexpr (kMode == kExpand) {
-        // Rows without data are zeros (a weight of zero times NaN is NaN).  A
-        // value that is not finite is stored as zero and marks the row's key
-        // as NaN instead: queries that see the row get NaN, queries whose mask
-        // hides it are not touched by it.
-        const bool live = row % 64 < pe.n;
-        const long long at = ((long long)nt * p.rows_cap + (long long)mt * kPairRows + row) * 128;
-        bool fine = true;
-#pragma unroll 1
-        for (int c = 96; c >= 0; c -= 32) {
-          float v[32];
-          tmem_ld32_sync(acc + 128 + c, v);
-          uint32_t w[16];
-#pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            const bool f0 = fabsf(v[2 * j]) <= 3.38953139e38f, f1 = fabsf(v[2 * j + 1]) <= 3.38953139e38f;
-            fine = fine && f0 && f1;
-            w[j] = pack2(live && f0 ? v[2 * j] : 0.f, live && f1 ? v[2 * j + 1] : 0.f);
-          }
-          uint4* o = reinterpret_cast<uint4*>(p.v_out + at + c);
-#pragma unroll
-          for (int j = 0; j < 4; ++j) o[j] = make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
-        }
-#pragma unroll 1
-        for (int c = 96; c >= 0; c -= 32) {
-          float v[32];
-          tmem_ld32_sync(acc + c, v);
-          if (c == 0 && !fine) v[0] = __int_as_float(0x7fc00000);
-          uint32_t w[16];
-#pragma unroll
-          for (int j = 0; j < 16; ++j) w[j] = live ? pack2(v[2 * j], v[2 * j + 1]) : 0u;
-          uint4* o = reinterpret_cast<uint4*>(p.k_out + at + c);
-#pragma unroll
-          for (int j = 0; j < 4; ++j) o[j] = make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
-        }
-      } else if (s.k1 - s.k0 < p.k_steps) {
+      if (s.k1 - s.k0 < p.k_steps) {
         // part of a tile: the pair's first slot holds a segment that starts
         // its run, the second one that ends it
         const bool first = (long long)s.tile * p.k_steps + s.k0 == (long long)pair * p.chunk;

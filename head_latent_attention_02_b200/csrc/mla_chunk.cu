@@ -3,7 +3,7 @@
 //
 // Two routes compute the same result, chosen by a rule on sizes (chunk_route):
 //   expanded   bf16 rows of 512 + 64, 128-wide heads: keys and values are
-//              expanded once per call into the workspace (gemm_tc.cuh), the
+//              expanded once per call into the workspace (expand_tc.cuh), the
 //              rotary keys moved to their request positions, and the direct
 //              form attends over them (chunk_tc.cuh).  For chunks.
 //   absorbed   everything else -- few tokens, fp32, other widths: each token is
@@ -21,7 +21,7 @@
 #include "common.cuh"
 #include "ptx.cuh"
 #include "host_tma.cuh"
-#include "gemm_tc.cuh"
+#include "expand_tc.cuh"
 #include "chunk_tc.cuh"
 
 namespace mla {
@@ -64,7 +64,7 @@ __device__ int sequence_pages(const ChunkArgs& a, int b) {
 
 // The i-th page of sequence b's segments (i below sequence_pages): false when
 // its id is out of range.
-__device__ bool page_at(const ChunkArgs& a, int b, int i, gm::PageEntry* e) {
+__device__ bool page_at(const ChunkArgs& a, int b, int i, PageEntry* e) {
   const mla_seg_t* sg = a.segs + (size_t)b * a.max_segs;
   for (int s = 0; s < a.max_segs; ++s) {
     const int len = sg[s].row_end - sg[s].row_begin;
@@ -132,7 +132,7 @@ __device__ __forceinline__ int last_at_most(const int* off, int n, int x) {
 // [B].  A sequence that does not fit `cap` pages is invalid.
 __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(
     const __grid_constant__ ChunkArgs a, int cap, ck::Plan* plan, int* seq, ck::Item* items,
-    gm::PageEntry* pages) {
+    PageEntry* pages) {
   asm volatile("griddepcontrol.launch_dependents;");
   __shared__ int scratch[33], n_pg, n_it, used;
   int* pg = seq;
@@ -174,7 +174,7 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(
   }
   __syncthreads();
   for (int e = threadIdx.x; e < whole; e += kPlanThreads) {
-    gm::PageEntry pe = {INT32_MAX - 2 * kPage, INT32_MAX, 0, 0};   // no rows
+    PageEntry pe = {INT32_MAX - 2 * kPage, INT32_MAX, 0, 0};   // no rows
     if (e < in_use) {
       const int b = last_at_most(pg, a.B, e);
       if (!bad[b] && e - pg[b] < sequence_pages(a, b) && !page_at(a, b, e - pg[b], &pe)) {
@@ -206,13 +206,13 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(
 // four threads a row.
 __global__ void __launch_bounds__(256) chunk_rotary_kernel(const __grid_constant__ ChunkArgs a,
                                                            const ck::Plan* plan,
-                                                           const gm::PageEntry* pages,
+                                                           const PageEntry* pages,
                                                            __nv_bfloat16* kr) {
   asm volatile("griddepcontrol.launch_dependents;");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   __shared__ double2 cs[ck::kDr / 2];
   if ((int)blockIdx.x >= 4 * plan->n_row_tiles) return;
-  const gm::PageEntry e = pages[blockIdx.x];
+  const PageEntry e = pages[blockIdx.x];
   const int delta = e.n > 0 ? a.delta[e.ver] : 0;
   if (delta != 0) {
     for (int i = threadIdx.x; i < ck::kDr / 2; i += 256)
@@ -232,8 +232,8 @@ __global__ void __launch_bounds__(256) chunk_rotary_kernel(const __grid_constant
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const double2 t = cs[part * 8 + i];
-        const double x0 = gm::lo_f(w[i]), x1 = gm::hi_f(w[i]);
-        w[i] = gm::pack2((float)(x0 * t.x - x1 * t.y), (float)(x0 * t.y + x1 * t.x));
+        const double x0 = lo_f(w[i]), x1 = hi_f(w[i]);
+        w[i] = pack2((float)(x0 * t.x - x1 * t.y), (float)(x0 * t.y + x1 * t.x));
       }
     }
   }
@@ -272,7 +272,7 @@ __global__ void __launch_bounds__(256) chunk_spread_kernel(const __grid_constant
   if (b >= 0) {
     const int np = sequence_pages(a, b);
     if (np < 0 && threadIdx.x == 0) s_bad = 1;
-    gm::PageEntry e;
+    PageEntry e;
     for (int k = threadIdx.x; k < np; k += blockDim.x)
       if (!page_at(a, b, k, &e)) s_bad = 1;
   }
@@ -369,7 +369,7 @@ bool make_layout(const mla_dims_t* d, int B, int n_tok, int n_ver, int max_pages
     l->plan = take(sizeof(ck::Plan));
     l->seq = take(sizeof(int) * (3 * (size_t)B + 2));
     l->items = take(sizeof(ck::Item) * ((size_t)n_tok / ck::kItemTokens + B));
-    l->pages = take(sizeof(gm::PageEntry) * (size_t)cap);
+    l->pages = take(sizeof(PageEntry) * (size_t)cap);
     l->kr = take((size_t)l->rows_cap * ck::kDr * 2);
     l->k = take((size_t)l->rows_cap * l->heads * ck::kDn * 2);
     l->v = take((size_t)l->rows_cap * l->heads * ck::kDv * 2);
@@ -407,11 +407,11 @@ mla_status_t run_expanded(const mla_dims_t* d, const ChunkArgs& a, const Layout&
   if (!sms) return MLA_ERR_CUDA;
   ck::Plan* plan = reinterpret_cast<ck::Plan*>(ws + l.plan);
   ck::Item* items = reinterpret_cast<ck::Item*>(ws + l.items);
-  gm::PageEntry* pages = reinterpret_cast<gm::PageEntry*>(ws + l.pages);
+  PageEntry* pages = reinterpret_cast<PageEntry*>(ws + l.pages);
   __nv_bfloat16* kr = reinterpret_cast<__nv_bfloat16*>(ws + l.kr);
   const uint64_t cache_rows = (uint64_t)a.n_pages * kPage;
 
-  CUtensorMap tc;
+  ex::Maps xm;
   ck::Maps mp;
   const uint64_t q_ext[3] = {64, (uint64_t)a.n_tok, 3ull * d->H};
   const uint64_t q_str[2] = {(uint64_t)d->H * (ck::kDn + ck::kDr) * 2, 128};
@@ -419,14 +419,17 @@ mla_status_t run_expanded(const mla_dims_t* d, const ChunkArgs& a, const Layout&
   const uint64_t s_ext[3] = {64, (uint64_t)l.rows_cap * l.heads, 2};
   const uint64_t s_str[2] = {(uint64_t)ck::kDn * 2, 128};
   const uint32_t k_box[3] = {64, ck::kKTile / 2, 2}, v_box[3] = {64, ck::kKTile, 1};
-  if (!map_rows(&tc, a.cache, ck::kDc, cache_rows, ck::kDc + ck::kDr, kPage) ||
+  const uint32_t o_box[3] = {64, 32, 1};
+  if (!map_rows(&xm.c, a.cache, ck::kDc, cache_rows, ck::kDc + ck::kDr, kPage) ||
       !map_bf16(&mp.q, a.q, 3, q_ext, q_str, q_box) ||
       !map_bf16(&mp.k, ws + l.k, 3, s_ext, s_str, k_box) ||
       !map_bf16(&mp.v, ws + l.v, 3, s_ext, s_str, v_box) ||
+      !map_bf16(&xm.k, ws + l.k, 3, s_ext, s_str, o_box) ||
+      !map_bf16(&xm.v, ws + l.v, 3, s_ext, s_str, o_box) ||
       !map_rows(&mp.kr, kr, ck::kDr, (uint64_t)l.rows_cap, ck::kDr, ck::kKTile / 2))
     return MLA_ERR_CUDA;
-  if (cudaFuncSetAttribute(gm::gemm_kernel<gm::kExpand>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           gm::kSmemMax) != cudaSuccess ||
+  if (cudaFuncSetAttribute(ex::expand_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           ex::kSmemBytes) != cudaSuccess ||
       cudaFuncSetAttribute(ck::chunk_attn_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            ck::kSmemBytes) != cudaSuccess)
     return MLA_ERR_CUDA;
@@ -436,19 +439,13 @@ mla_status_t run_expanded(const mla_dims_t* d, const ChunkArgs& a, const Layout&
   if (cudaGetLastError() != cudaSuccess) return MLA_ERR_CUDA;
   if (launch_dependent(chunk_rotary_kernel, dim3(l.cap), dim3(256), 0, st, true, a,
                        static_cast<const ck::Plan*>(plan),
-                       static_cast<const gm::PageEntry*>(pages), kr) != cudaSuccess)
+                       static_cast<const PageEntry*>(pages), kr) != cudaSuccess)
     return MLA_ERR_CUDA;
 
-  gm::Params g = {};
-  g.k_steps = ck::kDc / gm::kKStep;
-  g.BN = ck::kDn + ck::kDv;
-  const int stage = gm::kABytes + g.BN / 2 * 128;
-  g.stages = (gm::kSmemMax - gm::kBarBytes - 1024) / stage;
+  ex::Params g;
   g.pages = pages;
-  g.n_tiles = &plan->n_row_tiles;
+  g.n_row_tiles = &plan->n_row_tiles;
   g.rows_cap = l.rows_cap;
-  g.k_out = reinterpret_cast<__nv_bfloat16*>(ws + l.k);
-  g.v_out = reinterpret_cast<__nv_bfloat16*>(ws + l.v);
   ck::Params p;
   p.plan = plan;
   p.items = items;
@@ -463,19 +460,17 @@ mla_status_t run_expanded(const mla_dims_t* d, const ChunkArgs& a, const Layout&
   const int max_items = a.n_tok / ck::kItemTokens + a.B;
   for (int h0 = 0; h0 < d->H; h0 += l.heads) {
     const int nh = std::min(l.heads, d->H - h0);
-    CUtensorMap tk, tv;
     const uint64_t w_rows = (uint64_t)nh * ck::kDn;
-    if (!map_rows(&tk, static_cast<const __nv_bfloat16*>(w_uk) + (size_t)h0 * ck::kDn * ck::kDc,
+    if (!map_rows(&xm.uk, static_cast<const __nv_bfloat16*>(w_uk) + (size_t)h0 * ck::kDn * ck::kDc,
                   ck::kDc, w_rows, ck::kDc, 128) ||
-        !map_rows(&tv, static_cast<const __nv_bfloat16*>(w_uv) + (size_t)h0 * ck::kDv * ck::kDc,
+        !map_rows(&xm.uv, static_cast<const __nv_bfloat16*>(w_uv) + (size_t)h0 * ck::kDv * ck::kDc,
                   ck::kDc, w_rows, ck::kDc, 128))
       return MLA_ERR_CUDA;
     g.n_heads = nh;
     const long long tiles = (long long)l.cap / 4 * nh;
     const int grid = 2 * (int)std::min<long long>(tiles, sms / 2 > 0 ? sms / 2 : 1);
-    if (launch_dependent(gm::gemm_kernel<gm::kExpand>, dim3(grid), dim3(gm::kThreads),
-                         g.stages * stage + gm::kBarBytes + 1024, st, true, g, tc, tk, tv) !=
-        cudaSuccess)
+    if (launch_dependent(ex::expand_kernel, dim3(grid), dim3(ex::kThreads), ex::kSmemBytes, st, true,
+                         g, xm) != cudaSuccess)
       return MLA_ERR_CUDA;
     p.h0 = h0;
     p.n_heads = nh;

@@ -293,11 +293,11 @@ extern "C" mla_status_t mla_linear(int32_t dtype, int32_t M, int32_t N, int32_t 
                                      map_panels(&tb, b, K, br, bs, t.BN / 2, t.P);
   if (!mapped) return MLA_ERR_CUDA;
   const int smem = t.stages * t.P * (gm::kABytes + t.BN / 2 * 128) + gm::kBarBytes + 1024;
-  if (cudaFuncSetAttribute(gm::gemm_kernel<gm::kLinear>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  if (cudaFuncSetAttribute(gm::gemm_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            gm::kSmemMax) != cudaSuccess)
     return MLA_ERR_CUDA;
-  if (launch_dependent(gm::gemm_kernel<gm::kLinear>, dim3(t.grid), dim3(gm::kThreads), smem, st,
-                       false, p, ta, tb, tb) != cudaSuccess)
+  if (launch_dependent(gm::gemm_kernel, dim3(t.grid), dim3(gm::kThreads), smem, st,
+                       false, p, ta, tb) != cudaSuccess)
     return MLA_ERR_CUDA;
   if (t.chunk &&
       launch_dependent(linear_finish_kernel, dim3(t.n_mt * t.n_nt, t.BN / 8), dim3(256), 0, st,

@@ -292,6 +292,16 @@ __device__ __forceinline__ void tmem_ld128_sync(uint32_t taddr, float (&v)[4][32
     for (int i = 0; i < 32; ++i) v[k][i] = __uint_as_float(r[32 * k + i]);
 }
 
+// Registers a thread of the executing warpgroup: every warp of it runs this.
+template <int N>
+__device__ __forceinline__ void setmaxnreg_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void setmaxnreg_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+
 // Two floats in one 64-bit register pair: the FMA pipe's packed operations.
 __device__ __forceinline__ uint64_t pack_f32x2(float lo, float hi) {
   uint64_t r;
