@@ -249,14 +249,25 @@ enum TokState : int { kLive = 0, kNone = 1, kBad = 2 };
 // segment rows, their queries split into both parts, a zero rotation position
 // (q is rotated already; absorption then turns it by -delta alone), and
 // whether they belong to a sequence.  A token without one, or of an invalid
-// one, gets no segments.  One block per token.
-template <typename T>
+// one, gets no segments.  grid (tokens, head blocks of eight), a warp per head;
+// w_n and w_r count the 16-byte or single-element words of both query parts.
+template <typename W>
 __global__ void __launch_bounds__(256) chunk_spread_kernel(const __grid_constant__ ChunkArgs a,
-                                                           int t0, int32_t* table,
-                                                           mla_seg_t* segs, T* q_nope, T* q_rope,
+                                                           int t0, int w_n, int w_r,
+                                                           int32_t* table, mla_seg_t* segs,
+                                                           W* q_nope, W* q_rope,
                                                            int32_t* rot_pos, int* state) {
   __shared__ int s_b, s_bad;
-  const int i = blockIdx.x, t = t0 + i;
+  const int i = blockIdx.x, t = t0 + i, first = blockIdx.y == 0;
+  const int h = blockIdx.y * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  // the queries do not depend on the sequence
+  if (h < a.H) {
+    const W* q = static_cast<const W*>(a.q) + ((size_t)t * a.H + h) * (w_n + w_r);
+    const size_t at = (size_t)i * a.H + h;
+    for (int k = lane; k < w_n; k += 32) q_nope[at * w_n + k] = q[k];
+    for (int k = lane; k < w_r; k += 32) q_rope[at * w_r + k] = q[w_n + k];
+  }
+  if (!first) return;
   if (threadIdx.x == 0) {
     s_b = -1;
     s_bad = 0;
@@ -289,28 +300,37 @@ __global__ void __launch_bounds__(256) chunk_spread_kernel(const __grid_constant
   for (int k = threadIdx.x; k < a.max_segs; k += blockDim.x)
     segs[(size_t)i * a.max_segs + k] =
         st == kLive ? a.segs[(size_t)b * a.max_segs + k] : mla_seg_t{0, 0, 0, 0};
-  const T* q = static_cast<const T*>(a.q) + (size_t)t * a.H * (a.d_n + a.d_r);
-  for (int k = threadIdx.x; k < a.H * a.d_n; k += blockDim.x)
-    q_nope[(size_t)i * a.H * a.d_n + k] = q[(size_t)(k / a.d_n) * (a.d_n + a.d_r) + k % a.d_n];
-  for (int k = threadIdx.x; k < a.H * a.d_r; k += blockDim.x)
-    q_rope[(size_t)i * a.H * a.d_r + k] =
-        q[(size_t)(k / a.d_r) * (a.d_n + a.d_r) + a.d_n + k % a.d_r];
 }
 
 // Results of those tokens in the storage type; tokens of no sequence keep
-// what their rows held.
-template <typename T>
-__global__ void __launch_bounds__(256) chunk_store_kernel(int t0, int H, int d_v, const int* state,
-                                                          const float* v, const float* lse_in,
+// what their rows held.  kValue: the value expansion v = W_UV[h] o_lat happens
+// here (widths that the tensor-core product does not take; its CUDA-core
+// counterpart walks all tokens in one warp), else `x` holds v already.  grid
+// (tokens, head blocks of eight), a warp per head.
+template <typename T, bool kValue>
+__global__ void __launch_bounds__(256) chunk_store_kernel(int t0, int H, int d_c, int d_v,
+                                                          const int* state, const float* x,
+                                                          const T* w_uv, const float* lse_in,
                                                           T* out, float* lse) {
   const int i = blockIdx.x, st = state[i];
-  if (st == kNone) return;
-  const size_t row = (size_t)(t0 + i) * H;
-  for (int k = threadIdx.x; k < H * d_v; k += blockDim.x)
-    out[row * d_v + k] = from_f<T>(st == kBad ? kNaN : v[(size_t)i * H * d_v + k]);
-  if (lse)
-    for (int k = threadIdx.x; k < H; k += blockDim.x)
-      lse[row + k] = st == kBad ? kNaN : lse_in[(size_t)i * H + k];
+  const int h = blockIdx.y * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  if (st == kNone || h >= H) return;
+  const size_t at = (size_t)i * H + h, row = (size_t)(t0 + i) * H + h;
+  if (lse && lane == 0) lse[row] = st == kBad ? kNaN : lse_in[at];
+  if (kValue && st == kLive) {
+    const float* o = x + at * d_c;
+    for (int d = 0; d < d_v; ++d) {
+      const T* w = w_uv + ((size_t)h * d_v + d) * d_c;
+      float s = 0.f;
+      for (int c = lane; c < d_c; c += 32) s = fmaf(to_f(w[c]), o[c], s);
+#pragma unroll
+      for (int k = 16; k; k >>= 1) s += __shfl_xor_sync(0xffffffffu, s, k);
+      if (lane == 0) out[row * d_v + d] = from_f<T>(s);
+    }
+  } else {
+    for (int d = lane; d < d_v; d += 32)
+      out[row * d_v + d] = from_f<T>(st == kBad ? kNaN : x[at * d_v + d]);
+  }
 }
 
 // ------------------------------------------------------------ host
@@ -319,6 +339,11 @@ size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
 bool expandable(const mla_dims_t* d) {
   return d->dtype == MLA_BF16 && d->d_c == ck::kDc && d->d_r == ck::kDr && d->d_n == ck::kDn &&
          d->d_v == ck::kDv;
+}
+
+// widths of the tensor-core value product (mla_out_proj)
+bool value_tc(const mla_dims_t* d) {
+  return d->dtype == MLA_BF16 && d->d_v % 128 == 0 && d->d_c % 64 == 0;
 }
 
 struct Layout {
@@ -386,7 +411,7 @@ bool make_layout(const mla_dims_t* d, int B, int n_tok, int n_ver, int max_pages
     l->q_abs = take(n * n_ver * d->H * row * es);
     l->o_lat = take(n * d->H * d->d_c * 4);
     l->lse = take(n * d->H * 4);
-    l->vf = take(n * d->H * d->d_v * 4);
+    l->vf = take(value_tc(d) ? n * d->H * d->d_v * 4 : 0);
     l->ws_bytes = mla_decode_workspace_size(d, l->slab, 1, n_ver, d->H);
     if (l->ws_bytes == 0) return false;
     l->ws = take(l->ws_bytes);
@@ -496,7 +521,15 @@ mla_status_t run_absorbed(const mla_dims_t* d, const ChunkArgs& a, const Layout&
   mla_stream_t ms = reinterpret_cast<mla_stream_t>(st);
   for (int t0 = 0; t0 < a.n_tok; t0 += l.slab) {
     const int n = std::min(l.slab, a.n_tok - t0);
-    chunk_spread_kernel<T><<<n, 256, 0, st>>>(a, t0, table, segs, q_nope, q_rope, rot, state);
+    const dim3 grid(n, (d->H + 7) / 8);
+    const int es = (int)sizeof(T);
+    if (d->d_n * es % 16 == 0 && d->d_r * es % 16 == 0)
+      chunk_spread_kernel<uint4><<<grid, 256, 0, st>>>(
+          a, t0, d->d_n * es / 16, d->d_r * es / 16, table, segs, reinterpret_cast<uint4*>(q_nope),
+          reinterpret_cast<uint4*>(q_rope), rot, state);
+    else
+      chunk_spread_kernel<T><<<grid, 256, 0, st>>>(a, t0, d->d_n, d->d_r, table, segs, q_nope,
+                                                   q_rope, rot, state);
     if (cudaGetLastError() != cudaSuccess) return MLA_ERR_CUDA;
     mla_status_t rc = mla_absorb_q(d, n, q_nope, q_rope, rot, a.delta, a.n_ver, w_uk, ws + l.q_abs, ms);
     if (rc != MLA_OK) return rc;
@@ -504,10 +537,16 @@ mla_status_t run_absorbed(const mla_dims_t* d, const ChunkArgs& a, const Layout&
                     a.max_pages, segs, a.max_segs, nullptr, nullptr, 0, a.q_pos + t0, o_lat, lse_t,
                     ws + l.ws, l.ws_bytes, ms);
     if (rc != MLA_OK) return rc;
-    rc = mla_out_proj(d, n, o_lat, w_uv, nullptr, vf, nullptr, ms);
-    if (rc != MLA_OK) return rc;
-    chunk_store_kernel<T><<<n, 256, 0, st>>>(t0, d->H, d->d_v, state, vf, lse_t,
-                                             static_cast<T*>(v), lse);
+    const T* wv = static_cast<const T*>(w_uv);
+    if (value_tc(d)) {
+      rc = mla_out_proj(d, n, o_lat, w_uv, nullptr, vf, nullptr, ms);
+      if (rc != MLA_OK) return rc;
+      chunk_store_kernel<T, false><<<grid, 256, 0, st>>>(t0, d->H, d->d_c, d->d_v, state, vf, wv,
+                                                         lse_t, static_cast<T*>(v), lse);
+    } else {
+      chunk_store_kernel<T, true><<<grid, 256, 0, st>>>(t0, d->H, d->d_c, d->d_v, state, o_lat, wv,
+                                                        lse_t, static_cast<T*>(v), lse);
+    }
     if (cudaGetLastError() != cudaSuccess) return MLA_ERR_CUDA;
   }
   return MLA_OK;

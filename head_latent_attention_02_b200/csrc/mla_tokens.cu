@@ -7,8 +7,8 @@
 // d_r / 2 pairs of a vector are cut into n_axes runs of sections[a] pairs; pair
 // i of run a turns by pos[a][token] * base^(-2i / d_r), i counted over the
 // whole vector, so that equal positions on every axis are the one-axis
-// rotation.  Angles, sines and cosines are computed in double (a float angle
-// at position 10^6 is off by 0.03 rad).
+// rotation.  Angles are computed in double (a float angle at position 10^6 is
+// off by 0.03 rad).
 //
 // Append: token i of sequence b becomes the cache row of logical row
 // row0[b] + i: [c * w / sqrt(mean(c^2) + eps) | R(pos) k] from the raw row
@@ -22,6 +22,7 @@
 
 #include <cmath>
 #include <cstdint>
+#include <type_traits>
 
 #include "mla.h"
 #include "common.cuh"
@@ -88,9 +89,24 @@ __device__ __forceinline__ void store8(float* p, const float (&v)[8]) {
   *reinterpret_cast<float4*>(p + 4) = make_float4(v[4], v[5], v[6], v[7]);
 }
 
-// The turned pair.  fp32 rows are computed in double and rounded once; bf16
-// rows in float, whose error (2^-23 of the pair's length) is far below the
-// rounding to bf16.
+// Cosine and sine of pos * theta.  kExact: in double throughout.  Otherwise the
+// angle is reduced to a fraction of a turn in double and the functions are
+// float, off by at most 2^-22 each: far below a rounding to bf16, and a short
+// chain where the double functions take 1 to 2 us, most of a small call.
+template <bool kExact>
+__device__ __forceinline__ void trig(double angle, double& c, double& s) {
+  sincos(angle, &s, &c);
+}
+template <>
+__device__ __forceinline__ void trig<false>(double angle, double& c, double& s) {
+  const double turns = angle * 0.15915494309189535;      // 1 / (2 pi)
+  float fs, fc;
+  sincospif((float)(2.0 * (turns - rint(turns))), &fs, &fc);
+  c = fc;
+  s = fs;
+}
+
+// The turned pair, in double (fp32 rows, rounded once) or in float.
 template <typename T> struct Trig;
 template <> struct Trig<float> { using type = double2; };
 template <> struct Trig<__nv_bfloat16> { using type = float2; };
@@ -132,7 +148,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_axes_kernel(const __grid_co
     for (int i = threadIdx.x; i < nt * ax.half; i += kRopeThreads) {
       const int t = i / ax.half, p = i % ax.half;
       double sn, c;
-      sincos((double)a.pos[(size_t)ax.axis_of(p) * a.n_tok + t0 + t] * ax.theta[p], &sn, &c);
+      trig<sizeof(T) == 4>((double)a.pos[(size_t)ax.axis_of(p) * a.n_tok + t0 + t] * ax.theta[p], c, sn);
       if (a.inverse) sn = -sn;
       cs[i].x = c;
       cs[i].y = sn;
@@ -221,17 +237,43 @@ __device__ __forceinline__ uint32_t code_of(float x, float scale, int bits) {
 }
 
 // A warp per token; lane l holds the latent groups of eight channels l, l + 32,
-// ... and the rotary pairs l, l + 32, ...  A is the type of the norm's sum and
-// product: float for rows of the storage type; double for a low-bit pool, where
-// one rounding of a value next to the border of two codes moves it by a
-// whole step.
-template <typename T, typename A>
+// ... (kHeld of them in registers, which covers 512 channels; wider rows are
+// read again) and the rotary pairs l, l + 32, ...  The token's row, its norm
+// weights and its first rotary pair are on their way before the owner search,
+// whose loads (starts, then row0 and the page id) form a chain of their own.
+// kLow: a packed pool.  What decides a code is computed in double, since one
+// rounding of a value next to the border of two codes moves it by a whole step;
+// rows of the storage type use float.
+constexpr int kHeld = 2;
+
+template <typename T, bool kLow>
 __global__ void __launch_bounds__(kTokThreads) append_tokens_kernel(
     const __grid_constant__ AppendTokArgs a, const __grid_constant__ Axes ax) {
+  using A = typename std::conditional<kLow, double, float>::type;
+  constexpr bool kExact = kLow || sizeof(T) == 4;
   const long long gw = (long long)blockIdx.x * (kTokThreads / 32) + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
   if (gw >= a.n_tok) return;
   const int t = (int)gw;
+  const T* src = static_cast<const T*>(a.kv) + (long long)t * a.kv_stride;
+  const int groups = (a.d_c + 7) / 8;
+  const bool vec_in = a.d_c % 8 == 0 && (reinterpret_cast<uintptr_t>(src) & 15) == 0;
+  const bool vec_w = a.norm_w && a.d_c % 8 == 0 && (reinterpret_cast<uintptr_t>(a.norm_w) & 15) == 0;
+  float v[kHeld][8], w[kHeld][8];
+#pragma unroll
+  for (int u = 0; u < kHeld; ++u) {
+    const int g = lane + 32 * u;
+    if (g >= groups) break;
+    load_group(src + 8 * g, vec_in, a.d_c - 8 * g, v[u]);
+    if (a.norm_w) load_group(a.norm_w + 8 * g, vec_w, a.d_c - 8 * g, w[u]);
+  }
+  const T* key = src + a.d_c;
+  const bool has_pair = lane < ax.half;
+  const float k0 = has_pair ? to_f(key[2 * lane]) : 0.f, k1 = has_pair ? to_f(key[2 * lane + 1]) : 0.f;
+  double2 cs = make_double2(1.0, 0.0);
+  if (has_pair)
+    trig<kExact>((double)a.pos[(size_t)ax.axis_of(lane) * a.n_tok + t] * ax.theta[lane], cs.x, cs.y);
+
   const int b = owner_of(a.tok_start, a.B, t, lane);
   if (b == -1) return;
   int page = -1, slot = 0;
@@ -246,59 +288,70 @@ __global__ void __launch_bounds__(kTokThreads) append_tokens_kernel(
     if (lane == 0) set_status(MLA_ERR_BAD_INDEX);
     return;
   }
-  const T* src = static_cast<const T*>(a.kv) + (long long)t * a.kv_stride;
-  const int groups = (a.d_c + 7) / 8;
-  const bool vec_in = a.d_c % 8 == 0 && (reinterpret_cast<uintptr_t>(src) & 15) == 0;
+
   A inv = (A)1;
   if (a.norm_w) {
     A ss = (A)0;
-    for (int g = lane; g < groups; g += 32) {
-      float v[8];
-      load_group(src + 8 * g, vec_in, a.d_c - 8 * g, v);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) ss += (A)v[j] * (A)v[j];
+    for (int u = 0; u < kHeld; ++u)
+      if (lane + 32 * u < groups) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) ss += (A)v[u][j] * (A)v[u][j];
+      }
+    for (int g = lane + 32 * kHeld; g < groups; g += 32) {
+      float x[8];
+      load_group(src + 8 * g, vec_in, a.d_c - 8 * g, x);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) ss += (A)x[j] * (A)x[j];
     }
 #pragma unroll
     for (int o = 16; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
     inv = (A)1 / sqrt(ss / (A)a.d_c + (A)a.eps);
   }
   const size_t row = (size_t)page * kPage + slot;
-  const int row_bytes = a.bits_c ? (a.d_c * a.bits_c + a.d_r * 4) / 8
-                                 : (a.d_c + a.d_r) * (int)sizeof(T);
+  const int row_bytes = kLow ? (a.d_c * a.bits_c + a.d_r * 4) / 8 : (a.d_c + a.d_r) * (int)sizeof(T);
   uint8_t* dst = static_cast<uint8_t*>(a.cache) + row * row_bytes;
   T* dst_t = reinterpret_cast<T*>(dst);
   const bool vec_out = a.d_c % 8 == 0 && (reinterpret_cast<uintptr_t>(dst) & 15) == 0;
-  for (int g = lane; g < groups; g += 32) {
+  auto store_group = [&](int g, float (&x)[8], const float (&wt)[8]) {
     const int n = min(8, a.d_c - 8 * g);
-    float v[8];
-    load_group(src + 8 * g, vec_in, n, v);
     if (a.norm_w) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (j < n) v[j] = (float)((A)v[j] * inv * (A)a.norm_w[8 * g + j]);
+      for (int j = 0; j < 8; ++j) x[j] = (float)((A)x[j] * inv * (A)wt[j]);
     }
-    if (!a.bits_c) {
+    if constexpr (!kLow) {
       if (vec_out) {
-        store8(dst_t + 8 * g, v);
+        store8(dst_t + 8 * g, x);
       } else {
-        for (int j = 0; j < n; ++j) dst_t[8 * g + j] = from_f<T>(v[j]);
+        for (int j = 0; j < n; ++j) dst_t[8 * g + j] = from_f<T>(x[j]);
       }
     } else {
       uint32_t word = 0;
 #pragma unroll
       for (int j = 0; j < 8; ++j)
-        word |= code_of(to_f(from_f<T>(v[j])), a.scale_c[8 * g + j], a.bits_c) << (a.bits_c * j);
+        word |= code_of(to_f(from_f<T>(x[j])), a.scale_c[8 * g + j], a.bits_c) << (a.bits_c * j);
       if (a.bits_c == 4) reinterpret_cast<uint32_t*>(dst)[g] = word;
       else reinterpret_cast<uint16_t*>(dst)[g] = (uint16_t)word;
     }
+  };
+#pragma unroll
+  for (int u = 0; u < kHeld; ++u)
+    if (lane + 32 * u < groups) store_group(lane + 32 * u, v[u], w[u]);
+  for (int g = lane + 32 * kHeld; g < groups; g += 32) {
+    float x[8], wt[8] = {};
+    load_group(src + 8 * g, vec_in, a.d_c - 8 * g, x);
+    if (a.norm_w) load_group(a.norm_w + 8 * g, vec_w, a.d_c - 8 * g, wt);
+    store_group(g, x, wt);
   }
-  const T* k = src + a.d_c;
   for (int i = lane; i < ax.half; i += 32) {
-    double2 cs;
-    sincos((double)a.pos[(size_t)ax.axis_of(i) * a.n_tok + t] * ax.theta[i], &cs.y, &cs.x);
-    float y0, y1;
-    turn(cs, to_f(k[2 * i]), to_f(k[2 * i + 1]), y0, y1);
-    if (!a.bits_c) {
+    float x0 = k0, x1 = k1, y0, y1;
+    if (i != lane) {
+      x0 = to_f(key[2 * i]);
+      x1 = to_f(key[2 * i + 1]);
+      trig<kExact>((double)a.pos[(size_t)ax.axis_of(i) * a.n_tok + t] * ax.theta[i], cs.x, cs.y);
+    }
+    turn(cs, x0, x1, y0, y1);
+    if constexpr (!kLow) {
       dst_t[a.d_c + 2 * i] = from_f<T>(y0);
       dst_t[a.d_c + 2 * i + 1] = from_f<T>(y1);
     } else {
@@ -441,11 +494,11 @@ extern "C" mla_status_t mla_append_tokens(const mla_dims_t* dims, int32_t B, int
   const unsigned blocks = (unsigned)(((long long)n_tok * 32 + kTokThreads - 1) / kTokThreads);
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   if (dims->dtype == MLA_BF16) {
-    if (low) append_tokens_kernel<__nv_bfloat16, double><<<blocks, kTokThreads, 0, st>>>(a, ax);
-    else append_tokens_kernel<__nv_bfloat16, float><<<blocks, kTokThreads, 0, st>>>(a, ax);
+    if (low) append_tokens_kernel<__nv_bfloat16, true><<<blocks, kTokThreads, 0, st>>>(a, ax);
+    else append_tokens_kernel<__nv_bfloat16, false><<<blocks, kTokThreads, 0, st>>>(a, ax);
   } else {
-    if (low) append_tokens_kernel<float, double><<<blocks, kTokThreads, 0, st>>>(a, ax);
-    else append_tokens_kernel<float, float><<<blocks, kTokThreads, 0, st>>>(a, ax);
+    if (low) append_tokens_kernel<float, true><<<blocks, kTokThreads, 0, st>>>(a, ax);
+    else append_tokens_kernel<float, false><<<blocks, kTokThreads, 0, st>>>(a, ax);
   }
   return cudaGetLastError() == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
 }
