@@ -3,21 +3,22 @@
 // accumulation in tensor memory; out = act(x W^T + bias) + residual
 // (mla_linear).
 //
-// Tile.  A cluster of two CTAs computes 256 x BN (cta_group::2, BN <= 256):
-// each CTA holds 128 rows of A and half of B's rows in shared memory, and the
-// pair's MMA reads both halves of B, so a CTA loads (128 + BN / 2) x 64
-// elements for every 128 x BN x 64 product -- at BN = 256 two thirds of what
-// two independent 128 x 256 tiles would take from L2, whose bandwidth is
-// what such tiles run into first.  Two accumulators (2 x 256 tensor-memory
-// columns) let the epilogue of one tile overlap the next one's products.
+// Tile.  A cluster of two CTAs computes 256 x (NB x BN) (cta_group::2, BN <= 256,
+// NB 1 or 2): each CTA holds 128 rows of A and half of each of B's NB column
+// blocks in shared memory, and the pair's MMA reads both halves.  What such
+// tiles run into first is the way from L2: at BN = 256 a CTA loads 64 bytes a
+// clock of MMA time with NB = 1, 48 with NB = 2.  NB = 1 has two accumulators
+// (2 x 256 tensor-memory columns), so that the epilogue of one tile overlaps
+// the next one's products; with NB = 2 both belong to one tile, and the next
+// tile's products start on a block as soon as it is drained.
 //
 // Roles per CTA (192 threads): warp 0 loads its CTA's operand halves by TMA
-// into a ring of stages (64 of K each); warp 1 of the first CTA issues the
-// MMAs of the pair; warps 2-5 read the accumulator (32 lanes each) and apply
-// the epilogue.
+// into a ring of stages; warp 1 of the first CTA issues the MMAs of the pair;
+// warps 2-5 read the accumulator (32 lanes each) and apply the epilogue.
 //
-// Work.  A pair takes whole tiles pair, pair + pairs, ... ; or (split) a
-// contiguous run of (tile, k-step) units, so that few tiles with a long K
+// Work.  Pairs take whole tiles for as many full rounds as there are; the
+// tiles that are left (fewer than pairs) are split along K into contiguous
+// runs of (tile, k-step) units of equal length, so that few tiles with a long K
 // still fill every SM.  A split tile's partial sums go to the workspace, a
 // slot of the pair that made them, and a second launch (mla_linear.cu) adds them in the
 // order of the pairs: the result does not depend on timing.
@@ -47,16 +48,17 @@ constexpr int kGroupM = 8;               // row tiles that share a pass over the
 enum Act : int { kNone = 0, kSilu = 1, kGelu = 2 };
 
 struct Params {
-  int k_steps, n_mt, n_nt, BN, stages;
+  int k_steps, n_mt, n_nt, BN, NB, stages;
   int P;                     // 64-K panels of a stage; > 1: three-axis maps over whole panels
-  int chunk;                 // split: units of a pair's run; 0: whole tiles
+  int rounds;                // whole tiles of each pair
+  int chunk;                 // units of a pair's run over the tiles that are left; 0: whole tiles
   // the M x N result; swapped: A holds W's rows and B x's
   int swapped, M, N, act;
   long long res_stride, out_stride;
   const float* bias;
   const __nv_bfloat16* residual;
   __nv_bfloat16* out;
-  float* partial;            // split: [2 x pairs][BN][256]
+  float* partial;            // split: [2 x pairs][NB x BN][256]
   int vec;                   // out and residual rows take 16-byte accesses
 };
 
@@ -73,22 +75,24 @@ struct Seg {
 
 // The i-th segment of a pair's work; false when there is none.
 __device__ __forceinline__ bool segment(const Params& p, int tiles, int pair, int pairs, int i, Seg* s) {
-  if (p.chunk) {
-    const long long U = (long long)tiles * p.k_steps;
-    const long long u0 = (long long)pair * p.chunk;
-    const long long u1 = u0 + p.chunk < U ? u0 + p.chunk : U;
-    const long long at = i == 0 ? u0 : (u0 / p.k_steps + i) * p.k_steps;
-    if (at >= u1) return false;
-    s->tile = (int)(at / p.k_steps);
-    s->k0 = (int)(at % p.k_steps);
-    s->k1 = (int)(u1 - at < p.k_steps - s->k0 ? s->k0 + (u1 - at) : p.k_steps);
-  } else {
+  if (i < p.rounds || !p.chunk) {
     const long long t = pair + (long long)i * pairs;
     if (t >= tiles) return false;
     s->tile = (int)t;
     s->k0 = 0;
     s->k1 = p.k_steps;
+    return true;
   }
+  i -= p.rounds;
+  const int base = p.rounds * pairs;
+  const long long U = (long long)(tiles - base) * p.k_steps;
+  const long long u0 = (long long)pair * p.chunk;
+  const long long u1 = u0 + p.chunk < U ? u0 + p.chunk : U;
+  const long long at = i == 0 ? u0 : (u0 / p.k_steps + i) * p.k_steps;
+  if (at >= u1) return false;
+  s->tile = base + (int)(at / p.k_steps);
+  s->k0 = (int)(at % p.k_steps);
+  s->k1 = (int)(u1 - at < p.k_steps - s->k0 ? s->k0 + (u1 - at) : p.k_steps);
   return true;
 }
 
@@ -104,35 +108,62 @@ __device__ __forceinline__ void tile_at(const Params& p, int t, int* mt, int* nt
 }
 
 __device__ __forceinline__ float activate(float x, int act) {
-  if (act == kSilu) return x / (1.f + __expf(-x));
+  if (act == kSilu) return __fdividef(x, 1.f + __expf(-x));
   if (act == kGelu) return 0.5f * x * (1.f + erff(x * 0.70710678118654752f));
   return x;
 }
 
-// Eight consecutive results of one row: out[m][n .. n + 8) = act(v + bias) +
-// residual.  Handles columns past N and rows that take no 16-byte access.
-__device__ __forceinline__ void finish8(const Params& p, int m, int n, const float* v) {
+// What the epilogue adds to 32 consecutive columns of one row: the bias and the
+// residual, loaded before the accumulator they meet is ready.
+struct Addend {
+  float bias[32];
+  uint4 res[4];
+};
+
+__device__ __forceinline__ void load_addend(const Params& p, int m, int n, Addend& d) {
+  const bool whole = p.vec && n + 32 <= p.N;
+  if (p.bias) {
+#pragma unroll
+    for (int j = 0; j < 32; ++j) d.bias[j] = n + j < p.N ? __ldg(p.bias + n + j) : 0.f;
+  }
+  if (p.residual && whole && m < p.M) {
+    const uint4* r = reinterpret_cast<const uint4*>(p.residual + (long long)m * p.res_stride + n);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) d.res[j] = r[j];
+  }
+}
+
+// 32 consecutive results of one row: out[m][n .. n + 32) = act(v + bias) +
+// residual.  Columns past N and rows that take no 16-byte access go one by one.
+__device__ __forceinline__ void finish32(const Params& p, int m, int n, float* v, const Addend& d) {
+  if (p.bias) {
+#pragma unroll
+    for (int j = 0; j < 32; ++j) v[j] += d.bias[j];
+  }
+  if (p.act != kNone) {
+#pragma unroll
+    for (int j = 0; j < 32; ++j) v[j] = activate(v[j], p.act);
+  }
+  if (m >= p.M) return;
   __nv_bfloat16* o = p.out + (long long)m * p.out_stride + n;
-  const __nv_bfloat16* r = p.residual ? p.residual + (long long)m * p.res_stride + n : nullptr;
-  float y[8];
-  if (p.vec && n + 8 <= p.N) {
+  if (p.vec && n + 32 <= p.N) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) y[j] = activate(v[j] + (p.bias ? __ldg(p.bias + n + j) : 0.f), p.act);
-    if (r) {
-      const uint4 u = *reinterpret_cast<const uint4*>(r);
-      y[0] += lo_f(u.x); y[1] += hi_f(u.x); y[2] += lo_f(u.y); y[3] += hi_f(u.y);
-      y[4] += lo_f(u.z); y[5] += hi_f(u.z); y[6] += lo_f(u.w); y[7] += hi_f(u.w);
-    }
-    *reinterpret_cast<uint4*>(o) =
-        make_uint4(pack2(y[0], y[1]), pack2(y[2], y[3]), pack2(y[4], y[5]), pack2(y[6], y[7]));
-  } else {
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (n + j < p.N) {
-        float t = activate(v[j] + (p.bias ? __ldg(p.bias + n + j) : 0.f), p.act);
-        if (r) t += __bfloat162float(r[j]);
-        o[j] = __float2bfloat16_rn(t);
+    for (int j = 0; j < 4; ++j) {
+      float* y = v + 8 * j;
+      if (p.residual) {
+        const uint4 u = d.res[j];
+        y[0] += lo_f(u.x); y[1] += hi_f(u.x); y[2] += lo_f(u.y); y[3] += hi_f(u.y);
+        y[4] += lo_f(u.z); y[5] += hi_f(u.z); y[6] += lo_f(u.w); y[7] += hi_f(u.w);
       }
+      reinterpret_cast<uint4*>(o)[j] =
+          make_uint4(pack2(y[0], y[1]), pack2(y[2], y[3]), pack2(y[4], y[5]), pack2(y[6], y[7]));
+    }
+  } else {
+    const __nv_bfloat16* r = p.residual ? p.residual + (long long)m * p.res_stride + n : nullptr;
+#pragma unroll
+    for (int j = 0; j < 32; ++j)
+      if (n + j < p.N)
+        o[j] = __float2bfloat16_rn(v[j] + (r ? __bfloat162float(r[j]) : 0.f));
   }
 }
 
@@ -149,7 +180,8 @@ gemm_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtensorMa
   const int P = p.P;
   const int b_panel = p.BN / 2 * 128;
   const int a_bytes = P * kABytes;
-  const int stage = a_bytes + P * b_panel;
+  const int NB = p.NB, b_bytes = P * b_panel;      // one column block of B
+  const int stage = a_bytes + NB * b_bytes;
   Bars* bar = reinterpret_cast<Bars*>(smem + S * stage);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
@@ -172,6 +204,8 @@ gemm_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtensorMa
   cluster_sync();
   tc_fence_after();
   const uint32_t tmem = bar->tmem_base;
+  // operands and workspace may come from the launch before this one
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const int tiles = p.n_mt * p.n_nt;
 
   if (warp == 0) {
@@ -184,7 +218,7 @@ gemm_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtensorMa
       for (int i = 0, n = 0; ok && segment(p, tiles, pair, pairs, i, &s); ++i) {
         int mt, nt;
         tile_at(p, s.tile, &mt, &nt);
-        const int ra = mt * kPairRows + (int)rank * kRows, rb = nt * p.BN + (int)rank * (p.BN / 2);
+        const int ra = mt * kPairRows + (int)rank * kRows, rb = nt * NB * p.BN + (int)rank * (p.BN / 2);
         for (int k = s.k0; k < s.k1; ++k, ++n) {
           const int slot = n % S;
           if (!mbar_wait(&bar->empty[slot], ((n / S) & 1) ^ 1)) {
@@ -198,10 +232,12 @@ gemm_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtensorMa
           uint8_t* dst = smem + slot * stage;
           if (P == 1) {
             tma_load_2d_pair(dst, &ta, fb, k * kKStep, ra);
-            tma_load_2d_pair(dst + a_bytes, &tb, fb, k * kKStep, rb);
+            for (int nb = 0; nb < NB; ++nb)
+              tma_load_2d_pair(dst + a_bytes + nb * b_bytes, &tb, fb, k * kKStep, rb + nb * p.BN);
           } else {
             tma_load_3d_pair(dst, &ta, fb, 0, ra, k * P);
-            tma_load_3d_pair(dst + a_bytes, &tb, fb, 0, rb, k * P);
+            for (int nb = 0; nb < NB; ++nb)
+              tma_load_3d_pair(dst + a_bytes + nb * b_bytes, &tb, fb, 0, rb + nb * p.BN, k * P);
           }
         }
       }
@@ -213,35 +249,40 @@ gemm_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtensorMa
       bool ok = true;
       Seg s;
       for (int i = 0, n = 0; ok && segment(p, tiles, pair, pairs, i, &s); ++i) {
-        const int ab = i & 1;
-        if (!__all_sync(0xffffffffu, mbar_wait(&bar->acc_empty[ab], ((i >> 1) & 1) ^ 1))) {
-          if (lane == 0) set_status(MLA_ERR_TIMEOUT);
-          break;
-        }
-        tc_fence_after();
-        for (int k = s.k0; k < s.k1; ++k, ++n) {
+        for (int k = s.k0; ok && k < s.k1; ++k, ++n) {
           const int slot = n % S;
           if (!__all_sync(0xffffffffu, mbar_wait(&bar->full[slot], (n / S) & 1))) {
             if (lane == 0) set_status(MLA_ERR_TIMEOUT);
             ok = false;
             break;
           }
-          tc_fence_after();
           // descriptors of the stage; a panel or a K step further is an addition
           // (16-byte units) that never leaves the address field
           const uint32_t a0 = smem_u32(smem + slot * stage);
-          uint64_t ad = smem_desc_sw128(a0, 16, 1024), bd = smem_desc_sw128(a0 + a_bytes, 16, 1024);
-          for (int pn = 0; pn < P; ++pn) {
+          for (int nb = 0; nb < NB; ++nb) {
+            const int ab = NB == 2 ? nb : i & 1;
+            if (k == s.k0 &&
+                !__all_sync(0xffffffffu,
+                            mbar_wait(&bar->acc_empty[ab], ((NB == 2 ? i : i >> 1) & 1) ^ 1))) {
+              if (lane == 0) set_status(MLA_ERR_TIMEOUT);
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            uint64_t ad = smem_desc_sw128(a0, 16, 1024);
+            uint64_t bd = smem_desc_sw128(a0 + a_bytes + nb * b_bytes, 16, 1024);
+            for (int pn = 0; pn < P; ++pn) {
 #pragma unroll
-            for (int ks = 0; ks < 4; ++ks)
-              mma_pair_bf16_ss_elect(tmem + ab * kMaxBN, ad + 2 * ks, bd + 2 * ks, idesc,
-                                     (k == s.k0 && (pn | ks) == 0) ? 0u : 1u);
-            ad += kABytes >> 4;
-            bd += b_panel >> 4;
+              for (int ks = 0; ks < 4; ++ks)
+                mma_pair_bf16_ss_elect(tmem + ab * kMaxBN, ad + 2 * ks, bd + 2 * ks, idesc,
+                                       (k == s.k0 && (pn | ks) == 0) ? 0u : 1u);
+              ad += kABytes >> 4;
+              bd += b_panel >> 4;
+            }
           }
           mma_pair_commit_both_elect(&bar->empty[slot]);
         }
-        if (ok) mma_pair_commit_both_elect(&bar->acc_full[ab]);
+        if (ok) mma_pair_commit_both_elect(&bar->acc_full[NB == 2 ? 0 : i & 1]);
       }
     }
   } else {
@@ -250,62 +291,71 @@ gemm_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtensorMa
     const int row = (int)rank * kRows + quad * 32 + lane;      // row of the pair's tile
     Seg s;
     for (int i = 0; segment(p, tiles, pair, pairs, i, &s); ++i) {
-      const int ab = i & 1;
-      const uint32_t acc = tmem + ab * kMaxBN + ((uint32_t)(quad * 32) << 16);
       int mt, nt;
       tile_at(p, s.tile, &mt, &nt);
-      if (!__all_sync(0xffffffffu, mbar_wait(&bar->acc_full[ab], (i >> 1) & 1))) {
+      const bool part = s.k1 - s.k0 < p.k_steps;
+      const int m = mt * kPairRows + row;          // row of A
+      const int n0 = nt * NB * p.BN;               // first row of B
+      Addend add;
+      if (!part && !p.swapped) load_addend(p, m, n0, add);
+      const int full = NB == 2 ? 0 : i & 1;
+      if (!__all_sync(0xffffffffu,
+                      mbar_wait(&bar->acc_full[full], (NB == 2 ? i : i >> 1) & 1))) {
         if (lane == 0) set_status(MLA_ERR_TIMEOUT);
         break;
       }
       tc_fence_after();
-      if (s.k1 - s.k0 < p.k_steps) {
-        // part of a tile: the pair's first slot holds a segment that starts
-        // its run, the second one that ends it
-        const bool first = (long long)s.tile * p.k_steps + s.k0 == (long long)pair * p.chunk;
-        float* o = p.partial + ((long long)(2 * pair + (first ? 0 : 1)) * p.BN) * kPairRows + row;
+      for (int nb = 0; nb < NB; ++nb) {
+        const int ab = NB == 2 ? nb : full;
+        const uint32_t acc = tmem + ab * kMaxBN + ((uint32_t)(quad * 32) << 16);
+        const int c0 = nb * p.BN;                  // column of the tile
+        if (part) {
+          // the pair's first slot holds a segment that starts its run, the
+          // second one that ends it
+          const bool first = (long long)(s.tile - p.rounds * pairs) * p.k_steps + s.k0 ==
+                             (long long)pair * p.chunk;
+          float* o = p.partial +
+                     ((long long)(2 * pair + (first ? 0 : 1)) * NB * p.BN + c0) * kPairRows + row;
 #pragma unroll 1
-        for (int c = 0; c < p.BN; c += 32) {
-          float v[32];
-          tmem_ld32_sync(acc + c, v);
+          for (int c = 0; c < p.BN; c += 32) {
+            float v[32];
+            tmem_ld32_sync(acc + c, v);
 #pragma unroll
-          for (int j = 0; j < 32; ++j) o[(long long)(c + j) * kPairRows] = v[j];
-        }
-      } else if (p.swapped) {
-        const int n = mt * kPairRows + row;        // feature of this lane
-        const float bias = p.bias && n < p.N ? __ldg(p.bias + n) : 0.f;
+            for (int j = 0; j < 32; ++j) o[(long long)(c + j) * kPairRows] = v[j];
+          }
+        } else if (p.swapped) {
+          const float bias = p.bias && m < p.N ? __ldg(p.bias + m) : 0.f;   // feature of this lane
 #pragma unroll 1
-        for (int c = 0; c < p.BN; c += 32) {
-          const int m0 = nt * p.BN + c;
-          if (m0 >= p.M) break;
-          float v[32];
-          tmem_ld32_sync(acc + c, v);
+          for (int c = 0; c < p.BN; c += 32) {
+            const int t0 = n0 + c0 + c;
+            if (t0 >= p.M) break;
+            float v[32];
+            tmem_ld32_sync(acc + c, v);
 #pragma unroll
-          for (int j = 0; j < 32; ++j) {
-            if (n >= p.N || m0 + j >= p.M) continue;
-            float y = activate(v[j] + bias, p.act);
-            if (p.residual) y += __bfloat162float(p.residual[(long long)(m0 + j) * p.res_stride + n]);
-            p.out[(long long)(m0 + j) * p.out_stride + n] = __float2bfloat16_rn(y);
+            for (int j = 0; j < 32; ++j) {
+              if (m >= p.N || t0 + j >= p.M) continue;
+              float y = activate(v[j] + bias, p.act);
+              if (p.residual)
+                y += __bfloat162float(p.residual[(long long)(t0 + j) * p.res_stride + m]);
+              p.out[(long long)(t0 + j) * p.out_stride + m] = __float2bfloat16_rn(y);
+            }
+          }
+        } else {
+#pragma unroll 1
+          for (int c = 0; c < p.BN; c += 32) {
+            const int n = n0 + c0 + c;
+            if (n >= p.N) break;
+            float v[32];
+            tmem_ld32_sync(acc + c, v);
+            finish32(p, m, n, v, add);
+            // the next 32 columns'; past this block they lie in the next one
+            if (n + 32 < p.N && c0 + c + 32 < NB * p.BN) load_addend(p, m, n + 32, add);
           }
         }
-      } else {
-        const int m = mt * kPairRows + row;
-#pragma unroll 1
-        for (int c = 0; c < p.BN; c += 32) {
-          const int n0 = nt * p.BN + c;
-          if (n0 >= p.N) break;
-          float v[32];
-          tmem_ld32_sync(acc + c, v);
-          if (m < p.M) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-              if (n0 + 8 * j < p.N) finish8(p, m, n0 + 8 * j, v + 8 * j);
-          }
-        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_pair(mapa(smem_u32(&bar->acc_empty[ab]), 0));
       }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive_pair(mapa(smem_u32(&bar->acc_empty[ab]), 0));
     }
   }
 

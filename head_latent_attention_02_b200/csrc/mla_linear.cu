@@ -116,50 +116,62 @@ void launch_simt(const SimtArgs& a, cudaStream_t st) {
 
 // ------------------------------------------------------------ tensor cores
 // Sum of a split tile's partials in the order of the pairs, and the epilogue.
-// grid (tiles, BN / 8); 256 threads, one row of the tile each, eight columns.
-__global__ void __launch_bounds__(256) linear_finish_kernel(const __grid_constant__ gm::Params p) {
+// grid (tiles that were split, columns / 8); 256 threads, one row of the tile
+// each, eight columns.
+__global__ void __launch_bounds__(256) linear_finish_kernel(const __grid_constant__ gm::Params p,
+                                                            int base) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int t = blockIdx.x, c0 = blockIdx.y * 8, row = threadIdx.x;
+  const int t = blockIdx.x, c0 = blockIdx.y * 8, row = threadIdx.x, wide = p.NB * p.BN;
   const long long u0 = (long long)t * p.k_steps;
   const int g0 = (int)(u0 / p.chunk), g1 = (int)((u0 + p.k_steps - 1) / p.chunk);
   if (g0 == g1) return;                    // one pair made the whole tile
   int mt, nt;
-  gm::tile_at(p, t, &mt, &nt);
-  const int a = mt * gm::kPairRows + row, b = nt * p.BN + c0;    // operand rows
+  gm::tile_at(p, base + t, &mt, &nt);
+  const int a = mt * gm::kPairRows + row, b = nt * wide + c0;    // operand rows
   if (p.swapped ? (a >= p.N || b >= p.M) : (a >= p.M || b >= p.N)) return;
   float v[8] = {};
 #pragma unroll 4
   for (int g = g0; g <= g1; ++g) {
     const int second = (long long)g * p.chunk < u0 ? 1 : 0;   // the tile starts inside the run
-    const float* s = p.partial + ((long long)(2 * g + second) * p.BN + c0) * gm::kPairRows + row;
+    const float* s = p.partial + ((long long)(2 * g + second) * wide + c0) * gm::kPairRows + row;
 #pragma unroll
     for (int j = 0; j < 8; ++j) v[j] += s[(long long)j * gm::kPairRows];
   }
-  if (!p.swapped) {
-    gm::finish8(p, a, b, v);
-    return;
-  }
-  const float bias = p.bias ? __ldg(p.bias + a) : 0.f;
+  const bool vec = !p.swapped && p.vec && b + 8 <= p.N;
+  const uint4* res = vec && p.residual ? reinterpret_cast<const uint4*>(
+                                             p.residual + (long long)a * p.res_stride + b)
+                                       : nullptr;
+  const uint4 u = res ? *res : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
-    if (b + j >= p.M) break;
-    float y = gm::activate(v[j] + bias, p.act);
-    if (p.residual) y += __bfloat162float(p.residual[(long long)(b + j) * p.res_stride + a]);
-    p.out[(long long)(b + j) * p.out_stride + a] = __float2bfloat16_rn(y);
+    const int m = p.swapped ? b + j : a, n = p.swapped ? a : b + j;
+    if (m >= p.M || n >= p.N) break;
+    v[j] = gm::activate(v[j] + (p.bias ? __ldg(p.bias + n) : 0.f), p.act);
+    if (vec) {
+      const uint32_t w = j < 2 ? u.x : j < 4 ? u.y : j < 6 ? u.z : u.w;
+      v[j] += j & 1 ? hi_f(w) : lo_f(w);
+    } else {
+      if (p.residual) v[j] += __bfloat162float(p.residual[(long long)m * p.res_stride + n]);
+      p.out[(long long)m * p.out_stride + n] = __float2bfloat16_rn(v[j]);
+    }
   }
+  if (vec)
+    *reinterpret_cast<uint4*>(p.out + (long long)a * p.out_stride + b) =
+        make_uint4(pack2(v[0], v[1]), pack2(v[2], v[3]), pack2(v[4], v[5]), pack2(v[6], v[7]));
 }
 
 struct TilePlan {
-  int swapped, BN, n_mt, n_nt, P, k_steps, stages, chunk, grid;
+  int swapped, BN, NB, n_mt, n_nt, P, k_steps, stages, rounds, chunk, grid;
   size_t ws;
 };
 
-// Which operand takes the tile's 256 rows, how wide the tile is, and whether K
-// is split.  Few rows of x: W takes the rows (its stream is what the call
-// costs) and the tile is as wide as x is high, in runs of units of equal
-// length.  Otherwise the width with the least estimated time: a pair's step
-// costs the larger of the MMA (2 BN clocks) and its operand loads at about 60
-// bytes a clock and SM.
+// Which operand takes the tile's 256 rows, how wide the tile is, and how much
+// of the work is split along K.  Few rows of x: W takes the rows (its stream is
+// what the call costs) and the tile is as wide as x is high.  Otherwise the
+// shape with the least estimated time: a pair's step costs the larger of its
+// MMAs (2 NB BN clocks) and its operand loads at about 50 bytes a clock and SM;
+// a split costs a second launch and the partial sums' trip through memory; two
+// column blocks cost an epilogue that little overlaps.
 TilePlan plan_tiles(int M, int N, int K, int sms) {
   TilePlan t = {};
   const int pairs = sms / 2 > 0 ? sms / 2 : 1;
@@ -171,30 +183,36 @@ TilePlan plan_tiles(int M, int N, int K, int sms) {
   double best = 0;
   const int rows = t.swapped ? N : M, cols = t.swapped ? M : N;
   t.n_mt = (rows + gm::kPairRows - 1) / gm::kPairRows;
-  for (int bn = 32; bn <= gm::kMaxBN; bn += 32) {
-    if (t.swapped ? (bn != (cols + 31) / 32 * 32) : (bn < 64 && cols > bn)) continue;
-    const long long n_nt = (cols + bn - 1) / bn, tiles = (long long)t.n_mt * n_nt;
-    const double load = (gm::kRows + bn / 2) * 128 / 60.0;
-    const double step = t.P * (2.0 * bn > load ? 2.0 * bn : load);
-    const long long units = tiles * t.k_steps;
-    // a run of at least eight steps, so that a partial sum is worth its trip
-    long long run = (units + pairs - 1) / pairs;
-    if (run * t.P < 8) run = (8 + t.P - 1) / t.P < t.k_steps ? (8 + t.P - 1) / t.P : t.k_steps;
-    const double whole = (double)((tiles + pairs - 1) / pairs) * t.k_steps * step;
-    const double split = (double)run * step + 6000;
-    const bool use_split = split < whole;
-    const double cost = (use_split ? split : whole) + 4.0 * bn;
-    if (best == 0 || cost < best) {
-      best = cost;
-      t.BN = bn;
-      t.n_nt = (int)n_nt;
-      t.chunk = use_split ? (int)run : 0;
-      const long long g = use_split ? (units + run - 1) / run : (tiles < pairs ? tiles : pairs);
-      t.grid = 2 * (int)g;
-      t.ws = use_split ? (size_t)(2 * g) * bn * gm::kPairRows * sizeof(float) : 0;
+  for (int nb = 1; nb <= (t.swapped ? 1 : 2); ++nb)
+    for (int bn = 32; bn <= gm::kMaxBN; bn += 32) {
+      if (t.swapped ? (bn != (cols + 31) / 32 * 32) : (bn < 64 && cols > bn)) continue;
+      if (nb == 2 && bn < 192) continue;
+      const long long n_nt = (cols + nb * bn - 1) / (nb * bn), tiles = (long long)t.n_mt * n_nt;
+      const double load = (gm::kRows + nb * bn / 2) * 128 / 50.0, mma = 2.0 * nb * bn;
+      const double step = t.P * (mma > load ? mma : load), tile = t.k_steps * step;
+      const long long rounds = tiles / pairs, left = tiles - rounds * pairs;
+      // a run of at least eight steps of 64, so that a partial sum is worth its trip
+      long long run = (left * t.k_steps + pairs - 1) / pairs;
+      const long long least = (8 + t.P - 1) / t.P < t.k_steps ? (8 + t.P - 1) / t.P : t.k_steps;
+      if (run < least) run = least;
+      // up to two partial sums a pair, written and read at about 1600 bytes a clock
+      const double trip = 6000 + 3.0 * pairs * nb * bn * gm::kPairRows * sizeof(float) / 1600.0;
+      const bool split = left > 0 && run * step + trip < tile;
+      const double drain = nb == 2 ? 8.0 * nb * bn * (rounds + 1) : 4.0 * bn;
+      const double cost = rounds * tile + (left ? (split ? run * step + trip : tile) : 0) + drain;
+      if (best == 0 || cost < best) {
+        best = cost;
+        t.BN = bn;
+        t.NB = nb;
+        t.n_nt = (int)n_nt;
+        t.rounds = (int)rounds;
+        t.chunk = split ? (int)run : 0;
+        const long long used = split ? (left * t.k_steps + run - 1) / run : left;
+        t.grid = 2 * (int)(rounds ? pairs : used);
+        t.ws = split ? (size_t)(2 * used) * nb * bn * gm::kPairRows * sizeof(float) : 0;
+      }
     }
-  }
-  const int stage = t.P * (gm::kABytes + t.BN / 2 * 128);
+  const int stage = t.P * (gm::kABytes + t.NB * t.BN / 2 * 128);
   t.stages = (gm::kSmemMax - gm::kBarBytes - 1024) / stage;
   if (t.stages > gm::kMaxStages) t.stages = gm::kMaxStages;
   return t;
@@ -267,6 +285,8 @@ extern "C" mla_status_t mla_linear(int32_t dtype, int32_t M, int32_t N, int32_t 
   p.n_mt = t.n_mt;
   p.n_nt = t.n_nt;
   p.BN = t.BN;
+  p.NB = t.NB;
+  p.rounds = t.rounds;
   p.stages = t.stages;
   p.P = t.P;
   p.chunk = t.chunk;
@@ -292,16 +312,17 @@ extern "C" mla_status_t mla_linear(int32_t dtype, int32_t M, int32_t N, int32_t 
                                : map_panels(&ta, a, K, ar, as, gm::kRows, t.P) &&
                                      map_panels(&tb, b, K, br, bs, t.BN / 2, t.P);
   if (!mapped) return MLA_ERR_CUDA;
-  const int smem = t.stages * t.P * (gm::kABytes + t.BN / 2 * 128) + gm::kBarBytes + 1024;
+  const int smem = t.stages * t.P * (gm::kABytes + t.NB * t.BN / 2 * 128) + gm::kBarBytes + 1024;
   if (cudaFuncSetAttribute(gm::gemm_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            gm::kSmemMax) != cudaSuccess)
     return MLA_ERR_CUDA;
   if (launch_dependent(gm::gemm_kernel, dim3(t.grid), dim3(gm::kThreads), smem, st,
-                       false, p, ta, tb) != cudaSuccess)
+                       true, p, ta, tb) != cudaSuccess)
     return MLA_ERR_CUDA;
+  const int base = t.rounds * (t.grid / 2);
   if (t.chunk &&
-      launch_dependent(linear_finish_kernel, dim3(t.n_mt * t.n_nt, t.BN / 8), dim3(256), 0, st,
-                       true, p) != cudaSuccess)
+      launch_dependent(linear_finish_kernel, dim3(t.n_mt * t.n_nt - base, t.NB * t.BN / 8), dim3(256),
+                       0, st, true, p, base) != cudaSuccess)
     return MLA_ERR_CUDA;
   return MLA_OK;
 }

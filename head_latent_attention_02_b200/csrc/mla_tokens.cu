@@ -33,7 +33,7 @@ namespace {
 constexpr int kMaxPairs = 64;       // d_r <= 128
 constexpr int kMaxAxes = 4;
 constexpr int kRopeThreads = 256;
-constexpr int kRopeUnroll = 4;
+constexpr int kRopeUnroll = 8;      // 16-byte loads a thread has on their way
 constexpr int kRopeTokens = 8;      // tokens of a block at most
 constexpr int kTokThreads = 256;    // append: a warp per token
 
@@ -69,16 +69,24 @@ bool make_axes(const mla_dims_t* d, int n_axes, const int32_t* sections, Axes* a
   return sum == ax->half;
 }
 
-// Eight consecutive elements as floats; 16-byte accesses.
-__device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&v)[8]) {
-  const uint4 u = *reinterpret_cast<const uint4*>(p);
+// Eight consecutive elements, in 16-byte pieces, and as floats.
+struct alignas(16) Raw8f {
+  float4 lo, hi;
+};
+template <typename T> struct RawGroup;
+template <> struct RawGroup<__nv_bfloat16> { using type = uint4; };
+template <> struct RawGroup<float> { using type = Raw8f; };
+__device__ __forceinline__ void open_group(const uint4& u, float (&v)[8]) {
   v[0] = lo_f(u.x); v[1] = hi_f(u.x); v[2] = lo_f(u.y); v[3] = hi_f(u.y);
   v[4] = lo_f(u.z); v[5] = hi_f(u.z); v[6] = lo_f(u.w); v[7] = hi_f(u.w);
 }
-__device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
-  const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
-  v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-  v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+__device__ __forceinline__ void open_group(const Raw8f& u, float (&v)[8]) {
+  v[0] = u.lo.x; v[1] = u.lo.y; v[2] = u.lo.z; v[3] = u.lo.w;
+  v[4] = u.hi.x; v[5] = u.hi.y; v[6] = u.hi.z; v[7] = u.hi.w;
+}
+template <typename T>
+__device__ __forceinline__ void load8(const T* p, float (&v)[8]) {
+  open_group(*reinterpret_cast<const typename RawGroup<T>::type*>(p), v);
 }
 __device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&v)[8]) {
   *reinterpret_cast<uint4*>(p) =
@@ -155,37 +163,58 @@ __global__ void __launch_bounds__(kRopeThreads) rope_axes_kernel(const __grid_co
     }
     __syncthreads();
   };
+  // A thread's items are `step` apart; their token, head and pair advance by
+  // constant amounts with a carry, so that the divisions happen once.
+  int p = threadIdx.x % per, h = threadIdx.x / per % nh, t = threadIdx.x / per / nh;
+  const int dp = kRopeThreads % per, dh = kRopeThreads / per % nh, dt = kRopeThreads / per / nh;
+  auto advance = [&] {
+    p += dp;
+    h += dh;
+    t += dt;
+    if (p >= per) {
+      p -= per;
+      ++h;
+    }
+    if (h >= nh) {
+      h -= nh;
+      ++t;
+    }
+  };
   if constexpr (kVec) {
-    for (int base = 0; base < n; base += kRopeThreads * kRopeUnroll) {
-      float v[kRopeUnroll][8];
-      int t[kRopeUnroll], h[kRopeUnroll], p0[kRopeUnroll];
+    using Raw = typename RawGroup<T>::type;
+    for (int base = threadIdx.x; base < n || base == threadIdx.x; base += kRopeThreads * kRopeUnroll) {
+      Raw raw[kRopeUnroll];
+      const int p0 = p, h0_ = h, t0_ = t;
 #pragma unroll
       for (int u = 0; u < kRopeUnroll; ++u) {
-        const int i = base + u * kRopeThreads + threadIdx.x;
-        p0[u] = i % per * 4;
-        h[u] = i / per % nh;
-        t[u] = i / per / nh;
-        if (i < n) load8(x + t[u] * a.x_tok + h[u] * a.x_head + p0[u] * 2, v[u]);
+        if (base + u * kRopeThreads < n)
+          raw[u] = *reinterpret_cast<const Raw*>(x + t * a.x_tok + h * a.x_head + p * 8);
+        advance();
       }
-      if (base == 0) table();
+      if (base == threadIdx.x) table();
+      p = p0;
+      h = h0_;
+      t = t0_;
 #pragma unroll
       for (int u = 0; u < kRopeUnroll; ++u) {
-        if (base + u * kRopeThreads + (int)threadIdx.x >= n) break;
-        const CS* c = cs + t[u] * ax.half + p0[u];
-        float y[8];
+        if (base + u * kRopeThreads < n) {
+          const CS* c = cs + t * ax.half + p * 4;
+          float v[8], y[8];
+          open_group(raw[u], v);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) turn(c[j], v[u][2 * j], v[u][2 * j + 1], y[2 * j], y[2 * j + 1]);
-        store8(out + t[u] * a.o_tok + h[u] * a.o_head + p0[u] * 2, y);
+          for (int j = 0; j < 4; ++j) turn(c[j], v[2 * j], v[2 * j + 1], y[2 * j], y[2 * j + 1]);
+          store8(out + t * a.o_tok + h * a.o_head + p * 8, y);
+        }
+        advance();
       }
     }
   } else {
     table();
-    for (int i = threadIdx.x; i < n; i += kRopeThreads) {
-      const int p = i % per, h = i / per % nh, t = i / per / nh;
-      const T* s = x + t * a.x_tok + h * a.x_head + 2 * p;
+    for (int i = threadIdx.x; i < n; i += kRopeThreads, advance()) {
+      const T* src = x + t * a.x_tok + h * a.x_head + 2 * p;
       T* d = out + t * a.o_tok + h * a.o_head + 2 * p;
       float y0, y1;
-      turn(cs[t * ax.half + p], to_f(s[0]), to_f(s[1]), y0, y1);
+      turn(cs[t * ax.half + p], to_f(src[0]), to_f(src[1]), y0, y1);
       d[0] = from_f<T>(y0);
       d[1] = from_f<T>(y1);
     }
