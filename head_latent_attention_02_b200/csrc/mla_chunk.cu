@@ -1,14 +1,15 @@
 // mla_chunk.cu -- attention of a ragged chunk of new tokens over the paged
 // latent cache (mla_chunk_attn): host side, planner and the small kernels.
 //
-// Two routes compute the same result, chosen by a rule on sizes (chunk_route):
+// Three routes compute the same result, chosen by a rule on sizes (chunk_route):
 //   expanded   bf16 rows of 512 + 64, 128-wide heads: keys and values are
 //              expanded once per call into the workspace (expand_tc.cuh), the
 //              rotary keys moved to their request positions, and the direct
 //              form attends over them (chunk_tc.cuh).  For chunks.
-//   absorbed   everything else -- few tokens, fp32, other widths: each token is
-//              a one-token sequence of mla_decode between mla_absorb_q and the
-//              value expansion of mla_out_proj.
+//   absorbed   few tokens over those rows: each token is a one-token sequence
+//              of mla_decode between mla_absorb_q and the value expansion of
+//              mla_out_proj.
+//   generic    fp32 and other widths: one kernel on the CUDA cores.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -333,6 +334,153 @@ __global__ void __launch_bounds__(256) chunk_store_kernel(int t0, int H, int d_c
   }
 }
 
+// ------------------------------------------------------------ generic widths
+// One block per (token, head), any widths, fp32 arithmetic: the head's absorbed
+// query W_UK[h]^T q_nope and its rotary part turned by -delta[version] (in
+// shared memory, not rounded), an online softmax over chunks of 128 rows -- a
+// thread per row for the scores; (row group, channel) for the weighted sum,
+// so that narrow latents keep all threads at work -- and the value expansion.
+// A masked row is not read.  Bound by the latency of its chain (about 2 us a
+// chunk of rows).
+constexpr int kGenThreads = 128;
+
+int generic_groups(int d_c) {
+  int wide = 1;
+  while (wide < d_c && wide < kGenThreads) wide *= 2;
+  return kGenThreads / wide;
+}
+
+size_t generic_smem(const mla_dims_t* d, int n_ver) {
+  return sizeof(float) * ((size_t)n_ver * (d->d_c + d->d_r) + d->d_n + d->d_r +
+                          (size_t)generic_groups(d->d_c) * d->d_c + kGenThreads + 8) +
+         sizeof(int) * kGenThreads;
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kGenThreads) chunk_generic_kernel(
+    const __grid_constant__ ChunkArgs a, int d_c, int groups, float scale, const T* w_uk,
+    const T* w_uv, T* v, float* lse) {
+  extern __shared__ float sm_gen[];
+  const int t = blockIdx.x, h = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int row = d_c + a.d_r;
+  float* qa = sm_gen;                        // [n_ver][row]
+  float* qn = qa + a.n_ver * row;            // [d_n + d_r]
+  float* acc = qn + a.d_n + a.d_r;           // [groups][d_c]
+  float* pw = acc + groups * d_c;            // [128] weights of the chunk
+  float* red = pw + kGenThreads;             // [8]
+  int* prow = reinterpret_cast<int*>(red + 8);   // [128] cache rows, -1: none
+  __shared__ int s_b, s_bad;
+  if (tid == 0) {
+    s_b = -1;
+    s_bad = 0;
+  }
+  const T* q = static_cast<const T*>(a.q) + ((size_t)t * a.H + h) * (a.d_n + a.d_r);
+  for (int k = tid; k < a.d_n + a.d_r; k += kGenThreads) qn[k] = to_f(q[k]);
+  for (int k = tid; k < groups * d_c; k += kGenThreads) acc[k] = 0.f;
+  __syncthreads();
+  for (int b = tid; b < a.B; b += kGenThreads) {
+    const int lo = a.tok_start[b], hi = a.tok_start[b + 1];
+    if (lo < 0 || hi < lo || hi > a.n_tok) set_status(MLA_ERR_BAD_INDEX);
+    else if (lo <= t && t < hi) atomicMax(&s_b, b);
+  }
+  for (int c = tid; c < d_c; c += kGenThreads) {
+    const T* w = w_uk + (size_t)h * a.d_n * d_c + c;
+    float s = 0.f;
+    for (int k = 0; k < a.d_n; ++k) s = fmaf(to_f(w[(size_t)k * d_c]), qn[k], s);
+    for (int u = 0; u < a.n_ver; ++u) qa[u * row + c] = s;
+  }
+  for (int i = tid; i < a.n_ver * (a.d_r / 2); i += kGenThreads) {
+    const int u = i / (a.d_r / 2), k = i % (a.d_r / 2);
+    const float x0 = qn[a.d_n + 2 * k], x1 = qn[a.d_n + 2 * k + 1];
+    double sn = 0.0, cs = 1.0;
+    if (a.delta[u] != 0) sincos(-(double)a.delta[u] * pow(a.rope_base, -2.0 * k / a.d_r), &sn, &cs);
+    qa[u * row + d_c + 2 * k] = (float)(x0 * cs - x1 * sn);
+    qa[u * row + d_c + 2 * k + 1] = (float)(x0 * sn + x1 * cs);
+  }
+  __syncthreads();
+  const int b = s_b;
+  if (b < 0) return;
+  const int np = sequence_pages(a, b);
+  PageEntry e;
+  if (np < 0 && tid == 0) s_bad = 1;
+  for (int k = tid; k < np; k += kGenThreads)
+    if (!page_at(a, b, k, &e)) s_bad = 1;
+  __syncthreads();
+  const size_t at = (size_t)t * a.H + h;
+  if (s_bad) {
+    if (tid == 0) set_status(MLA_ERR_BAD_INDEX);
+    for (int d = tid; d < a.d_v; d += kGenThreads) v[at * a.d_v + d] = from_f<T>(kNaN);
+    if (lse && tid == 0) lse[at] = kNaN;
+    return;
+  }
+  const T* cache = static_cast<const T*>(a.cache);
+  const int qp = a.q_pos[t];
+  const int wide = kGenThreads / groups;
+  float m = kNegInf, l = 0.f;
+  for (int base = 0; base < np * kPage; base += kGenThreads) {
+    const int i = base + tid;
+    float s = kNegInf;
+    int phys = -1;
+    if (i < np * kPage && page_at(a, b, i / kPage, &e) && i % kPage < e.n &&
+        (long long)e.kpos + i % kPage <= qp) {
+      phys = e.row + i % kPage;
+      const T* r = cache + (size_t)phys * row;
+      const float* x = qa + e.ver * row;
+      float d0 = 0.f, d1 = 0.f;
+      int k = 0;
+#pragma unroll 4
+      for (; k + 1 < row; k += 2) {
+        d0 = fmaf(x[k], to_f(r[k]), d0);
+        d1 = fmaf(x[k + 1], to_f(r[k + 1]), d1);
+      }
+      if (k < row) d0 = fmaf(x[k], to_f(r[k]), d0);
+      s = (d0 + d1) * scale;
+    }
+    // the chunk's maximum and sum; a NaN score makes the sum NaN
+    float mx = s;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+    if (lane == 0) red[warp] = mx;
+    __syncthreads();
+    const float m_new = fmaxf(m, fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3])));
+    const float p = phys < 0 ? 0.f : expf(s - (m_new == kNegInf ? 0.f : m_new));
+    pw[tid] = p;
+    prow[tid] = phys;
+    float sum = p;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (lane == 0) red[4 + warp] = sum;
+    __syncthreads();
+    const float f = m == kNegInf ? 0.f : expf(m - m_new);
+    l = l * f + ((red[4] + red[5]) + (red[6] + red[7]));
+    m = m_new;
+    for (int c = tid % wide; c < d_c; c += wide) {
+      float o = acc[(tid / wide) * d_c + c] * f;
+#pragma unroll 4
+      for (int k = tid / wide; k < kGenThreads; k += groups)
+        if (prow[k] >= 0) o = fmaf(pw[k], to_f(cache[(size_t)prow[k] * row + c]), o);
+      acc[(tid / wide) * d_c + c] = o;
+    }
+    __syncthreads();
+  }
+  const bool none = l == 0.f;
+  for (int c = tid; c < d_c; c += kGenThreads) {
+    float o = 0.f;
+    for (int g = 0; g < groups; ++g) o += acc[g * d_c + c];
+    acc[c] = none ? 0.f : o / l;
+  }
+  __syncthreads();
+  for (int d = warp; d < a.d_v; d += kGenThreads / 32) {
+    const T* w = w_uv + ((size_t)h * a.d_v + d) * d_c;
+    float s = 0.f;
+    for (int c = lane; c < d_c; c += 32) s = fmaf(to_f(w[c]), acc[c], s);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    if (lane == 0) v[at * a.d_v + d] = from_f<T>(s);
+  }
+  if (lse && tid == 0) lse[at] = none ? kNegInf : m + logf(l);
+}
+
 // ------------------------------------------------------------ host
 size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
 
@@ -346,8 +494,13 @@ bool value_tc(const mla_dims_t* d) {
   return d->dtype == MLA_BF16 && d->d_v % 128 == 0 && d->d_c % 64 == 0;
 }
 
+// rows that mla_decode takes on the tensor cores
+bool decodable(const mla_dims_t* d) {
+  return d->dtype == MLA_BF16 && d->d_c == ck::kDc && d->d_r == ck::kDr;
+}
+
 struct Layout {
-  bool expanded;
+  bool expanded, generic;
   // expanded
   int cap, heads, groups;      // page entries; heads per launch; launches
   long long rows_cap;
@@ -380,6 +533,7 @@ bool make_layout(const mla_dims_t* d, int B, int n_tok, int n_ver, int max_pages
     return here;
   };
   l->expanded = chunk_route(d, B, n_tok, max_rows);
+  l->generic = !decodable(d);
   const size_t es = d->dtype == MLA_BF16 ? 2 : 4;
   if (l->expanded) {
     // an even number of pages a sequence
@@ -398,6 +552,9 @@ bool make_layout(const mla_dims_t* d, int B, int n_tok, int n_ver, int max_pages
     l->kr = take((size_t)l->rows_cap * ck::kDr * 2);
     l->k = take((size_t)l->rows_cap * l->heads * ck::kDn * 2);
     l->v = take((size_t)l->rows_cap * l->heads * ck::kDv * 2);
+  } else if (l->generic) {
+    if (generic_smem(d, n_ver) > 48 * 1024 || d->H > 65535) return false;
+    take(256);        // it needs none; an empty workspace is not told from an error
   } else {
     // tokens per pass: 32768 query rows of heads, which bounds the workspace
     l->slab = std::min(n_tok, std::max(1, 32768 / d->H));
@@ -507,8 +664,17 @@ mla_status_t run_expanded(const mla_dims_t* d, const ChunkArgs& a, const Layout&
 }
 
 template <typename T>
+mla_status_t run_generic(const mla_dims_t* d, const ChunkArgs& a, const void* w_uk, const void* w_uv,
+                         void* v, float* lse, cudaStream_t st) {
+  chunk_generic_kernel<T><<<dim3(a.n_tok, d->H), kGenThreads, generic_smem(d, a.n_ver), st>>>(
+      a, d->d_c, generic_groups(d->d_c), d->scale, static_cast<const T*>(w_uk),
+      static_cast<const T*>(w_uv), static_cast<T*>(v), lse);
+  return cudaGetLastError() == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
+}
+
 mla_status_t run_absorbed(const mla_dims_t* d, const ChunkArgs& a, const Layout& l, uint8_t* ws,
                           const void* w_uk, const void* w_uv, void* v, float* lse, cudaStream_t st) {
+  using T = __nv_bfloat16;
   int32_t* table = reinterpret_cast<int32_t*>(ws + l.table);
   mla_seg_t* segs = reinterpret_cast<mla_seg_t*>(ws + l.segs);
   T* q_nope = reinterpret_cast<T*>(ws + l.q_nope);
@@ -617,7 +783,7 @@ extern "C" mla_status_t mla_chunk_attn(const mla_dims_t* dims, int32_t B, int32_
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   if (l.expanded) return run_expanded(dims, a, l, ws, w_uk, w_uv, v, lse, st);
-  if (dims->dtype == MLA_BF16)
-    return run_absorbed<__nv_bfloat16>(dims, a, l, ws, w_uk, w_uv, v, lse, st);
-  return run_absorbed<float>(dims, a, l, ws, w_uk, w_uv, v, lse, st);
+  if (!l.generic) return run_absorbed(dims, a, l, ws, w_uk, w_uv, v, lse, st);
+  if (dims->dtype == MLA_BF16) return run_generic<__nv_bfloat16>(dims, a, w_uk, w_uv, v, lse, st);
+  return run_generic<float>(dims, a, w_uk, w_uv, v, lse, st);
 }

@@ -195,8 +195,10 @@ TilePlan plan_tiles(int M, int N, int K, int sms) {
       long long run = (left * t.k_steps + pairs - 1) / pairs;
       const long long least = (8 + t.P - 1) / t.P < t.k_steps ? (8 + t.P - 1) / t.P : t.k_steps;
       if (run < least) run = least;
-      // up to two partial sums a pair, written and read at about 1600 bytes a clock
-      const double trip = 6000 + 3.0 * pairs * nb * bn * gm::kPairRows * sizeof(float) / 1600.0;
+      // one or two partial sums a pair, written and read at about 1600 bytes a
+      // clock, and the second launch
+      const long long used = left > 0 ? (left * t.k_steps + run - 1) / run : 0;
+      const double trip = 4500 + 2.6 * used * nb * bn * gm::kPairRows * sizeof(float) / 1600.0;
       const bool split = left > 0 && run * step + trip < tile;
       const double drain = nb == 2 ? 8.0 * nb * bn * (rounds + 1) : 4.0 * bn;
       const double cost = rounds * tile + (left ? (split ? run * step + trip : tile) : 0) + drain;
@@ -207,8 +209,7 @@ TilePlan plan_tiles(int M, int N, int K, int sms) {
         t.n_nt = (int)n_nt;
         t.rounds = (int)rounds;
         t.chunk = split ? (int)run : 0;
-        const long long used = split ? (left * t.k_steps + run - 1) / run : left;
-        t.grid = 2 * (int)(rounds ? pairs : used);
+        t.grid = 2 * (int)(rounds ? pairs : split ? used : left);
         t.ws = split ? (size_t)(2 * used) * nb * bn * gm::kPairRows * sizeof(float) : 0;
       }
     }

@@ -522,7 +522,9 @@ mla_status_t mla_append_tokens(const mla_dims_t* dims, int32_t B, int32_t n_tok,
  * is left out.  bf16: products round their operands (expanded keys and values,
  * weights of the softmax) to bf16, sums and statistics are fp32.
  * Errors: INVALID_ARG (scale must be > 0), UNSUPPORTED (page_size != 64,
- * n_ver > 8, row counts beyond 2^31 - 1), WORKSPACE. */
+ * n_ver > 8, row counts beyond 2^31 - 1; outside bf16 rows of 512 + 64, a query
+ * of n_ver (d_c + d_r) and a latent of d_c floats that 48 KB do not hold),
+ * WORKSPACE. */
 mla_status_t mla_chunk_attn(const mla_dims_t* dims, int32_t B, int32_t n_tok, const void* q,
                             const int32_t* tok_start, const int32_t* q_pos, const void* w_uk,
                             const void* w_uv, const void* cache, int64_t n_pages,
