@@ -45,7 +45,7 @@ struct ChunkArgs {
 };
 
 // Pages of sequence b's segments; -1 when its token range or its segment table
-// is invalid (the rules of mla_decode).
+// is invalid (the rules of mla_decode; positions that do not fit in 32 bits).
 __device__ int sequence_pages(const ChunkArgs& a, int b) {
   const int t0 = a.tok_start[b], t1 = a.tok_start[b + 1];
   if (t0 < 0 || t1 < t0 || t1 > a.n_tok) return -1;
@@ -55,7 +55,8 @@ __device__ int sequence_pages(const ChunkArgs& a, int b) {
     const int rb = sg[s].row_begin, re = sg[s].row_end;
     if (re == rb) continue;
     if (rb < prev_end || re < rb || rb % kPage != 0 || (long long)re > (long long)a.max_pages * kPage ||
-        sg[s].q_version < 0 || sg[s].q_version >= a.n_ver)
+        sg[s].q_version < 0 || sg[s].q_version >= a.n_ver ||
+        (long long)sg[s].key_pos_base + (re - rb) > (long long)INT32_MAX + 1)
       return -1;
     prev_end = re;
     pages += (re - rb + kPage - 1) / kPage;
@@ -247,7 +248,7 @@ __global__ void __launch_bounds__(256) chunk_rotary_kernel(const __grid_constant
 enum TokState : int { kLive = 0, kNone = 1, kBad = 2 };
 
 // Tokens [t0, t0 + gridDim.x) as one-token sequences: their block-table and
-// segment rows, their queries split into both parts, a zero rotation position
+// segment rows, a query position, their queries split into both parts, a zero rotation position
 // (q is rotated already; absorption then turns it by -delta alone), and
 // whether they belong to a sequence.  A token without one, or of an invalid
 // one, gets no segments.  grid (tokens, head blocks of eight), a warp per head;
@@ -257,7 +258,8 @@ __global__ void __launch_bounds__(256) chunk_spread_kernel(const __grid_constant
                                                            int t0, int w_n, int w_r,
                                                            int32_t* table, mla_seg_t* segs,
                                                            W* q_nope, W* q_rope,
-                                                           int32_t* rot_pos, int* state) {
+                                                           int32_t* rot_pos, int32_t* q_pos,
+                                                           int* state) {
   __shared__ int s_b, s_bad;
   const int i = blockIdx.x, t = t0 + i, first = blockIdx.y == 0;
   const int h = blockIdx.y * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
@@ -294,13 +296,26 @@ __global__ void __launch_bounds__(256) chunk_spread_kernel(const __grid_constant
     state[i] = st;
     rot_pos[i] = 0;
     if (st == kBad) set_status(MLA_ERR_BAD_INDEX);
+    q_pos[i] = INT32_MAX / 2;      // every row of the cut segments is seen
   }
   for (int k = threadIdx.x; k < a.max_pages; k += blockDim.x)
     table[(size_t)i * a.max_pages + k] =
         st == kLive ? a.block_table[(size_t)b * a.max_pages + k] : 0;
-  for (int k = threadIdx.x; k < a.max_segs; k += blockDim.x)
-    segs[(size_t)i * a.max_segs + k] =
-        st == kLive ? a.segs[(size_t)b * a.max_segs + k] : mla_seg_t{0, 0, 0, 0};
+  // Each segment up to the last row the token sees: rows behind it are then no
+  // rows of the one-token sequence, whatever they hold.  The decode's positions
+  // are shifted to start at zero; its mask sees every row that is left.
+  const long long qp = a.q_pos[t];
+  for (int k = threadIdx.x; k < a.max_segs; k += blockDim.x) {
+    mla_seg_t sg = {0, 0, 0, 0};
+    if (st == kLive) {
+      sg = a.segs[(size_t)b * a.max_segs + k];
+      const long long seen = qp - sg.key_pos_base + 1;
+      if (seen < sg.row_end - sg.row_begin)
+        sg.row_end = sg.row_begin + (int)(seen > 0 ? seen : 0);
+      sg.key_pos_base = 0;
+    }
+    segs[(size_t)i * a.max_segs + k] = sg;
+  }
 }
 
 // Results of those tokens in the storage type; tokens of no sequence keep
@@ -507,7 +522,7 @@ struct Layout {
   size_t plan, seq, items, pages, kr, k, v;
   // absorbed
   int slab;
-  size_t table, segs, q_nope, q_rope, rot, state, q_abs, o_lat, lse, vf, ws, ws_bytes;
+  size_t table, segs, q_nope, q_rope, rot, pos, state, q_abs, o_lat, lse, vf, ws, ws_bytes;
   size_t total;
 };
 
@@ -564,6 +579,7 @@ bool make_layout(const mla_dims_t* d, int B, int n_tok, int n_ver, int max_pages
     l->q_nope = take(n * d->H * d->d_n * es);
     l->q_rope = take(n * d->H * d->d_r * es);
     l->rot = take(n * 4);
+    l->pos = take(n * 4);
     l->state = take(n * 4);
     l->q_abs = take(n * n_ver * d->H * row * es);
     l->o_lat = take(n * d->H * d->d_c * 4);
@@ -680,6 +696,7 @@ mla_status_t run_absorbed(const mla_dims_t* d, const ChunkArgs& a, const Layout&
   T* q_nope = reinterpret_cast<T*>(ws + l.q_nope);
   T* q_rope = reinterpret_cast<T*>(ws + l.q_rope);
   int32_t* rot = reinterpret_cast<int32_t*>(ws + l.rot);
+  int32_t* pos = reinterpret_cast<int32_t*>(ws + l.pos);
   int* state = reinterpret_cast<int*>(ws + l.state);
   float* o_lat = reinterpret_cast<float*>(ws + l.o_lat);
   float* lse_t = reinterpret_cast<float*>(ws + l.lse);
@@ -692,15 +709,15 @@ mla_status_t run_absorbed(const mla_dims_t* d, const ChunkArgs& a, const Layout&
     if (d->d_n * es % 16 == 0 && d->d_r * es % 16 == 0)
       chunk_spread_kernel<uint4><<<grid, 256, 0, st>>>(
           a, t0, d->d_n * es / 16, d->d_r * es / 16, table, segs, reinterpret_cast<uint4*>(q_nope),
-          reinterpret_cast<uint4*>(q_rope), rot, state);
+          reinterpret_cast<uint4*>(q_rope), rot, pos, state);
     else
       chunk_spread_kernel<T><<<grid, 256, 0, st>>>(a, t0, d->d_n, d->d_r, table, segs, q_nope,
-                                                   q_rope, rot, state);
+                                                   q_rope, rot, pos, state);
     if (cudaGetLastError() != cudaSuccess) return MLA_ERR_CUDA;
     mla_status_t rc = mla_absorb_q(d, n, q_nope, q_rope, rot, a.delta, a.n_ver, w_uk, ws + l.q_abs, ms);
     if (rc != MLA_OK) return rc;
     rc = mla_decode(d, n, 1, ws + l.q_abs, a.n_ver, nullptr, d->H, a.cache, a.n_pages, table,
-                    a.max_pages, segs, a.max_segs, nullptr, nullptr, 0, a.q_pos + t0, o_lat, lse_t,
+                    a.max_pages, segs, a.max_segs, nullptr, nullptr, 0, pos, o_lat, lse_t,
                     ws + l.ws, l.ws_bytes, ms);
     if (rc != MLA_OK) return rc;
     const T* wv = static_cast<const T*>(w_uv);

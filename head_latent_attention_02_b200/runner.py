@@ -193,3 +193,71 @@ def offline_partial(p: DeviceProblem, k_off: np.ndarray, stream=None):
         mla.decode(p.dims, p.B, p.s_q, p.q_abs, p.n_ver, p.local_ids, p.n_local, p.cache,
                    p.block_table, p.segs, p.q_pos, p.o_off, p.lse_off, p.workspace,
                    gather_rows=rows, n_gather=n, stream=stream)
+
+
+# ------------------------------------------------------------------ prompt chunks
+@dataclasses.dataclass
+class ChunkProblem:
+    """One layer's attention over a ragged chunk of new tokens: the projected
+    queries and raw latent rows of every new token in, the residual stream out."""
+    dims: mla.Dims
+    w_uk: torch.Tensor           # [H, d_n, d_c]
+    w_uv: torch.Tensor           # [H, d_v, d_c]
+    w_o: torch.Tensor            # [d_model, H * d_v]
+    norm_weight: Optional[torch.Tensor]   # [d_c] float RMSNorm weight of the latent, or None
+    norm_eps: float
+    cache: torch.Tensor          # [n_pages, 64, d_c + d_r]
+    block_table: torch.Tensor    # [B, max_pages]
+    segs: torch.Tensor           # [B, max_segs, 4], the new tokens' rows included
+    deltas: list                 # relocation offsets of the segments' versions
+    max_rows: int                # bound on the rows of all segments, in whole pages
+    tok_start: torch.Tensor      # [B + 1] first token of each sequence
+    row0: torch.Tensor           # [B] first logical row of each sequence's new tokens
+    q_pos: torch.Tensor          # [n_tok] request positions (the causal mask)
+    pos: torch.Tensor            # [axes, n_tok] rotation positions
+    sections: list               # rotary pairs of each axis
+    # outputs and scratch
+    v: torch.Tensor              # [n_tok, H, d_v]
+    out: torch.Tensor            # [n_tok, d_model]
+    workspace: torch.Tensor      # of the attention
+    linear_workspace: torch.Tensor
+
+
+def chunk_problem(dims: mla.Dims, w_uk, w_uv, w_o, cache, block_table, segs, deltas, max_rows: int,
+                  tok_start, row0, q_pos, pos, sections, norm_weight=None,
+                  norm_eps: float = 1e-6) -> ChunkProblem:
+    """Allocates the outputs and workspaces of run_chunk for these sizes."""
+    n_tok, B = q_pos.shape[0], row0.shape[0]
+    dev, dt = cache.device, cache.dtype
+    v = torch.zeros((n_tok, dims.H, dims.d_v), dtype=dt, device=dev)   # padded tokens stay zero
+    out = torch.empty((n_tok, w_o.shape[0]), dtype=dt, device=dev)
+    size = mla.chunk_workspace_size(dims, B, n_tok, len(deltas), block_table.shape[1], segs.shape[1],
+                                    max_rows)
+    if size == 0:
+        raise ValueError("sizes that mla_chunk_attn does not take")
+    linear = mla.linear_workspace_size(v.view(n_tok, -1), w_o)
+    return ChunkProblem(dims, w_uk, w_uv, w_o, norm_weight, norm_eps, cache, block_table, segs,
+                        list(deltas), max_rows, tok_start, row0, q_pos, pos, list(sections), v, out,
+                        torch.empty(size, dtype=torch.uint8, device=dev),
+                        torch.empty(max(linear, 256), dtype=torch.uint8, device=dev))
+
+
+def run_chunk(p: ChunkProblem, q: torch.Tensor, kv: torch.Tensor, residual=None, stream=None):
+    """One layer over the chunk: q [n_tok, H, d_n + d_r] as projected (its rotary
+    part is rotated in place), kv [n_tok, d_c + d_r] raw rows of the
+    down-projection, residual [n_tok, d_model] or None.  Appends the tokens to the
+    cache, attends and projects; returns p.out.  Rows of tokens outside every
+    sequence project zeros: they keep the residual."""
+    with _nvtx("mla_rope_axes"):
+        rot = q[..., p.dims.d_n:]
+        mla.rope_axes(p.dims, rot, p.pos, p.sections, rot, stream=stream)
+    with _nvtx("mla_append_tokens"):
+        mla.append_tokens(p.dims, kv, p.tok_start, p.row0, p.pos, p.sections, p.cache, p.block_table,
+                          norm_weight=p.norm_weight, norm_eps=p.norm_eps, stream=stream)
+    with _nvtx("mla_chunk_attn"):
+        mla.chunk_attn(p.dims, q, p.tok_start, p.q_pos, p.w_uk, p.w_uv, p.cache, p.block_table, p.segs,
+                       p.deltas, p.max_rows, p.v, p.workspace, stream=stream)
+    with _nvtx("mla_linear"):
+        mla.linear(p.v.view(p.v.shape[0], -1), p.w_o, p.out, residual=residual,
+                   workspace=p.linear_workspace, stream=stream)
+    return p.out

@@ -87,14 +87,15 @@ def attended(b, cache, block_table, segs, deltas, d_c, base):
 
 def chunk_attn(q, tok_start, q_pos, w_uk, w_uv, cache, block_table, segs, deltas, scale, base,
                heads=None):
-    """(v [n, H, d_v], lse [n, H], spread [n, H, d_v] = sum_t a_t |V_t|, which scales the error
-    bounds); rows of tokens outside every range are NaN.  A masked row has no part in anything.
-    ``heads`` limits the work to some heads (the others stay NaN)."""
+    """v [n, H, d_v], lse [n, H] and what scales the error bounds: spread [n, H, d_v] = sum_t a_t
+    |V_t|, lat [n, H, d_v] = |W_UV| |sum_t a_t c_t| and key [n, H] = max_t sum_i |q_i K_ti| over the
+    seen rows' content.  Rows of tokens outside every range are NaN.  A masked row has no part in
+    anything.  ``heads`` limits the work to some heads (the others stay NaN)."""
     n, H, _ = q.shape
     d_c, d_n, d_v = w_uk.shape[2], w_uk.shape[1], w_uv.shape[1]
     nan = dict(dtype=torch.float64, device=q.device)
-    v, spread = torch.full((n, H, d_v), math.nan, **nan), torch.full((n, H, d_v), math.nan, **nan)
-    lse = torch.full((n, H), math.nan, **nan)
+    v, spread, lat = (torch.full((n, H, d_v), math.nan, **nan) for _ in range(3))
+    lse, key = torch.full((n, H), math.nan, **nan), torch.zeros((n, H), **nan)
     ts = [int(t) for t in tok_start]
     for b in range(len(ts) - 1):
         if ts[b + 1] <= ts[b]:
@@ -113,14 +114,18 @@ def chunk_attn(q, tok_start, q_pos, w_uk, w_uv, cache, block_table, segs, deltas
             l = torch.logsumexp(s, 1) if s.shape[1] else torch.full((s.shape[0],), -math.inf, **nan)
             a = torch.where(see, torch.exp(s - torch.where(torch.isinf(l), 0.0, l)[:, None]), 0.0)
             # a weight of zero times a value that is not finite: only seen rows count
-            vals = [a @ torch.nan_to_num(V, nan=0.0, posinf=0.0, neginf=0.0),
-                    a @ torch.nan_to_num(V.abs(), nan=0.0, posinf=0.0)]
+            num = lambda x: torch.nan_to_num(x, nan=0.0, posinf=0.0, neginf=0.0)
+            vals = [a @ num(V), a @ num(V).abs(),
+                    (a @ num(rows[:, :d_c])).abs() @ w_uv[h].double().abs().T]
+            if rows.shape[0]:
+                size = qh[:, :d_n].abs() @ num(K).abs().T
+                key[mine, h] = torch.where(see, size, 0.0).amax(1)
             broken = (see & ~torch.isfinite(rows).all(1)[None, :]).any(1)
             for x in vals:
                 x[broken] = math.nan
             l[broken] = math.nan
-            v[mine, h], spread[mine, h], lse[mine, h] = vals[0], vals[1], l
-    return v, lse, spread
+            v[mine, h], spread[mine, h], lat[mine, h], lse[mine, h] = (*vals, l)
+    return v, lse, dict(spread=spread, lat=lat, key=key)
 
 
 def linear(x, w, bias=None, act="none", residual=None):
