@@ -17,7 +17,8 @@
 // cores read both halves, so a CTA loads 40 KB a tile instead of 80 KB.  With one
 // CTA per 256 tokens the ring held a tile and a half and its loads, 1.5 us
 // from issue to landing, stalled the products.  S and O of both query tiles
-// fill the 512 tensor-memory columns; P (bf16) overwrites its S.  The
+// fill the 512 tensor-memory columns; P (16 bits, half or bf16 as the values
+// are: values_as_half) overwrites its S.  The
 // tensor core works on one query tile while the other one's softmax runs:
 //     ... P0 V | S0 | P1 V | S1 | P0 V | S0 ...
 // At 192 + 128 columns a tile costs the tensor core 1280 clocks and its
@@ -27,14 +28,15 @@
 // issues the MMAs, warps 4-7 and 8-11 run the softmax of query tiles 0 and 1 (a
 // thread per query row, so that row statistics need no exchange between
 // threads).  The running maximum is only raised when it grew by more than
-// 2^8 (the weights then stay below 2^8, harmless in fp32 sums and in bf16,
-// whose precision is relative); O is rescaled by the softmax threads in that
-// rare case.  S of step j is issued after P V of step j - 1 and its barrier
+// 2^4, which keeps the weights in range; O is rescaled by the softmax threads
+// in that rare case.  S of step j is issued after P V of step j - 1 and its barrier
 // covers both, so O is at rest while a softmax thread holds S.
 //
 // Every wait is bounded and records MLA_ERR_TIMEOUT when it gives up.
 #pragma once
 #include <cuda.h>
+
+#include <type_traits>
 
 #include "common.cuh"
 #include "ptx.cuh"
@@ -64,7 +66,10 @@ static_assert(kRegsIssue + 2 * kRegsSoftmax == 3 * 168, "register split");
 constexpr int kTmemCols = 512;
 constexpr int kColS = 0, kColO = 256;
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kMargin = 8.0f;              // log2 units: lazy rescale margin
+constexpr float kMargin = 4.0f;              // log2 units: lazy rescale margin
+// weights are kept times 2^11: at most 2^15, the top of half's range, so that
+// the small ones of a long row reach 2^-35 before they vanish
+constexpr float kShift = 11.0f;
 static_assert(kSmemBytes <= 232448, "shared memory budget");
 
 struct Item {
@@ -74,14 +79,8 @@ struct Item {
   int tiles;     // 128-row tiles of the sequence; -1: the sequence is invalid
 };
 
-// What the planner leaves on the device.
-struct Plan {
-  int n_items;
-  int n_row_tiles;    // 256-row tiles of the page list (the expansion's row tiles)
-};
-
 struct Params {
-  const Plan* plan;
+  const ChunkPlan* plan;
   const Item* items;
   const PageEntry* pages;
   const int32_t* q_pos;
@@ -130,6 +129,7 @@ chunk_attn_kernel(const __grid_constant__ Params p, const __grid_constant__ Maps
 
   // the item list and the expanded rows are complete after this wait
   asm volatile("griddepcontrol.wait;" ::: "memory");
+  const bool half = values_as_half(p.plan);
   const int item = blockIdx.x >> 1;
   const int rank = (int)cluster_ctarank();
   if (item >= p.plan->n_items) return;       // both CTAs of the pair
@@ -242,7 +242,8 @@ chunk_attn_kernel(const __grid_constant__ Params p, const __grid_constant__ Maps
       // ------------------------------------------------------------ MMA
       if (rank == 0 && nt > 0) {        // the whole warp, converged
         constexpr uint32_t idesc_s = idesc_bf16_f32(kPairTile, kKTile, false, false);
-        constexpr uint32_t idesc_o = idesc_bf16_f32(kPairTile, kDv, false, true);
+        constexpr uint32_t idesc_pv = idesc_bf16_f32(kPairTile, kDv, false, true);
+      const uint32_t idesc_o = half ? idesc_half_f32(idesc_pv) : idesc_pv;
         // Descriptors of the first panels; a panel, a slot or a K step further is
         // an addition (16-byte units) that never leaves the address field.  The
         // issuing warp shares its scheduler with softmax warps: building each
@@ -272,12 +273,12 @@ chunk_attn_kernel(const __grid_constant__ Params p, const __grid_constant__ Maps
             const uint32_t s_col = tmem + kColS + t * kKTile, o_col = tmem + kColO + t * kDv;
             if (j > 0 && j - 1 < mine) {
 #pragma unroll
-              for (int half = 0; half < 2; ++half) {
-                wait(&bar->p_full[t][half], (j - 1) & 1);
+              for (int part = 0; part < 2; ++part) {
+                wait(&bar->p_full[t][part], (j - 1) & 1);
                 tc_fence_after();
                 if (!ok) break;
 #pragma unroll
-                for (int ks = 4 * half; ks < 4 * half + 4; ++ks)
+                for (int ks = 4 * part; ks < 4 * part + 4; ++ks)
                   mma_pair_bf16_ts_elect(o_col, s_col + 8 * ks, vd + ks * (2048 >> 4), idesc_o,
                                          (j > 1 || ks > 0) ? 1u : 0u);
               }
@@ -372,30 +373,34 @@ chunk_attn_kernel(const __grid_constant__ Params p, const __grid_constant__ Maps
             }
           }
         }
-        const float off = m == kNegInf ? 0.f : -m * p.scale_log2;
+        const float off = m == kNegInf ? 0.f : kShift - m * p.scale_log2;
         const uint64_t off2 = pack_f32x2(off, off), mul2 = pack_f32x2(p.scale_log2, p.scale_log2);
         uint64_t sum[2] = {0ull, 0ull};
         // the weights of 64 columns at a time, so that P V may start on the first
         // half while the second one is computed
+        auto weights = [&](auto as_half) {
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          float w[32];
+          for (int c = 0; c < 2; ++c) {
+            float w[32];
 #pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            const int c0 = 2 * c + i / 16, i0 = 2 * (i % 16);
-            float x, y;
-            unpack_f32x2(fma_f32x2(pack_f32x2(s[c0][i0], s[c0][i0 + 1]), mul2, off2), x, y);
-            x = ex2_approx(x);
-            y = ex2_approx(y);
-            sum[i & 1] = add_f32x2(sum[i & 1], pack_f32x2(x, y));
-            w[i] = __uint_as_float(pack2(x, y));
+            for (int i = 0; i < 32; ++i) {
+              const int c0 = 2 * c + i / 16, i0 = 2 * (i % 16);
+              float x, y;
+              unpack_f32x2(fma_f32x2(pack_f32x2(s[c0][i0], s[c0][i0 + 1]), mul2, off2), x, y);
+              x = ex2_approx(x);
+              y = ex2_approx(y);
+              sum[i & 1] = add_f32x2(sum[i & 1], pack_f32x2(x, y));
+              w[i] = __uint_as_float(decltype(as_half)::value ? pack2_half(x, y) : pack2(x, y));
+            }
+            tmem_st32(s_col + 32 * c, w);
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_pair(mapa(smem_u32(&bar->p_full[t][c]), 0));
           }
-          tmem_st32(s_col + 32 * c, w);
-          tmem_wait_st();
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive_pair(mapa(smem_u32(&bar->p_full[t][c]), 0));
-        }
+        };
+        if (half) weights(std::true_type());
+        else weights(std::false_type());
         float a0, a1;
         unpack_f32x2(add_f32x2(sum[0], sum[1]), a0, a1);
         l += a0 + a1;
@@ -432,7 +437,7 @@ chunk_attn_kernel(const __grid_constant__ Params p, const __grid_constant__ Maps
       }
     }
     if (p.lse && tok < it.n)
-      p.lse[(long long)(it.tok0 + tok) * p.H + h] = none ? kNegInf : m * p.scale + logf(l);
+      p.lse[(long long)(it.tok0 + tok) * p.H + h] = none ? kNegInf : m * p.scale + (logf(l) - kShift / kLog2e);
     tc_fence_before();
   }
 

@@ -21,6 +21,8 @@
 #pragma once
 #include <cuda.h>
 
+#include <type_traits>
+
 #include "common.cuh"
 #include "ptx.cuh"
 
@@ -42,7 +44,7 @@ static_assert(kSmemBytes <= 232448, "shared memory budget");
 
 struct Params {
   const PageEntry* pages;  // four entries a row tile
-  const int* n_row_tiles;      // device: row tiles in use
+  const ChunkPlan* plan;
   int n_heads;                 // heads of this launch
   long long rows_cap;          // rows per head of the scratch
 };
@@ -97,7 +99,7 @@ expand_kernel(const __grid_constant__ Params p, const __grid_constant__ Maps mp)
   // the page list is complete, and the scratch no longer read, after this wait
   asm volatile("griddepcontrol.wait;" ::: "memory");
   // the pair's run of (row tile, head) tiles, heads innermost
-  const int tiles = *p.n_row_tiles * p.n_heads;
+  const int tiles = p.plan->n_row_tiles * p.n_heads;
   const int run = (tiles + pairs - 1) / pairs;
   const int u0 = min(tiles, pair * run), u1 = min(tiles, u0 + run);
 
@@ -194,6 +196,7 @@ expand_kernel(const __grid_constant__ Params p, const __grid_constant__ Maps mp)
     // are not touched by it.  So the values go first.
     const int quad = warp & 3;
     const int row = rank * 128 + quad * 32 + lane;      // row of the pair's tile
+    const bool half = values_as_half(p.plan);
     uint4* stage = reinterpret_cast<uint4*>(smem + kOffStage + quad * kStageWarp);
     if (lane == 0) {
       prefetch_tmap(&mp.k);
@@ -210,22 +213,23 @@ expand_kernel(const __grid_constant__ Params p, const __grid_constant__ Maps mp)
       const uint32_t acc = tmem + ab * 256 + ((uint32_t)(quad * 32) << 16);
       const int y = (int)(h * p.rows_cap) + mt * 256 + rank * 128 + quad * 32;
       bool fine = true;
-#pragma unroll 1
-      for (int c = 3; c >= 0; --c) {                // value panels 3, 2, key panels 1, 0
+      // 64 columns: tensor memory -> 16-bit pairs -> staging -> scratch
+      auto panel = [&](int c, auto is_value, auto as_half) {
         float v[2][32];
         tmem_ld64_sync(acc + 64 * c, v);
         uint32_t w[32];
 #pragma unroll
         for (int i = 0; i < 32; ++i) {
           float a = v[i >> 4][2 * (i & 15)], b = v[i >> 4][2 * (i & 15) + 1];
-          if (c >= 2) {
+          if constexpr (decltype(is_value)::value) {
             // the largest finite bf16: what rounds past it is not finite either
             const bool fa = fabsf(a) <= 3.38953139e38f, fb = fabsf(b) <= 3.38953139e38f;
             fine = fine && fa && fb;
             a = fa ? a : 0.f;
             b = fb ? b : 0.f;
           }
-          w[i] = live ? pack2(a, b) : 0u;
+          w[i] = decltype(as_half)::value ? pack2_half(a, b) : pack2(a, b);
+          if (!live) w[i] = 0u;
         }
         if (c == 0 && live && !fine) w[0] = 0x7fff7fffu;        // NaN
         if (lane == 0) bulk_wait_read<0>();         // the last store has left the staging tile
@@ -237,10 +241,19 @@ expand_kernel(const __grid_constant__ Params p, const __grid_constant__ Maps mp)
         fence_proxy_async();
         __syncwarp();
         if (lane == 0) {
-          tma_store_3d(c >= 2 ? &mp.v : &mp.k, stage, 0, y, c & 1);
+          tma_store_3d(decltype(is_value)::value ? &mp.v : &mp.k, stage, 0, y, c & 1);
           bulk_commit();
         }
+      };
+      if (half) {
+        panel(3, std::true_type(), std::true_type());
+        panel(2, std::true_type(), std::true_type());
+      } else {
+        panel(3, std::true_type(), std::false_type());
+        panel(2, std::true_type(), std::false_type());
       }
+      panel(1, std::false_type(), std::false_type());
+      panel(0, std::false_type(), std::false_type());
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive_pair(mapa(smem_u32(&bar->acc_empty[ab]), 0));

@@ -133,7 +133,7 @@ __device__ __forceinline__ int last_at_most(const int* off, int n, int x) {
 // their 512-token items.  seq: page offset [B + 1], item offset [B + 1], flag
 // [B].  A sequence that does not fit `cap` pages is invalid.
 __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(
-    const __grid_constant__ ChunkArgs a, int cap, ck::Plan* plan, int* seq, ck::Item* items,
+    const __grid_constant__ ChunkArgs a, int cap, ChunkPlan* plan, int* seq, ck::Item* items,
     PageEntry* pages) {
   asm volatile("griddepcontrol.launch_dependents;");
   __shared__ int scratch[33], n_pg, n_it, used;
@@ -173,6 +173,7 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(
     itm[a.B] = n_it;
     plan->n_items = n_it;
     plan->n_row_tiles = whole / 4;
+    plan->c_sq = plan->w_sq = 0;
   }
   __syncthreads();
   for (int e = threadIdx.x; e < whole; e += kPlanThreads) {
@@ -202,17 +203,48 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(
   }
 }
 
-// Rotary keys of the listed pages at their request positions: kr[64 e + r] =
-// R(delta[version]) k_rope of page entry e's row r (a plain copy where delta
-// is zero); rows without data are zeros.  One block of 256 threads per entry,
-// four threads a row.
+// Squared norm of 512 channels, four threads a row; every thread of the four
+// gets it.  Half of the row's additions are independent of the other half.
+__device__ __forceinline__ float row_norm_sq(const __nv_bfloat16* row, int part) {
+  const uint4* src = reinterpret_cast<const uint4*>(row) + part;
+  float a = 0.f, b = 0.f;
+#pragma unroll 8
+  for (int i = 0; i < ck::kDc / 32; ++i) {
+    const uint4 u = src[4 * i];
+    a = fmaf(lo_f(u.x), lo_f(u.x), a); b = fmaf(hi_f(u.x), hi_f(u.x), b);
+    a = fmaf(lo_f(u.y), lo_f(u.y), a); b = fmaf(hi_f(u.y), hi_f(u.y), b);
+    a = fmaf(lo_f(u.z), lo_f(u.z), a); b = fmaf(hi_f(u.z), hi_f(u.z), b);
+    a = fmaf(lo_f(u.w), lo_f(u.w), a); b = fmaf(hi_f(u.w), hi_f(u.w), b);
+  }
+  a += b;
+  a += __shfl_xor_sync(0xffffffffu, a, 1);
+  return a + __shfl_xor_sync(0xffffffffu, a, 2);
+}
+
+// Blocks [0, cap): rotary keys of the listed pages at their request positions,
+// kr[64 e + r] = R(delta[version]) k_rope of page entry e's row r (a plain copy
+// where delta is zero; rows without data are zeros), and the largest norm of
+// the rows' latents.  The blocks after them: the largest norm of 64 rows of
+// W_UV each.  The latents and weights read here are read again by the expansion,
+// from L2.  256 threads, four a row.
 __global__ void __launch_bounds__(256) chunk_rotary_kernel(const __grid_constant__ ChunkArgs a,
-                                                           const ck::Plan* plan,
+                                                           int cap, ChunkPlan* plan,
                                                            const PageEntry* pages,
+                                                           const __nv_bfloat16* w_uv,
                                                            __nv_bfloat16* kr) {
   asm volatile("griddepcontrol.launch_dependents;");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   __shared__ double2 cs[ck::kDr / 2];
+  const int r = threadIdx.x >> 2, part = threadIdx.x & 3;
+  if ((int)blockIdx.x >= cap) {
+    const float sq =
+        row_norm_sq(w_uv + ((size_t)(blockIdx.x - cap) * 64 + r) * ck::kDc, part);
+    // a weight that is not finite keeps the call from halves
+    const int bits = __float_as_int(sq == sq ? sq : __int_as_float(0x7f800000));
+    const int top = __reduce_max_sync(0xffffffffu, bits);
+    if ((threadIdx.x & 31) == 0) atomicMax(&plan->w_sq, top);
+    return;
+  }
   if ((int)blockIdx.x >= 4 * plan->n_row_tiles) return;
   const PageEntry e = pages[blockIdx.x];
   const int delta = e.n > 0 ? a.delta[e.ver] : 0;
@@ -221,12 +253,12 @@ __global__ void __launch_bounds__(256) chunk_rotary_kernel(const __grid_constant
       sincos((double)delta * pow(a.rope_base, -2.0 * i / ck::kDr), &cs[i].y, &cs[i].x);
     __syncthreads();
   }
-  const int r = threadIdx.x >> 2, part = threadIdx.x & 3;
+  const __nv_bfloat16* row = static_cast<const __nv_bfloat16*>(a.cache) +
+                             ((long long)e.row + r) * (ck::kDc + ck::kDr);
   uint4 u[2] = {make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)};
+  float sq = 0.f;
   if (r < e.n) {
-    const uint4* src = reinterpret_cast<const uint4*>(
-        static_cast<const __nv_bfloat16*>(a.cache) +
-        ((long long)e.row + r) * (ck::kDc + ck::kDr) + ck::kDc + part * 16);
+    const uint4* src = reinterpret_cast<const uint4*>(row + ck::kDc + part * 16);
     u[0] = src[0];
     u[1] = src[1];
     if (delta != 0) {
@@ -239,9 +271,19 @@ __global__ void __launch_bounds__(256) chunk_rotary_kernel(const __grid_constant
       }
     }
   }
-  uint4* dst = reinterpret_cast<uint4*>(kr + ((long long)blockIdx.x * kPage + r) * ck::kDr + part * 16);
+  uint4* dst =
+      reinterpret_cast<uint4*>(kr + ((long long)blockIdx.x * kPage + r) * ck::kDr + part * 16);
   dst[0] = u[0];
   dst[1] = u[1];
+  // rows 8 w .. 8 w + 7 of warp w; beyond the page's data the last row again
+  if (e.n > 0) {
+    sq = row_norm_sq(row - (r < e.n ? 0 : (r - e.n + 1) * (ck::kDc + ck::kDr)), part);
+    // a NaN latent's values are stored as zeros; an infinite norm (which finite
+    // channels can have) keeps the call from halves
+    const int bits = __float_as_int(sq == sq ? sq : 0.f);
+    const int top = __reduce_max_sync(0xffffffffu, bits);
+    if ((threadIdx.x & 31) == 0) atomicMax(&plan->c_sq, top);
+  }
 }
 
 // ------------------------------------------------------------ absorbed route
@@ -560,7 +602,7 @@ bool make_layout(const mla_dims_t* d, int B, int n_tok, int n_ver, int max_pages
     l->heads = (d->H + l->groups - 1) / l->groups;
     if (l->rows_cap * l->heads + 4 * kPage > INT32_MAX) return false;
     l->cap = (int)cap;
-    l->plan = take(sizeof(ck::Plan));
+    l->plan = take(sizeof(ChunkPlan));
     l->seq = take(sizeof(int) * (3 * (size_t)B + 2));
     l->items = take(sizeof(ck::Item) * ((size_t)n_tok / ck::kItemTokens + B));
     l->pages = take(sizeof(PageEntry) * (size_t)cap);
@@ -603,7 +645,7 @@ mla_status_t run_expanded(const mla_dims_t* d, const ChunkArgs& a, const Layout&
                           const void* w_uk, const void* w_uv, void* v, float* lse, cudaStream_t st) {
   const int sms = current_sms();
   if (!sms) return MLA_ERR_CUDA;
-  ck::Plan* plan = reinterpret_cast<ck::Plan*>(ws + l.plan);
+  ChunkPlan* plan = reinterpret_cast<ChunkPlan*>(ws + l.plan);
   ck::Item* items = reinterpret_cast<ck::Item*>(ws + l.items);
   PageEntry* pages = reinterpret_cast<PageEntry*>(ws + l.pages);
   __nv_bfloat16* kr = reinterpret_cast<__nv_bfloat16*>(ws + l.kr);
@@ -635,14 +677,14 @@ mla_status_t run_expanded(const mla_dims_t* d, const ChunkArgs& a, const Layout&
   chunk_plan_kernel<<<1, kPlanThreads, 0, st>>>(a, l.cap, plan, reinterpret_cast<int*>(ws + l.seq),
                                                 items, pages);
   if (cudaGetLastError() != cudaSuccess) return MLA_ERR_CUDA;
-  if (launch_dependent(chunk_rotary_kernel, dim3(l.cap), dim3(256), 0, st, true, a,
-                       static_cast<const ck::Plan*>(plan),
-                       static_cast<const PageEntry*>(pages), kr) != cudaSuccess)
+  if (launch_dependent(chunk_rotary_kernel, dim3(l.cap + d->H * ck::kDv / 64), dim3(256), 0, st, true,
+                       a, l.cap, plan, static_cast<const PageEntry*>(pages),
+                       static_cast<const __nv_bfloat16*>(w_uv), kr) != cudaSuccess)
     return MLA_ERR_CUDA;
 
   ex::Params g;
   g.pages = pages;
-  g.n_row_tiles = &plan->n_row_tiles;
+  g.plan = plan;
   g.rows_cap = l.rows_cap;
   ck::Params p;
   p.plan = plan;

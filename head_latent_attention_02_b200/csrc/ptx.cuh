@@ -373,6 +373,11 @@ __host__ __device__ constexpr uint32_t idesc_bf16_f32(int M, int N, bool a_mn_ma
          (uint32_t(b_mn_major) << 16) | (uint32_t(N >> 3) << 17) | (uint32_t(M >> 4) << 24);
 }
 
+// The same for 16-bit operands of either type: f16 (half) or bf16.
+__device__ __forceinline__ constexpr uint32_t idesc_half_f32(uint32_t idesc_bf16) {
+  return idesc_bf16 & ~((1u << 7) | (1u << 10));
+}
+
 }  // namespace mla
 
 namespace mla {

@@ -177,6 +177,27 @@ def test_every_head_of_a_wide_layer():
     Case("bf16", 128, [290, 600], [500, 130]).run().check(heads=[0, 1, 63, 127])
 
 
+@pytest.mark.parametrize("size", [2.0 ** -12, 2.0 ** -3, 2.0 ** 9, 2.0 ** 14, 2.0 ** 60])
+def test_values_of_every_size(size):
+    """Values are held as halves between limits on their size and as bfloat16 outside them."""
+    c = Case("bf16", 4, [300, 280], [100, 300])
+    c.w_uv.mul_(size)
+    c.run()
+    torch.cuda.synchronize()
+    assert mla.get_status() == 0
+    v, _, _ = c.reference()
+    off = (c.v.double() - v).norm() / v.norm()
+    # K (about 0.8 of a rounding in the scores), the result, and weights and values in bfloat16
+    assert off <= (2.3e-3 if 0.125 <= size <= 512 else 4.5e-3)
+    # the last row, seen by one token alone, far larger than all others
+    c.cache[int(c.bt[0, 399 // 64]), 399 % 64, :512] = 2.0 ** 40
+    c.run()
+    torch.cuda.synchronize()
+    assert torch.isfinite(c.v.float()).all() or size > 2.0 ** 50
+    others = [t for t in range(580) if t != 299]
+    assert (c.v[others].double() - v[others]).norm() <= 4.5e-3 * v[others].norm()
+
+
 def test_heads_in_groups():
     """More than 1 GiB of keys and values: the heads run in several passes."""
     c = Case("bf16", 128, [512], [17000])
