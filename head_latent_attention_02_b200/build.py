@@ -12,7 +12,8 @@ SOURCES = ["csrc/mla_lib.cu", "csrc/mla_static_ws.cu", "csrc/mla_append.cu",
            "csrc/mla_linear.cu", "csrc/mla_chunk.cu"]
 DEPENDS = ["csrc/mla_lib.cu", "csrc/mla_static_ws.cu", "csrc/mla_append.cu", "csrc/mla_qknorm.cu",
            "csrc/mla_lowbit_tc.cu", "csrc/mla_tokens.cu", "csrc/mla_linear.cu", "csrc/mla_chunk.cu",
-           "csrc/common.cuh", "csrc/host_tma.cuh", "csrc/gemm_tc.cuh", "csrc/chunk_tc.cuh", "csrc/expand_tc.cuh",
+           "csrc/common.cuh", "csrc/host_tma.cuh", "csrc/gemm_tc.cuh", "csrc/chunk_tc.cuh",
+           "csrc/expand_tc.cuh", "csrc/few_tc.cuh",
            "csrc/ptx.cuh", "csrc/kernels_simt.cuh", "csrc/kernels_lowbit.cuh", "csrc/wgemm.cuh", "csrc/decode_tc.cuh", "../include/mla.h"]
 
 NVCC_FLAGS = [

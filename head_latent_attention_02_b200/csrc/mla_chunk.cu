@@ -6,9 +6,8 @@
 //              expanded once per call into the workspace (expand_tc.cuh), the
 //              rotary keys moved to their request positions, and the direct
 //              form attends over them (chunk_tc.cuh).  For chunks.
-//   absorbed   few tokens over those rows: each token is a one-token sequence
-//              of mla_decode between mla_absorb_q and the value expansion of
-//              mla_out_proj.
+//   absorbed   few tokens over those rows (few_tc.cuh), between mla_absorb_q and
+//              the value expansion of mla_out_proj.
 //   generic    fp32 and other widths: one kernel on the CUDA cores.
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -24,6 +23,7 @@
 #include "host_tma.cuh"
 #include "expand_tc.cuh"
 #include "chunk_tc.cuh"
+#include "few_tc.cuh"
 
 namespace mla {
 namespace {
@@ -118,6 +118,35 @@ __device__ int block_scan(int x, int* scratch, int* carry) {
   return out;
 }
 
+// Largest x over the block's threads up to this one and over *carry, which ends
+// as the largest of all.
+__device__ int block_scan_max(int x, int* scratch, int* carry) {
+  const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int z = __shfl_up_sync(0xffffffffu, x, d);
+    if (lane >= d) x = max(x, z);
+  }
+  if (lane == 31) scratch[wid] = x;
+  __syncthreads();
+  if (wid == 0) {
+    int t = scratch[lane];
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int z = __shfl_up_sync(0xffffffffu, t, d);
+      if (lane >= d) t = max(t, z);
+    }
+    scratch[lane] = t;
+  }
+  __syncthreads();
+  const int out = max(max(*carry, x), wid ? scratch[wid - 1] : INT32_MIN);
+  const int total = scratch[31];
+  __syncthreads();
+  if (threadIdx.x == 0) *carry = max(*carry, total);
+  __syncthreads();
+  return out;
+}
+
 // last index i in [0, n) with off[i] <= x (off ascending, off[0] <= x)
 __device__ __forceinline__ int last_at_most(const int* off, int n, int x) {
   int lo = 0, hi = n - 1;
@@ -128,29 +157,141 @@ __device__ __forceinline__ int last_at_most(const int* off, int n, int x) {
   return lo;
 }
 
+// Flags of a sequence: its tokens get NaN; its token range is invalid (no tokens).
+constexpr int kInvalid = 1, kNoRange = 2;
+
+enum TokState : int { kNone = 0, kLive = 1, kBad = 2 };
+
+// One CTA, after the page list: the streams of the tokens [slab0, slab0 +
+// slab_n) with their tile counts (pages up to the last one that any row sees),
+// each token's state, and the run length.  A run that no stream boundary falls
+// into saves a pair its second set of partial sums: with equal streams, a
+// divisor or multiple of their length is taken if it costs at most a quarter
+// more tiles a pair.
+struct FewPlan {
+  int slab0, slab_n, pairs;
+  fw::Plan* plan;
+  fw::Stream* streams;
+  int* state;
+};
+
+__device__ void plan_few(const ChunkArgs& a, const FewPlan& f, const int* seq, const PageEntry* pages) {
+  const int slab0 = f.slab0, slab_n = f.slab_n, pairs = f.pairs;
+  fw::Plan* plan = f.plan;
+  fw::Stream* streams = f.streams;
+  int* state = f.state;
+  __shared__ int scratch[33], n_st, units, longest, shortest;
+  const int* pg = seq;
+  const int* bad = seq + 2 * (a.B + 1);
+  if (threadIdx.x == 0) {
+    n_st = units = longest = 0;
+    shortest = INT32_MAX;
+  }
+  for (int t = threadIdx.x; t < slab_n; t += kPlanThreads) state[t] = kNone;
+  __syncthreads();
+  // streams, in the order of the sequences
+  for (int b0 = 0; b0 < a.B; b0 += kPlanThreads) {
+    const int b = b0 + threadIdx.x;
+    int ns = 0, t0 = 0, t1 = 0;
+    if (b < a.B && bad[b] != kNoRange) {
+      t0 = max(a.tok_start[b] - slab0, 0);           // tokens of the slab
+      t1 = min(a.tok_start[b + 1] - slab0, slab_n);
+      for (int t = t0; t < t1; ++t) state[t] = bad[b] ? kBad : kLive;
+      if (!bad[b] && t1 > t0) ns = ((t1 - t0) * a.H + fw::kRows - 1) / fw::kRows;
+    }
+    const int at = block_scan(ns, scratch, &n_st);
+    for (int k = 0; k < ns; ++k) {
+      fw::Stream s;
+      s.q_row = t0 * a.H + k * fw::kRows;
+      s.rows = min(fw::kRows, t1 * a.H - s.q_row);
+      s.entry = pg[b];
+      s.q_min = INT32_MAX;
+      s.q_max = INT32_MIN;
+      for (int t = s.q_row / a.H; t <= (s.q_row + s.rows - 1) / a.H; ++t) {
+        s.q_min = min(s.q_min, a.q_pos[slab0 + t]);
+        s.q_max = max(s.q_max, a.q_pos[slab0 + t]);
+      }
+      s.tiles = pg[b + 1] - pg[b];
+      while (s.tiles > 0 && fw::visible(pages[s.entry + s.tiles - 1], s.q_max) == 0) --s.tiles;
+      s.off = 0;
+      streams[at + k] = s;
+      if (s.tiles > 0) {
+        atomicMax(&longest, s.tiles);
+        atomicMin(&shortest, s.tiles);
+      }
+    }
+  }
+  __syncthreads();
+  const int n = n_st;
+  for (int i0 = 0; i0 < n; i0 += kPlanThreads) {
+    const int i = i0 + threadIdx.x;
+    const int off = block_scan(i < n ? streams[i].tiles : 0, scratch, &units);
+    if (i < n) streams[i].off = off;
+  }
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    int run = max(1, (units + pairs - 1) / pairs);
+    if (units > 0 && longest == shortest) {
+      const int live = units / longest;          // streams with tiles
+      int even = 0;
+      if (live > pairs) {
+        even = longest * ((live + pairs - 1) / pairs);
+      } else {
+        for (int parts = min(longest, pairs / live); parts >= 1 && !even; --parts)
+          if (longest % parts == 0) even = longest / parts;
+      }
+      if (even > 0 && 4ll * even <= 5ll * run) run = even;
+    }
+    plan->n_streams = n;
+    plan->units = units;
+    plan->chunk = run;
+  }
+}
+
+// The streams of a later slab.
+__global__ void __launch_bounds__(kPlanThreads) few_plan_kernel(
+    const __grid_constant__ ChunkArgs a, const __grid_constant__ FewPlan f, const int* seq,
+    const PageEntry* pages) {
+  asm volatile("griddepcontrol.launch_dependents;");
+  plan_few(a, f, seq, pages);
+}
+
 // One CTA: validates the sequences, lists their pages (an even number each, so
 // that a 128-row tile belongs to one sequence; a multiple of four in all) and
 // their 512-token items.  seq: page offset [B + 1], item offset [B + 1], flag
-// [B].  A sequence that does not fit `cap` pages is invalid.
+// [B].  A sequence that does not fit `cap` pages is invalid.  A token range is
+// only taken if it starts at or behind every start before it: ranges are then
+// disjoint, which the item and stream lists rely on.
+// kFew: the absorbed route's streams follow, in place of the items.  That kernel
+// is launched as a dependent of the absorption, whose results it does not read:
+// it works beside it and only waits for it before it ends, so that what follows
+// finds both complete.
+template <bool kFew>
 __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(
-    const __grid_constant__ ChunkArgs a, int cap, ChunkPlan* plan, int* seq, ck::Item* items,
-    PageEntry* pages) {
+    const __grid_constant__ ChunkArgs a, const __grid_constant__ FewPlan f, int cap, ChunkPlan* plan,
+    int* seq, ck::Item* items, PageEntry* pages) {
   asm volatile("griddepcontrol.launch_dependents;");
-  __shared__ int scratch[33], n_pg, n_it, used;
+  __shared__ int scratch[33], n_pg, n_it, used, latest;
   int* pg = seq;
   int* itm = seq + a.B + 1;
   int* bad = seq + 2 * (a.B + 1);
-  if (threadIdx.x == 0) n_pg = n_it = used = 0;
+  if (threadIdx.x == 0) {
+    n_pg = n_it = used = 0;
+    latest = INT32_MIN;
+  }
   __syncthreads();
   for (int b0 = 0; b0 < a.B; b0 += kPlanThreads) {
     const int b = b0 + threadIdx.x;
     int np = 0, ni = 0;
-    bool wrong = false;
+    bool wrong = false, ranged = false;
+    const int from = b < a.B ? a.tok_start[b] : INT32_MIN;
+    const bool behind = from == block_scan_max(from, scratch, &latest);
     if (b < a.B) {
-      const int t0 = a.tok_start[b], t1 = a.tok_start[b + 1];
+      const int t0 = from, t1 = a.tok_start[b + 1];
       const int k = sequence_pages(a, b);
-      wrong = k < 0;
-      if (t0 >= 0 && t1 > t0 && t1 <= a.n_tok) {
+      wrong = k < 0 || !behind;
+      ranged = behind && t0 >= 0 && t1 >= t0 && t1 <= a.n_tok;
+      if (ranged && t1 > t0) {
         ni = (t1 - t0 - 1) / ck::kItemTokens + 1;
         np = wrong ? 0 : (k + 1) / 2 * 2;
       }
@@ -161,7 +302,7 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(
       if ((long long)po + np > cap) wrong = true;
       pg[b] = min(po, cap);
       itm[b] = io;
-      bad[b] = wrong ? 1 : 0;
+      bad[b] = !ranged ? kNoRange : wrong ? kInvalid : 0;
       if (wrong) set_status(MLA_ERR_BAD_INDEX);
       else atomicMax(&used, po + np);
     }
@@ -182,12 +323,17 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(
       const int b = last_at_most(pg, a.B, e);
       if (!bad[b] && e - pg[b] < sequence_pages(a, b) && !page_at(a, b, e - pg[b], &pe)) {
         set_status(MLA_ERR_BAD_INDEX);
-        atomicExch(&bad[b], 2);
+        atomicExch(&bad[b], kInvalid);
       }
     }
     pages[e] = pe;
   }
   __syncthreads();
+  if constexpr (kFew) {
+    plan_few(a, f, seq, pages);
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    return;
+  }
   const int total = itm[a.B];
   for (int i = threadIdx.x; i < total; i += kPlanThreads) {
     const int b = last_at_most(itm, a.B, i);
@@ -226,7 +372,8 @@ __device__ __forceinline__ float row_norm_sq(const __nv_bfloat16* row, int part)
 // where delta is zero; rows without data are zeros), and the largest norm of
 // the rows' latents.  The blocks after them: the largest norm of 64 rows of
 // W_UV each.  The latents and weights read here are read again by the expansion,
-// from L2.  256 threads, four a row.
+// from L2.  256 threads, four a row.  (Without kNorms, the rotary keys alone.)
+template <bool kNorms>
 __global__ void __launch_bounds__(256) chunk_rotary_kernel(const __grid_constant__ ChunkArgs a,
                                                            int cap, ChunkPlan* plan,
                                                            const PageEntry* pages,
@@ -276,7 +423,7 @@ __global__ void __launch_bounds__(256) chunk_rotary_kernel(const __grid_constant
   dst[0] = u[0];
   dst[1] = u[1];
   // rows 8 w .. 8 w + 7 of warp w; beyond the page's data the last row again
-  if (e.n > 0) {
+  if (kNorms && e.n > 0) {
     sq = row_norm_sq(row - (r < e.n ? 0 : (r - e.n + 1) * (ck::kDc + ck::kDr)), part);
     // a NaN latent's values are stored as zeros; an infinite norm (which finite
     // channels can have) keeps the call from halves
@@ -287,107 +434,120 @@ __global__ void __launch_bounds__(256) chunk_rotary_kernel(const __grid_constant
 }
 
 // ------------------------------------------------------------ absorbed route
-enum TokState : int { kLive = 0, kNone = 1, kBad = 2 };
+// The queries' two parts as the absorption takes them, a zero rotation position
+// (they are rotated already).  grid (tokens, head blocks of eight), a warp
+// per head; w_n and w_r count 16-byte words.
+__global__ void __launch_bounds__(256) few_split_kernel(int H, int w_n, int w_r, const uint4* q,
+                                                        uint4* q_nope, uint4* q_rope,
+                                                        int32_t* rot_pos) {
+  const int t = blockIdx.x, h = blockIdx.y * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  if (blockIdx.y == 0 && threadIdx.x == 0) rot_pos[t] = 0;
+  if (h >= H) return;
+  const size_t at = (size_t)t * H + h;
+  const uint4* src = q + at * (w_n + w_r);
+  for (int k = lane; k < w_n; k += 32) q_nope[at * w_n + k] = src[k];
+  for (int k = lane; k < w_r; k += 32) q_rope[at * w_r + k] = src[w_n + k];
+}
 
-// Tokens [t0, t0 + gridDim.x) as one-token sequences: their block-table and
-// segment rows, a query position, their queries split into both parts, a zero rotation position
-// (q is rotated already; absorption then turns it by -delta alone), and
-// whether they belong to a sequence.  A token without one, or of an invalid
-// one, gets no segments.  grid (tokens, head blocks of eight), a warp per head;
-// w_n and w_r count the 16-byte or single-element words of both query parts.
-template <typename W>
-__global__ void __launch_bounds__(256) chunk_spread_kernel(const __grid_constant__ ChunkArgs a,
-                                                           int t0, int w_n, int w_r,
-                                                           int32_t* table, mla_seg_t* segs,
-                                                           W* q_nope, W* q_rope,
-                                                           int32_t* rot_pos, int32_t* q_pos,
-                                                           int* state) {
-  __shared__ int s_b, s_bad;
-  const int i = blockIdx.x, t = t0 + i, first = blockIdx.y == 0;
-  const int h = blockIdx.y * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-  // the queries do not depend on the sequence
-  if (h < a.H) {
-    const W* q = static_cast<const W*>(a.q) + ((size_t)t * a.H + h) * (w_n + w_r);
-    const size_t at = (size_t)i * a.H + h;
-    for (int k = lane; k < w_n; k += 32) q_nope[at * w_n + k] = q[k];
-    for (int k = lane; k < w_r; k += 32) q_rope[at * w_r + k] = q[w_n + k];
+// The shares of every (token, head) row merged by log-sum-exp, and what the
+// rounding to bf16 leaves of the result: o [n, H, 512], then the rest [n, H,
+// 512], so that the value expansion, which rounds its input, takes both.
+// grid (streams at most, 16), 256 threads: eight rows of a stream, a thread per
+// (row, four columns) and 128-column block; the shares of eight rows of one
+// column group are 128 contiguous bytes.  Rows that no stream holds are left
+// out: their results are not stored.
+__global__ void __launch_bounds__(256) few_combine_kernel(int n_rows, const fw::Plan* plan,
+                                                          const fw::Stream* streams,
+                                                          const float* partial,
+                                                          const float* partial_lse, float* o,
+                                                          float* lse) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  __shared__ float4 stage[8][33];
+  const int si = blockIdx.x;
+  if (si >= plan->n_streams) return;
+  const fw::Stream s = streams[si];
+  const int r = threadIdx.x & 7, in = blockIdx.y * 8 + r, c = threadIdx.x >> 3;
+  if ((int)blockIdx.y * 8 >= s.rows) return;
+  const int g0 = s.tiles > 0 ? s.off / plan->chunk : 0;
+  const int g1 = s.tiles > 0 ? (s.off + s.tiles - 1) / plan->chunk : -1;
+  float top = kNegInf;
+  bool nan = false;
+  for (int g = g0; g <= g1; ++g) {
+    const float x = partial_lse[(size_t)(g + si) * fw::kRows + in];
+    nan = nan || x != x;
+    top = fmaxf(top, x);
   }
-  if (!first) return;
-  if (threadIdx.x == 0) {
-    s_b = -1;
-    s_bad = 0;
-  }
-  __syncthreads();
-  for (int b = threadIdx.x; b < a.B; b += blockDim.x) {
-    const int lo = a.tok_start[b], hi = a.tok_start[b + 1];
-    if (lo < 0 || hi < lo || hi > a.n_tok) set_status(MLA_ERR_BAD_INDEX);
-    else if (lo <= t && t < hi) atomicMax(&s_b, b);
-  }
-  __syncthreads();
-  const int b = s_b;
-  if (b >= 0) {
-    const int np = sequence_pages(a, b);
-    if (np < 0 && threadIdx.x == 0) s_bad = 1;
-    PageEntry e;
-    for (int k = threadIdx.x; k < np; k += blockDim.x)
-      if (!page_at(a, b, k, &e)) s_bad = 1;
-  }
-  __syncthreads();
-  const int st = b < 0 ? kNone : (s_bad ? kBad : kLive);
-  if (threadIdx.x == 0) {
-    state[i] = st;
-    rot_pos[i] = 0;
-    if (st == kBad) set_status(MLA_ERR_BAD_INDEX);
-    q_pos[i] = INT32_MAX / 2;      // every row of the cut segments is seen
-  }
-  for (int k = threadIdx.x; k < a.max_pages; k += blockDim.x)
-    table[(size_t)i * a.max_pages + k] =
-        st == kLive ? a.block_table[(size_t)b * a.max_pages + k] : 0;
-  // Each segment up to the last row the token sees: rows behind it are then no
-  // rows of the one-token sequence, whatever they hold.  The decode's positions
-  // are shifted to start at zero; its mask sees every row that is left.
-  const long long qp = a.q_pos[t];
-  for (int k = threadIdx.x; k < a.max_segs; k += blockDim.x) {
-    mla_seg_t sg = {0, 0, 0, 0};
-    if (st == kLive) {
-      sg = a.segs[(size_t)b * a.max_segs + k];
-      const long long seen = qp - sg.key_pos_base + 1;
-      if (seen < sg.row_end - sg.row_begin)
-        sg.row_end = sg.row_begin + (int)(seen > 0 ? seen : 0);
-      sg.key_pos_base = 0;
+  if (nan) top = kNaN;
+  float4 acc[4] = {};
+  float tot = 0.f;
+  if (top != kNegInf && in < s.rows) {
+#pragma unroll 4
+    for (int g = g0; g <= g1; ++g) {
+      const float w = __expf(partial_lse[(size_t)(g + si) * fw::kRows + in] - top);
+      const float4* src = reinterpret_cast<const float4*>(partial) +
+                          (size_t)(g + si) * (fw::kDc / 4) * fw::kRows + in;
+      tot += w;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float4 v = src[(size_t)(32 * i + c) * fw::kRows];
+        acc[i].x = fmaf(w, v.x, acc[i].x);
+        acc[i].y = fmaf(w, v.y, acc[i].y);
+        acc[i].z = fmaf(w, v.z, acc[i].z);
+        acc[i].w = fmaf(w, v.w, acc[i].w);
+      }
     }
-    segs[(size_t)i * a.max_segs + k] = sg;
+  }
+  const float inv = tot == 0.f ? 0.f : 1.f / tot;
+  if (c == 0 && in < s.rows) lse[s.q_row + in] = tot == 0.f ? kNegInf : top + logf(tot);
+  // 128 columns of the eight rows at a time, turned so that a row's are written
+  // together
+  const int wr = threadIdx.x >> 5, lane = threadIdx.x & 31, w_in = blockIdx.y * 8 + wr;
+  float4* d0 = reinterpret_cast<float4*>(o + (size_t)(s.q_row + w_in) * fw::kDc) + lane;
+  float4* d1 = d0 + (size_t)n_rows * (fw::kDc / 4);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    stage[r][c] = make_float4(acc[i].x * inv, acc[i].y * inv, acc[i].z * inv, acc[i].w * inv);
+    __syncthreads();
+    const float4 v = stage[wr][lane];
+    if (w_in < s.rows) {
+      d0[32 * i] = v;
+      d1[32 * i] = make_float4(v.x - round_bf16(v.x), v.y - round_bf16(v.y),
+                               v.z - round_bf16(v.z), v.w - round_bf16(v.w));
+    }
+    __syncthreads();
   }
 }
 
-// Results of those tokens in the storage type; tokens of no sequence keep
-// what their rows held.  kValue: the value expansion v = W_UV[h] o_lat happens
-// here (widths that the tensor-core product does not take; its CUDA-core
-// counterpart walks all tokens in one warp), else `x` holds v already.  grid
-// (tokens, head blocks of eight), a warp per head.
-template <typename T, bool kValue>
-__global__ void __launch_bounds__(256) chunk_store_kernel(int t0, int H, int d_c, int d_v,
-                                                          const int* state, const float* x,
-                                                          const T* w_uv, const float* lse_in,
-                                                          T* out, float* lse) {
-  const int i = blockIdx.x, st = state[i];
+// Results of the slab's tokens in the storage type; tokens of no sequence keep
+// what their rows held.  x: v of both parts of o where the tensor-core product
+// takes these widths, else (kValue) o itself, expanded here.  grid (tokens, head
+// blocks of eight), a warp per head.
+template <bool kValue>
+__global__ void __launch_bounds__(256) few_store_kernel(int n, int H, int d_v, const int* state,
+                                                        const float* x, const __nv_bfloat16* w_uv,
+                                                        const float* lse_in, __nv_bfloat16* out,
+                                                        float* lse) {
+  const int t = blockIdx.x, st = state[t];
   const int h = blockIdx.y * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
   if (st == kNone || h >= H) return;
-  const size_t at = (size_t)i * H + h, row = (size_t)(t0 + i) * H + h;
-  if (lse && lane == 0) lse[row] = st == kBad ? kNaN : lse_in[at];
-  if (kValue && st == kLive) {
-    const float* o = x + at * d_c;
+  const size_t at = (size_t)t * H + h;
+  if (lse && lane == 0) lse[at] = st == kBad ? kNaN : lse_in[at];
+  if (st == kBad) {
+    for (int d = lane; d < d_v; d += 32) out[at * d_v + d] = __float2bfloat16_rn(kNaN);
+  } else if (kValue) {
+    const float* o = x + at * fw::kDc;
     for (int d = 0; d < d_v; ++d) {
-      const T* w = w_uv + ((size_t)h * d_v + d) * d_c;
+      const __nv_bfloat16* w = w_uv + ((size_t)h * d_v + d) * fw::kDc;
       float s = 0.f;
-      for (int c = lane; c < d_c; c += 32) s = fmaf(to_f(w[c]), o[c], s);
+      for (int c = lane; c < fw::kDc; c += 32) s = fmaf(to_f(w[c]), o[c], s);
 #pragma unroll
       for (int k = 16; k; k >>= 1) s += __shfl_xor_sync(0xffffffffu, s, k);
-      if (lane == 0) out[row * d_v + d] = from_f<T>(s);
+      if (lane == 0) out[at * d_v + d] = __float2bfloat16_rn(s);
     }
   } else {
+    const float* rest = x + (size_t)n * H * d_v;
     for (int d = lane; d < d_v; d += 32)
-      out[row * d_v + d] = from_f<T>(st == kBad ? kNaN : x[at * d_v + d]);
+      out[at * d_v + d] = __float2bfloat16_rn(x[at * d_v + d] + rest[at * d_v + d]);
   }
 }
 
@@ -551,9 +711,9 @@ bool value_tc(const mla_dims_t* d) {
   return d->dtype == MLA_BF16 && d->d_v % 128 == 0 && d->d_c % 64 == 0;
 }
 
-// rows that mla_decode takes on the tensor cores
+// rows of the absorbed route; query parts in 16-byte words
 bool decodable(const mla_dims_t* d) {
-  return d->dtype == MLA_BF16 && d->d_c == ck::kDc && d->d_r == ck::kDr;
+  return d->dtype == MLA_BF16 && d->d_c == ck::kDc && d->d_r == ck::kDr && d->d_n % 8 == 0;
 }
 
 struct Layout {
@@ -561,10 +721,12 @@ struct Layout {
   // expanded
   int cap, heads, groups;      // page entries; heads per launch; launches
   long long rows_cap;
-  size_t plan, seq, items, pages, kr, k, v;
+  size_t k, v;
+  // both
+  size_t plan, seq, items, pages, kr;
   // absorbed
-  int slab;
-  size_t table, segs, q_nope, q_rope, rot, pos, state, q_abs, o_lat, lse, vf, ws, ws_bytes;
+  int slab, max_streams;       // tokens of a pass; streams of a pass at most
+  size_t few_plan, streams, state, q_nope, q_rope, rot, q_abs, partial, partial_lse, o, lse, vf;
   size_t total;
 };
 
@@ -592,44 +754,49 @@ bool make_layout(const mla_dims_t* d, int B, int n_tok, int n_ver, int max_pages
   l->expanded = chunk_route(d, B, n_tok, max_rows);
   l->generic = !decodable(d);
   const size_t es = d->dtype == MLA_BF16 ? 2 : 4;
+  if (l->generic) {
+    if (generic_smem(d, n_ver) > 48 * 1024 || d->H > 65535) return false;
+    take(256);        // it needs none; an empty workspace is not told from an error
+    l->total = at;
+    return true;
+  }
+  // page entries, an even number a sequence
+  const long long cap = ((max_rows + kPage - 1) / kPage + B + 3) / 4 * 4;
+  l->cap = (int)cap;
+  l->plan = take(sizeof(ChunkPlan));
+  l->seq = take(sizeof(int) * (3 * (size_t)B + 2));
+  l->items = take(sizeof(ck::Item) * ((size_t)n_tok / ck::kItemTokens + B));
+  l->pages = take(sizeof(PageEntry) * (size_t)cap);
+  l->kr = take((size_t)cap * kPage * ck::kDr * 2);
   if (l->expanded) {
-    // an even number of pages a sequence
-    const long long cap = ((max_rows + kPage - 1) / kPage + B + 3) / 4 * 4;
     l->rows_cap = cap * kPage;
     const size_t head = (size_t)l->rows_cap * (ck::kDn + ck::kDv) * 2;
     int hg = (int)std::min<size_t>(d->H, std::max<size_t>(1, ((size_t)1 << 30) / head));
     l->groups = (d->H + hg - 1) / hg;
     l->heads = (d->H + l->groups - 1) / l->groups;
     if (l->rows_cap * l->heads + 4 * kPage > INT32_MAX) return false;
-    l->cap = (int)cap;
-    l->plan = take(sizeof(ChunkPlan));
-    l->seq = take(sizeof(int) * (3 * (size_t)B + 2));
-    l->items = take(sizeof(ck::Item) * ((size_t)n_tok / ck::kItemTokens + B));
-    l->pages = take(sizeof(PageEntry) * (size_t)cap);
-    l->kr = take((size_t)l->rows_cap * ck::kDr * 2);
     l->k = take((size_t)l->rows_cap * l->heads * ck::kDn * 2);
     l->v = take((size_t)l->rows_cap * l->heads * ck::kDv * 2);
-  } else if (l->generic) {
-    if (generic_smem(d, n_ver) > 48 * 1024 || d->H > 65535) return false;
-    take(256);        // it needs none; an empty workspace is not told from an error
   } else {
-    // tokens per pass: 32768 query rows of heads, which bounds the workspace
+    // tokens per pass: 32768 (token, head) rows, which bounds the workspace
     l->slab = std::min(n_tok, std::max(1, 32768 / d->H));
-    const size_t n = l->slab, row = d->d_c + d->d_r;
-    l->table = take(n * max_pages * 4);
-    l->segs = take(n * max_segs * sizeof(mla_seg_t));
-    l->q_nope = take(n * d->H * d->d_n * es);
-    l->q_rope = take(n * d->H * d->d_r * es);
-    l->rot = take(n * 4);
-    l->pos = take(n * 4);
+    const size_t n = l->slab, rows = n * d->H;
+    const int pairs = current_sms() / 2;
+    if (pairs == 0) return false;
+    l->max_streams = (int)(rows / fw::kRows) + B;
+    l->few_plan = take(sizeof(fw::Plan));
+    l->streams = take(sizeof(fw::Stream) * (size_t)l->max_streams);
     l->state = take(n * 4);
-    l->q_abs = take(n * n_ver * d->H * row * es);
-    l->o_lat = take(n * d->H * d->d_c * 4);
-    l->lse = take(n * d->H * 4);
-    l->vf = take(value_tc(d) ? n * d->H * d->d_v * 4 : 0);
-    l->ws_bytes = mla_decode_workspace_size(d, l->slab, 1, n_ver, d->H);
-    if (l->ws_bytes == 0) return false;
-    l->ws = take(l->ws_bytes);
+    l->q_nope = take(rows * d->d_n * es);
+    l->q_rope = take(rows * d->d_r * es);
+    l->rot = take(n * 4);
+    l->q_abs = take(rows * fw::kWidth * es);
+    const size_t slots = (size_t)pairs + l->max_streams;
+    l->partial = take(slots * fw::kRows * fw::kDc * 4);
+    l->partial_lse = take(slots * fw::kRows * 4);
+    l->o = take(2 * rows * fw::kDc * 4);
+    l->lse = take(rows * 4);
+    l->vf = take(value_tc(d) ? 2 * rows * d->d_v * 4 : 0);
   }
   l->total = at;
   return true;
@@ -674,10 +841,10 @@ mla_status_t run_expanded(const mla_dims_t* d, const ChunkArgs& a, const Layout&
                            ck::kSmemBytes) != cudaSuccess)
     return MLA_ERR_CUDA;
 
-  chunk_plan_kernel<<<1, kPlanThreads, 0, st>>>(a, l.cap, plan, reinterpret_cast<int*>(ws + l.seq),
-                                                items, pages);
+  chunk_plan_kernel<false><<<1, kPlanThreads, 0, st>>>(
+      a, FewPlan{}, l.cap, plan, reinterpret_cast<int*>(ws + l.seq), items, pages);
   if (cudaGetLastError() != cudaSuccess) return MLA_ERR_CUDA;
-  if (launch_dependent(chunk_rotary_kernel, dim3(l.cap + d->H * ck::kDv / 64), dim3(256), 0, st, true,
+  if (launch_dependent(chunk_rotary_kernel<true>, dim3(l.cap + d->H * ck::kDv / 64), dim3(256), 0, st, true,
                        a, l.cap, plan, static_cast<const PageEntry*>(pages),
                        static_cast<const __nv_bfloat16*>(w_uv), kr) != cudaSuccess)
     return MLA_ERR_CUDA;
@@ -731,46 +898,95 @@ mla_status_t run_generic(const mla_dims_t* d, const ChunkArgs& a, const void* w_
 }
 
 mla_status_t run_absorbed(const mla_dims_t* d, const ChunkArgs& a, const Layout& l, uint8_t* ws,
-                          const void* w_uk, const void* w_uv, void* v, float* lse, cudaStream_t st) {
-  using T = __nv_bfloat16;
-  int32_t* table = reinterpret_cast<int32_t*>(ws + l.table);
-  mla_seg_t* segs = reinterpret_cast<mla_seg_t*>(ws + l.segs);
-  T* q_nope = reinterpret_cast<T*>(ws + l.q_nope);
-  T* q_rope = reinterpret_cast<T*>(ws + l.q_rope);
-  int32_t* rot = reinterpret_cast<int32_t*>(ws + l.rot);
-  int32_t* pos = reinterpret_cast<int32_t*>(ws + l.pos);
+                          const void* w_uk, const void* w_uv, void* v, float* lse,
+                          cudaStream_t st) {
+  const int pairs = current_sms() / 2;
+  if (!pairs) return MLA_ERR_CUDA;
+  ChunkPlan* cplan = reinterpret_cast<ChunkPlan*>(ws + l.plan);
+  int* seq = reinterpret_cast<int*>(ws + l.seq);
+  PageEntry* pages = reinterpret_cast<PageEntry*>(ws + l.pages);
+  __nv_bfloat16* kr = reinterpret_cast<__nv_bfloat16*>(ws + l.kr);
+  fw::Plan* plan = reinterpret_cast<fw::Plan*>(ws + l.few_plan);
+  fw::Stream* streams = reinterpret_cast<fw::Stream*>(ws + l.streams);
   int* state = reinterpret_cast<int*>(ws + l.state);
-  float* o_lat = reinterpret_cast<float*>(ws + l.o_lat);
+  int32_t* rot = reinterpret_cast<int32_t*>(ws + l.rot);
+  float* o = reinterpret_cast<float*>(ws + l.o);
   float* lse_t = reinterpret_cast<float*>(ws + l.lse);
   float* vf = reinterpret_cast<float*>(ws + l.vf);
   mla_stream_t ms = reinterpret_cast<mla_stream_t>(st);
+
+  fw::Params p;
+  p.plan = plan;
+  p.streams = streams;
+  p.pages = pages;
+  p.H = d->H;
+  p.rotary_moved = 0;
+  for (int i = 0; i < a.n_ver; ++i) p.rotary_moved |= a.delta[i] != 0;
+  p.scale = d->scale;
+  p.scale_log2 = d->scale * fw::kLog2e;
+  p.partial = reinterpret_cast<float*>(ws + l.partial);
+  p.partial_lse = reinterpret_cast<float*>(ws + l.partial_lse);
+  fw::Maps mp;
+  const uint64_t cache_rows = (uint64_t)a.n_pages * kPage;
+  const uint64_t c_ext[3] = {64, cache_rows, fw::kWidth / 64};
+  const uint64_t c_str[2] = {(uint64_t)fw::kWidth * 2, 128};
+  const uint32_t c_box[3] = {64, kPage, 4};
+  if (!map_rows(&mp.c, a.cache, fw::kWidth, cache_rows, fw::kWidth, kPage) ||
+      !map_bf16(&mp.c4, a.cache, 3, c_ext, c_str, c_box) ||
+      !map_rows(&mp.kr, kr, fw::kDr, (uint64_t)l.cap * kPage, fw::kDr, kPage))
+    return MLA_ERR_CUDA;
+  if (cudaFuncSetAttribute(fw::few_attn_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           fw::kSmemBytes) != cudaSuccess)
+    return MLA_ERR_CUDA;
+  const __nv_bfloat16* wv = static_cast<const __nv_bfloat16*>(w_uv);
   for (int t0 = 0; t0 < a.n_tok; t0 += l.slab) {
-    const int n = std::min(l.slab, a.n_tok - t0);
-    const dim3 grid(n, (d->H + 7) / 8);
-    const int es = (int)sizeof(T);
-    if (d->d_n * es % 16 == 0 && d->d_r * es % 16 == 0)
-      chunk_spread_kernel<uint4><<<grid, 256, 0, st>>>(
-          a, t0, d->d_n * es / 16, d->d_r * es / 16, table, segs, reinterpret_cast<uint4*>(q_nope),
-          reinterpret_cast<uint4*>(q_rope), rot, pos, state);
-    else
-      chunk_spread_kernel<T><<<grid, 256, 0, st>>>(a, t0, d->d_n, d->d_r, table, segs, q_nope,
-                                                   q_rope, rot, pos, state);
+    const int n = std::min(l.slab, a.n_tok - t0), rows = n * d->H;
+    const dim3 by_head(n, (d->H + 7) / 8);
+    const __nv_bfloat16* q =
+        static_cast<const __nv_bfloat16*>(a.q) + (size_t)t0 * d->H * (d->d_n + d->d_r);
+    few_split_kernel<<<by_head, 256, 0, st>>>(
+        d->H, d->d_n / 8, d->d_r / 8, reinterpret_cast<const uint4*>(q),
+        reinterpret_cast<uint4*>(ws + l.q_nope), reinterpret_cast<uint4*>(ws + l.q_rope), rot);
     if (cudaGetLastError() != cudaSuccess) return MLA_ERR_CUDA;
-    mla_status_t rc = mla_absorb_q(d, n, q_nope, q_rope, rot, a.delta, a.n_ver, w_uk, ws + l.q_abs, ms);
+    const int32_t zero = 0;
+    mla_status_t rc =
+        mla_absorb_q(d, n, ws + l.q_nope, ws + l.q_rope, rot, &zero, 1, w_uk, ws + l.q_abs, ms);
     if (rc != MLA_OK) return rc;
-    rc = mla_decode(d, n, 1, ws + l.q_abs, a.n_ver, nullptr, d->H, a.cache, a.n_pages, table,
-                    a.max_pages, segs, a.max_segs, nullptr, nullptr, 0, pos, o_lat, lse_t,
-                    ws + l.ws, l.ws_bytes, ms);
-    if (rc != MLA_OK) return rc;
-    const T* wv = static_cast<const T*>(w_uv);
-    if (value_tc(d)) {
-      rc = mla_out_proj(d, n, o_lat, w_uv, nullptr, vf, nullptr, ms);
-      if (rc != MLA_OK) return rc;
-      chunk_store_kernel<T, false><<<grid, 256, 0, st>>>(t0, d->H, d->d_c, d->d_v, state, vf, wv,
-                                                         lse_t, static_cast<T*>(v), lse);
+    const FewPlan few = {t0, n, pairs, plan, streams, state};
+    if (t0 == 0) {
+      if (launch_dependent(chunk_plan_kernel<true>, dim3(1), dim3(kPlanThreads), 0, st, true, a, few,
+                           l.cap, cplan, seq, reinterpret_cast<ck::Item*>(ws + l.items),
+                           pages) != cudaSuccess)
+        return MLA_ERR_CUDA;
+      if (p.rotary_moved &&
+          launch_dependent(chunk_rotary_kernel<false>, dim3(l.cap), dim3(256), 0, st, true, a, l.cap,
+                           cplan, static_cast<const PageEntry*>(pages), wv, kr) != cudaSuccess)
+        return MLA_ERR_CUDA;
     } else {
-      chunk_store_kernel<T, true><<<grid, 256, 0, st>>>(t0, d->H, d->d_c, d->d_v, state, o_lat, wv,
-                                                        lse_t, static_cast<T*>(v), lse);
+      few_plan_kernel<<<1, kPlanThreads, 0, st>>>(a, few, seq, pages);
+      if (cudaGetLastError() != cudaSuccess) return MLA_ERR_CUDA;
+    }
+    p.q_pos = a.q_pos + t0;
+    if (!map_rows(&mp.q, ws + l.q_abs, fw::kWidth, rows, fw::kWidth, fw::kRows)) return MLA_ERR_CUDA;
+    if (launch_dependent(fw::few_attn_kernel, dim3(2 * pairs), dim3(fw::kThreads), fw::kSmemBytes,
+                         st, true, p, mp) != cudaSuccess ||
+        launch_dependent(few_combine_kernel, dim3(l.max_streams, fw::kRows / 8), dim3(256), 0, st, true,
+                         rows,
+                         static_cast<const fw::Plan*>(plan),
+                         static_cast<const fw::Stream*>(streams),
+                         static_cast<const float*>(p.partial),
+                         static_cast<const float*>(p.partial_lse), o, lse_t) != cudaSuccess)
+      return MLA_ERR_CUDA;
+    __nv_bfloat16* out = static_cast<__nv_bfloat16*>(v) + (size_t)t0 * d->H * d->d_v;
+    float* lse_out = lse ? lse + (size_t)t0 * d->H : nullptr;
+    if (value_tc(d)) {
+      rc = mla_out_proj(d, 2 * n, o, w_uv, nullptr, vf, nullptr, ms);
+      if (rc != MLA_OK) return rc;
+      few_store_kernel<false><<<by_head, 256, 0, st>>>(n, d->H, d->d_v, state, vf, wv, lse_t, out,
+                                                       lse_out);
+    } else {
+      few_store_kernel<true><<<by_head, 256, 0, st>>>(n, d->H, d->d_v, state, o, wv, lse_t, out,
+                                                      lse_out);
     }
     if (cudaGetLastError() != cudaSuccess) return MLA_ERR_CUDA;
   }
