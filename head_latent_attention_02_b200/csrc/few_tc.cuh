@@ -108,7 +108,7 @@ struct Bars {
   uint64_t v_full[kVSlots], v_empty[kVSlots];
   uint64_t x_full[2], x_empty[2];
   uint64_t s_full[2], p_full[2];
-  uint64_t o_done;      // P c of one more tile complete
+  uint64_t o_done[2];   // P c of one more even, odd tile complete
   uint64_t o_free;      // o of one more stream read
   uint64_t broken_set;  // the softmax warps have agreed on the broken rows of a tile
   uint32_t broken[2][2];  // those rows, a bit each: of this tile and, cleared, of the next
@@ -171,8 +171,8 @@ few_attn_kernel(const __grid_constant__ Params p, const __grid_constant__ Maps m
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bar->s_full[i], 1);
       mbar_init(&bar->p_full[i], 4);
+      mbar_init(&bar->o_done[i], 1);
     }
-    mbar_init(&bar->o_done, 1);
     mbar_init(&bar->o_free, 4);
     mbar_init(&bar->broken_set, 4);
     for (int i = 0; i < 4; ++i) bar->broken[i >> 1][i & 1] = 0;
@@ -268,13 +268,11 @@ few_attn_kernel(const __grid_constant__ Params p, const __grid_constant__ Maps m
         }
         return ok;
       };
-      // P c of every tile before the n-th complete.  A parity tells two phases
-      // apart only if the one before them is known to be over, and of the last
-      // two tiles neither is.
+      // P c of every tile before the n-th complete.  A parity tells a phase from
+      // its two neighbours: tile n - 3 is over (the scores of tile n - 1, whose
+      // weights were waited for, followed its product) and tile n + 1 is not begun.
       auto wait_done = [&](int n) {
-        if (n > 1) wait(&bar->o_done, n & 1);
-        if (n > 0) wait(&bar->o_done, (n - 1) & 1);
-        return ok;
+        return n == 0 || wait(&bar->o_done[(n - 1) & 1], ((n - 1) >> 1) & 1);
       };
       int nv = 0, nq = 0, n = 0;     // value slots taken; streams; tiles
       for (int u = u0, si = s0; ok && u < u1; ++si) {
@@ -338,7 +336,7 @@ few_attn_kernel(const __grid_constant__ Params p, const __grid_constant__ Maps m
             mma_bf16_ts_elect(tmem + kColO, pc + 8 * k, d + (k & 3) * (2048 >> 4), idesc_o,
                               (i | k) ? 1u : 0u);
           mma_commit_elect(&bar->v_empty[vs]);
-          mma_commit_elect(&bar->o_done);
+          mma_commit_elect(&bar->o_done[n & 1]);
         }
         ++nq;
       }
@@ -425,8 +423,9 @@ few_attn_kernel(const __grid_constant__ Params p, const __grid_constant__ Maps m
           l *= f;
           m = m_new;
           if (u > begin) {
-            // o is at rest (the scores at hand followed P c of tile n - 2)
-            if (!wait(&bar->o_done, (n - 1) & 1)) break;
+            // o is at rest once P c of tile n - 1 is done (of tile n - 3 it is: the
+            // scores at hand followed it; that of tile n waits for these weights)
+            if (!wait(&bar->o_done[(n - 1) & 1], ((n - 1) >> 1) & 1)) break;
             tc_fence_after();
 #pragma unroll 1
             for (int c = 0; c < kHalf; c += 32) {
@@ -461,8 +460,7 @@ few_attn_kernel(const __grid_constant__ Params p, const __grid_constant__ Maps m
       }
       if (!ok) break;
       // o of this run's share of the stream, normalised, with its log sum
-      if (n > 1) wait(&bar->o_done, n & 1);              // tile n - 2, then n - 1
-      if (!wait(&bar->o_done, (n - 1) & 1)) break;
+      if (!wait(&bar->o_done[(n - 1) & 1], ((n - 1) >> 1) & 1)) break;
       tc_fence_after();
       const int slot = pair + si;
       const bool none = l == 0.f;

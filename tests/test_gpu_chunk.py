@@ -318,6 +318,23 @@ def test_same_bits_every_time_on_any_workspace():
         assert torch.equal(c.v, v)
 
 
+@pytest.mark.parametrize("H,lens,past", [(128, [4] * 32, 64), (128, [6, 1] * 10, 130), (64, [8] * 16, 1024)])
+def test_many_short_sequences_again_and_again(H, lens, past):
+    """Runs of a CTA pair that change sequences every few pages."""
+    c = Case("bf16", H, lens, [past] * len(lens))
+    ws = c.workspace()
+    c.run(ws)
+    torch.cuda.synchronize()
+    v = c.v.clone()
+    for _ in range(10):
+        for _ in range(30):
+            c.run(ws)
+        torch.cuda.synchronize()
+        assert mla.get_status() == 0
+        assert torch.equal(c.v, v)
+    c.check(heads=[0, H - 1])
+
+
 def test_streams_and_replayed_graphs():
     cs = [Case("bf16", 8, [600], [500], seed=1), Case("bf16", 8, [600], [500], seed=2)]
     streams = [torch.cuda.Stream() for _ in cs]
