@@ -730,15 +730,24 @@ struct Layout {
   size_t total;
 };
 
-// Expanded when its estimated time is the lower one.  A row's expansion costs
-// 2 * 512 * 256 flops a head at about 1.1 PFLOP/s; a query, row and head
-// 2 * 320 flops at about 0.7 PFLOP/s expanded (in query tiles of 256, so a
-// sequence's tokens round up) and 2 * 1088 at about 0.45 PFLOP/s absorbed.
+// Expanded when its estimated time (microseconds) is the lower one.
+//   Expanded: a row's expansion costs 2 * 512 * 256 flops a head at 1.15 PFLOP/s;
+//   a query, row and head 2 * 320 at 0.7, in query tiles of 256, but no less than
+//   one item's way through a sequence, 1.9 us per 128 rows.
+//   Absorbed: a query, row and head 2 * 1088 at 0.65 PFLOP/s, 6 ns a query and
+//   head for partial sums and projections, 0.2 us a query for its own work.
+// Tokens a sequence at which the two take the same time, measured and by this
+// estimate, and that time (sequences x cached rows):
+//                1 x 4096        4 x 2048        16 x 1024       1 x 16384
+//   16 heads     80, 121;  93    25, 29;   88    18, 21;   168   200, 247; 304
+//   64 heads     64, 74;  138    53, 57;  269    37, 39;   560   114, 115; 470
+//   128 heads    78, 85;  271    63, 66;  510    48, 45;  1180   129, 120; 985
 bool chunk_route(const mla_dims_t* d, int B, int n_tok, long long max_rows) {
   if (!expandable(d)) return false;
-  const double rows = (double)max_rows, per = std::ceil((double)n_tok / B);
-  const double e = rows * 262144.0 / 1.1e15 + rows * std::ceil(per / 256) * 256 * 640.0 / 0.7e15;
-  const double s = rows * per * 2176.0 / 0.45e15;
+  const double rows = (double)max_rows, heads = d->H, per = std::ceil((double)n_tok / B);
+  const double e = 25 + rows * heads * 262144.0 / 1.15e9 +
+                   std::max(rows * heads * std::ceil(per / 256) * 256 * 640.0 / 0.7e9, rows / B / 128 * 1.9);
+  const double s = 40 + rows * per * heads * 2176.0 / 0.65e9 + n_tok * (heads * 0.006 + 0.2);
   return e < s;
 }
 
