@@ -129,7 +129,15 @@ __global__ void __launch_bounds__(256) linear_finish_kernel(const __grid_constan
   gm::tile_at(p, base + t, &mt, &nt);
   const int a = mt * gm::kPairRows + row, b = nt * wide + c0;    // operand rows
   if (p.swapped ? (a >= p.N || b >= p.M) : (a >= p.M || b >= p.N)) return;
-  float v[8] = {};
+  // the residual first: the stores may be to its own place
+  float v[8] = {}, r[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const int m = p.swapped ? b + j : a, n = p.swapped ? a : b + j;
+    r[j] = p.residual && m < p.M && n < p.N
+               ? __bfloat162float(p.residual[(long long)m * p.res_stride + n])
+               : 0.f;
+  }
 #pragma unroll 4
   for (int g = g0; g <= g1; ++g) {
     const int second = (long long)g * p.chunk < u0 ? 1 : 0;   // the tile starts inside the run
@@ -138,26 +146,24 @@ __global__ void __launch_bounds__(256) linear_finish_kernel(const __grid_constan
     for (int j = 0; j < 8; ++j) v[j] += s[(long long)j * gm::kPairRows];
   }
   const bool vec = !p.swapped && p.vec && b + 8 <= p.N;
-  const uint4* res = vec && p.residual ? reinterpret_cast<const uint4*>(
-                                             p.residual + (long long)a * p.res_stride + b)
-                                       : nullptr;
-  const uint4 u = res ? *res : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const int n = p.swapped ? a : b + j;
+    if (p.bias && n < p.N) v[j] += __ldg(p.bias + n);
+  }
+  gm::activate_all(v, p.act);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) v[j] += r[j];
+  if (vec) {
+    *reinterpret_cast<uint4*>(p.out + (long long)a * p.out_stride + b) =
+        make_uint4(pack2(v[0], v[1]), pack2(v[2], v[3]), pack2(v[4], v[5]), pack2(v[6], v[7]));
+    return;
+  }
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
     const int m = p.swapped ? b + j : a, n = p.swapped ? a : b + j;
-    if (m >= p.M || n >= p.N) break;
-    v[j] = gm::activate(v[j] + (p.bias ? __ldg(p.bias + n) : 0.f), p.act);
-    if (vec) {
-      const uint32_t w = j < 2 ? u.x : j < 4 ? u.y : j < 6 ? u.z : u.w;
-      v[j] += j & 1 ? hi_f(w) : lo_f(w);
-    } else {
-      if (p.residual) v[j] += __bfloat162float(p.residual[(long long)m * p.res_stride + n]);
-      p.out[(long long)m * p.out_stride + n] = __float2bfloat16_rn(v[j]);
-    }
+    if (m < p.M && n < p.N) p.out[(long long)m * p.out_stride + n] = __float2bfloat16_rn(v[j]);
   }
-  if (vec)
-    *reinterpret_cast<uint4*>(p.out + (long long)a * p.out_stride + b) =
-        make_uint4(pack2(v[0], v[1]), pack2(v[2], v[3]), pack2(v[4], v[5]), pack2(v[6], v[7]));
 }
 
 struct TilePlan {
