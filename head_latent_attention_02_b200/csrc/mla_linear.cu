@@ -10,6 +10,7 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cstdint>
 
 #include "mla.h"
@@ -175,8 +176,8 @@ struct TilePlan {
 // of the work is split along K.  Few rows of x: W takes the rows (its stream is
 // what the call costs) and the tile is as wide as x is high.  Otherwise the
 // shape with the least estimated time: a pair's step costs the larger of its
-// MMAs (2 NB BN clocks) and its operand loads at about 50 bytes a clock and SM;
-// a split costs a second launch and the partial sums' trip through memory; two
+// MMAs (2 NB BN clocks), its operand loads at about 50 bytes a clock and SM, and
+// the issuing warp's bookkeeping (300 clocks a step and 350 a panel); a split costs a second launch and the partial sums' trip through memory; two
 // column blocks cost an epilogue that little overlaps.
 TilePlan plan_tiles(int M, int N, int K, int sms) {
   TilePlan t = {};
@@ -195,7 +196,8 @@ TilePlan plan_tiles(int M, int N, int K, int sms) {
       if (nb == 2 && bn < 192) continue;
       const long long n_nt = (cols + nb * bn - 1) / (nb * bn), tiles = (long long)t.n_mt * n_nt;
       const double load = (gm::kRows + nb * bn / 2) * 128 / 50.0, mma = 2.0 * nb * bn;
-      const double step = t.P * (mma > load ? mma : load), tile = t.k_steps * step;
+      const double step = std::max(t.P * std::max(mma, load), 300.0 + 350.0 * t.P);
+      const double tile = t.k_steps * step;
       const long long rounds = tiles / pairs, left = tiles - rounds * pairs;
       // a run of at least eight steps of 64, so that a partial sum is worth its trip
       long long run = (left * t.k_steps + pairs - 1) / pairs;
