@@ -527,6 +527,7 @@ __global__ void __launch_bounds__(256) few_store_kernel(int n, int H, int d_v, c
                                                         const float* x, const __nv_bfloat16* w_uv,
                                                         const float* lse_in, __nv_bfloat16* out,
                                                         float* lse) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const int t = blockIdx.x, st = state[t];
   const int h = blockIdx.y * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
   if (st == kNone || h >= H) return;
@@ -554,39 +555,62 @@ __global__ void __launch_bounds__(256) few_store_kernel(int n, int H, int d_v, c
 // ------------------------------------------------------------ generic widths
 // One block per (token, head), any widths, fp32 arithmetic: the head's absorbed
 // query W_UK[h]^T q_nope and its rotary part turned by -delta[version] (in
-// shared memory, not rounded), an online softmax over chunks of 128 rows -- a
-// thread per row for the scores; (row group, channel) for the weighted sum,
-// so that narrow latents keep all threads at work -- and the value expansion.
-// A masked row is not read.  Bound by the latency of its chain (about 2 us a
-// chunk of rows).
+// shared memory, not rounded), an online softmax over chunks of 128 rows, and
+// the value expansion.  Scores: four threads a row, so that a load of a warp
+// touches eight rows and a thread's loads are all under way at once (a thread a
+// row waited 11 000 clocks a chunk of 48-wide rows for its line-by-line loads).
+// Weighted sum: (row group, channels), so that narrow latents keep all threads
+// at work.  kVec: four elements a load, for widths that are multiples of four.
+// A masked row is not read.  Bound by the latency of its chain: 8 heads, 75
+// tokens over up to 331 rows of 48 take 18.5 us (33 with a thread a row).
 constexpr int kGenThreads = 128;
 
-int generic_groups(int d_c) {
+int generic_groups(int d_c, bool vec) {
+  const int units = vec ? d_c / 4 : d_c;
   int wide = 1;
-  while (wide < d_c && wide < kGenThreads) wide *= 2;
+  while (wide < units && wide < kGenThreads) wide *= 2;
   return kGenThreads / wide;
 }
 
+bool generic_vec(const mla_dims_t* d) { return d->d_c % 4 == 0 && d->d_r % 4 == 0; }
+
 size_t generic_smem(const mla_dims_t* d, int n_ver) {
-  return sizeof(float) * ((size_t)n_ver * (d->d_c + d->d_r) + d->d_n + d->d_r +
-                          (size_t)generic_groups(d->d_c) * d->d_c + kGenThreads + 8) +
+  return sizeof(float) * ((size_t)(n_ver * (d->d_c + d->d_r) + d->d_n + d->d_r + 3) / 4 * 4 +
+                          (size_t)generic_groups(d->d_c, generic_vec(d)) * d->d_c + 2 * kGenThreads + 8) +
          sizeof(int) * kGenThreads;
 }
 
-template <typename T>
+// n consecutive elements, n = 4 (aligned to them) or 1
+template <int n, typename T>
+__device__ __forceinline__ void load_some(const T* src, float (&x)[n]) {
+  if constexpr (n == 1) {
+    x[0] = to_f(src[0]);
+  } else if constexpr (sizeof(T) == 4) {
+    const float4 u = *reinterpret_cast<const float4*>(src);
+    x[0] = u.x; x[1] = u.y; x[2] = u.z; x[3] = u.w;
+  } else {
+    const uint2 u = *reinterpret_cast<const uint2*>(src);
+    x[0] = lo_f(u.x); x[1] = hi_f(u.x); x[2] = lo_f(u.y); x[3] = hi_f(u.y);
+  }
+}
+
+template <typename T, bool kVec>
 __global__ void __launch_bounds__(kGenThreads) chunk_generic_kernel(
     const __grid_constant__ ChunkArgs a, int d_c, int groups, float scale, const T* w_uk,
     const T* w_uv, T* v, float* lse) {
-  extern __shared__ float sm_gen[];
+  constexpr int V = kVec ? 4 : 1;
+  extern __shared__ __align__(16) float sm_gen[];
   const int t = blockIdx.x, h = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int row = d_c + a.d_r;
   float* qa = sm_gen;                        // [n_ver][row]
   float* qn = qa + a.n_ver * row;            // [d_n + d_r]
-  float* acc = qn + a.d_n + a.d_r;           // [groups][d_c]
+  float* acc = sm_gen + (a.n_ver * row + a.d_n + a.d_r + 3) / 4 * 4;   // [groups][d_c]
   float* pw = acc + groups * d_c;            // [128] weights of the chunk
-  float* red = pw + kGenThreads;             // [8]
+  float* score = pw + kGenThreads;           // [128]
+  float* red = score + kGenThreads;          // [8]
   int* prow = reinterpret_cast<int*>(red + 8);   // [128] cache rows, -1: none
   __shared__ int s_b, s_bad;
+  __shared__ PageEntry s_page[2][2];         // the pages of this chunk and of the next one
   if (tid == 0) {
     s_b = -1;
     s_bad = 0;
@@ -603,6 +627,7 @@ __global__ void __launch_bounds__(kGenThreads) chunk_generic_kernel(
   for (int c = tid; c < d_c; c += kGenThreads) {
     const T* w = w_uk + (size_t)h * a.d_n * d_c + c;
     float s = 0.f;
+#pragma unroll 8
     for (int k = 0; k < a.d_n; ++k) s = fmaf(to_f(w[(size_t)k * d_c]), qn[k], s);
     for (int u = 0; u < a.n_ver; ++u) qa[u * row + c] = s;
   }
@@ -633,26 +658,48 @@ __global__ void __launch_bounds__(kGenThreads) chunk_generic_kernel(
   const T* cache = static_cast<const T*>(a.cache);
   const int qp = a.q_pos[t];
   const int wide = kGenThreads / groups;
+  auto list_pages = [&](int i) {             // the pages of the i-th chunk
+    if (tid >= 2) return;
+    PageEntry x = {0, 0, 0, 0};
+    if (2 * i + tid < np) page_at(a, b, 2 * i + tid, &x);
+    s_page[i & 1][tid] = x;
+  };
+  // row r of the chunk: its cache row, -1 where there is none that the token sees
+  auto row_of = [&](const PageEntry* pages, int r) {
+    const PageEntry& x = pages[r / kPage];
+    return r % kPage < x.n && (long long)x.kpos + r % kPage <= qp ? x.row + r % kPage : -1;
+  };
   float m = kNegInf, l = 0.f;
+  list_pages(0);
+  __syncthreads();
   for (int base = 0; base < np * kPage; base += kGenThreads) {
-    const int i = base + tid;
-    float s = kNegInf;
-    int phys = -1;
-    if (i < np * kPage && page_at(a, b, i / kPage, &e) && i % kPage < e.n &&
-        (long long)e.kpos + i % kPage <= qp) {
-      phys = e.row + i % kPage;
-      const T* r = cache + (size_t)phys * row;
-      const float* x = qa + e.ver * row;
-      float d0 = 0.f, d1 = 0.f;
-      int k = 0;
+    const PageEntry* pages = s_page[(base / kGenThreads) & 1];
+    list_pages(base / kGenThreads + 1);
+    const int part = tid & 3;
+#pragma unroll
+    for (int i = 0; i < kGenThreads / 32; ++i) {
+      const int at = i * 32 + tid / 4, phys = row_of(pages, at);
+      float d[V] = {};
+      if (phys >= 0) {
+        const T* r = cache + (size_t)phys * row;
+        const float* x = qa + pages[at / kPage].ver * row;
 #pragma unroll 4
-      for (; k + 1 < row; k += 2) {
-        d0 = fmaf(x[k], to_f(r[k]), d0);
-        d1 = fmaf(x[k + 1], to_f(r[k + 1]), d1);
+        for (int k = part * V; k < row; k += 4 * V) {
+          float y[V], z[V];
+          load_some<V>(r + k, y);
+          load_some<V>(x + k, z);
+#pragma unroll
+          for (int u = 0; u < V; ++u) d[u] = fmaf(z[u], y[u], d[u]);
+        }
       }
-      if (k < row) d0 = fmaf(x[k], to_f(r[k]), d0);
-      s = (d0 + d1) * scale;
+      float s = kVec ? (d[0] + d[V / 2]) + (d[V / 4] + d[V - 1]) : d[0];
+      s += __shfl_xor_sync(0xffffffffu, s, 1);
+      s += __shfl_xor_sync(0xffffffffu, s, 2);
+      if (part == 0) score[at] = s * scale;
     }
+    __syncthreads();
+    const int phys = row_of(pages, tid);
+    const float s = phys < 0 ? kNegInf : score[tid];
     // the chunk's maximum and sum; a NaN score makes the sum NaN
     float mx = s;
 #pragma unroll
@@ -671,12 +718,20 @@ __global__ void __launch_bounds__(kGenThreads) chunk_generic_kernel(
     const float f = m == kNegInf ? 0.f : expf(m - m_new);
     l = l * f + ((red[4] + red[5]) + (red[6] + red[7]));
     m = m_new;
-    for (int c = tid % wide; c < d_c; c += wide) {
-      float o = acc[(tid / wide) * d_c + c] * f;
-#pragma unroll 4
-      for (int k = tid / wide; k < kGenThreads; k += groups)
-        if (prow[k] >= 0) o = fmaf(pw[k], to_f(cache[(size_t)prow[k] * row + c]), o);
-      acc[(tid / wide) * d_c + c] = o;
+    for (int c = tid % wide * V; c < d_c; c += wide * V) {
+      float* o = acc + (tid / wide) * d_c + c;
+      float sum_c[V];
+#pragma unroll
+      for (int u = 0; u < V; ++u) sum_c[u] = o[u] * f;
+#pragma unroll 8
+      for (int k = tid / wide; k < kGenThreads; k += groups) {
+        float y[V] = {};
+        if (prow[k] >= 0) load_some<V>(cache + (size_t)prow[k] * row + c, y);
+#pragma unroll
+        for (int u = 0; u < V; ++u) sum_c[u] = fmaf(pw[k], y[u], sum_c[u]);
+      }
+#pragma unroll
+      for (int u = 0; u < V; ++u) o[u] = sum_c[u];
     }
     __syncthreads();
   }
@@ -763,8 +818,8 @@ bool make_layout(const mla_dims_t* d, int B, int n_tok, int n_ver, int max_pages
   l->expanded = chunk_route(d, B, n_tok, max_rows);
   l->generic = !decodable(d);
   const size_t es = d->dtype == MLA_BF16 ? 2 : 4;
-  if (l->generic) {
-    if (generic_smem(d, n_ver) > 48 * 1024 || d->H > 65535) return false;
+  if (l->generic) {        // 48 KB of shared memory, a little of it static
+    if (generic_smem(d, n_ver) > 48 * 1024 - 256 || d->H > 65535) return false;
     take(256);        // it needs none; an empty workspace is not told from an error
     l->total = at;
     return true;
@@ -900,8 +955,10 @@ mla_status_t run_expanded(const mla_dims_t* d, const ChunkArgs& a, const Layout&
 template <typename T>
 mla_status_t run_generic(const mla_dims_t* d, const ChunkArgs& a, const void* w_uk, const void* w_uv,
                          void* v, float* lse, cudaStream_t st) {
-  chunk_generic_kernel<T><<<dim3(a.n_tok, d->H), kGenThreads, generic_smem(d, a.n_ver), st>>>(
-      a, d->d_c, generic_groups(d->d_c), d->scale, static_cast<const T*>(w_uk),
+  const bool vec = generic_vec(d);
+  auto kernel = vec ? chunk_generic_kernel<T, true> : chunk_generic_kernel<T, false>;
+  kernel<<<dim3(a.n_tok, d->H), kGenThreads, generic_smem(d, a.n_ver), st>>>(
+      a, d->d_c, generic_groups(d->d_c, vec), d->scale, static_cast<const T*>(w_uk),
       static_cast<const T*>(w_uv), static_cast<T*>(v), lse);
   return cudaGetLastError() == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
 }
@@ -991,13 +1048,12 @@ mla_status_t run_absorbed(const mla_dims_t* d, const ChunkArgs& a, const Layout&
     if (value_tc(d)) {
       rc = mla_out_proj(d, 2 * n, o, w_uv, nullptr, vf, nullptr, ms);
       if (rc != MLA_OK) return rc;
-      few_store_kernel<false><<<by_head, 256, 0, st>>>(n, d->H, d->d_v, state, vf, wv, lse_t, out,
-                                                       lse_out);
-    } else {
-      few_store_kernel<true><<<by_head, 256, 0, st>>>(n, d->H, d->d_v, state, o, wv, lse_t, out,
-                                                      lse_out);
     }
-    if (cudaGetLastError() != cudaSuccess) return MLA_ERR_CUDA;
+    const float* x = value_tc(d) ? vf : o;
+    if (launch_dependent(value_tc(d) ? few_store_kernel<false> : few_store_kernel<true>, by_head, dim3(256), 0,
+                         st, true, n, d->H, d->d_v, static_cast<const int*>(state), x, wv,
+                         static_cast<const float*>(lse_t), out, lse_out) != cudaSuccess)
+      return MLA_ERR_CUDA;
   }
   return MLA_OK;
 }

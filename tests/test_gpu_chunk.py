@@ -159,6 +159,13 @@ def test_bf16_other_widths(d):
     Case("bf16", 3, [40, 2, 1], [100, 900, 0], 100, 1, d=d).run().check()
 
 
+@pytest.mark.parametrize("kind,d", [("bf16", dict(d_c=42, d_r=6, d_n=9, d_v=7)), ("bf16", dict(d_c=600, d_r=8, d_n=8, d_v=8)),
+                                    ("f32", dict(d_c=4, d_r=4, d_n=1, d_v=1)), ("f32", dict(d_c=516, d_r=2, d_n=3, d_v=2))])
+def test_generic_widths(kind, d):
+    """Rows of whole and of broken groups of four elements, narrow and wide ones."""
+    Case(kind, 2, [40, 2, 1], [200, 300, 0], 100, 1, d=d).run().check()
+
+
 LARGE = [
     ([256], [0], 0, 0), ([512], [128], 0, 0), ([513], [1], 0, 0), ([700], [63], 0, 5), ([1100], [1000], 0, 0),
     ([300, 0, 333, 290], [64, 700, 129, 5], 0, 7), ([400, 600], [700, 1500], 500, 0), ([257], [4000], 0, 0),
