@@ -125,11 +125,11 @@ chunk_attn_kernel(const __grid_constant__ Params p, const __grid_constant__ Maps
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   Bars* bar = reinterpret_cast<Bars*>(smem + kOffBar);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
 
   // the item list and the expanded rows are complete after this wait
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const bool half = values_as_half(p.plan);
+  const bool half = uniform(values_as_half(p.plan));
   const int item = blockIdx.x >> 1;
   const int rank = (int)cluster_ctarank();
   if (item >= p.plan->n_items) return;       // both CTAs of the pair
@@ -194,7 +194,7 @@ chunk_attn_kernel(const __grid_constant__ Params p, const __grid_constant__ Maps
   cluster_sync();       // the peer's barriers are ready
   tc_fence_after();
   const uint32_t tmem = bar->tmem_base;
-  const int nt0 = bar->n_tiles[0], nt1 = bar->n_tiles[1];
+  const int nt0 = uniform(bar->n_tiles[0]), nt1 = uniform(bar->n_tiles[1]);
   const int nt = max(nt0, nt1);
 
   if (warp < 4) {

@@ -154,7 +154,7 @@ few_attn_kernel(const __grid_constant__ Params p, const __grid_constant__ Maps m
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   Bars* bar = reinterpret_cast<Bars*>(smem + kOffBar);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
   const int pair = blockIdx.x >> 1, half = blockIdx.x & 1;
 
   if (threadIdx.x == 0) {

@@ -210,7 +210,7 @@ gemm_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtensorMa
   const int NB = p.NB, b_bytes = P * b_panel;      // one column block of B
   const int stage = a_bytes + NB * b_bytes;
   Bars* bar = reinterpret_cast<Bars*>(smem + S * stage);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
   const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
 

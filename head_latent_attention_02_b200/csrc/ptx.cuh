@@ -95,6 +95,11 @@ __device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity
   return true;
 }
 
+// The warp's value of x, in a form that the compiler knows to be the same in all
+// lanes: what depends on it alone may stay in uniform registers, where the
+// operands of an MMA have to be.
+__device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
+
 // ------------------------------------------------------------------ cluster
 __device__ __forceinline__ uint32_t cluster_ctarank() {
   uint32_t r;
