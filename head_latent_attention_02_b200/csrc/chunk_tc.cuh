@@ -243,7 +243,7 @@ chunk_attn_kernel(const __grid_constant__ Params p, const __grid_constant__ Maps
       if (rank == 0 && nt > 0) {        // the whole warp, converged
         constexpr uint32_t idesc_s = idesc_bf16_f32(kPairTile, kKTile, false, false);
         constexpr uint32_t idesc_pv = idesc_bf16_f32(kPairTile, kDv, false, true);
-      const uint32_t idesc_o = half ? idesc_half_f32(idesc_pv) : idesc_pv;
+        const uint32_t idesc_o = half ? idesc_half_f32(idesc_pv) : idesc_pv;
         // Descriptors of the first panels; a panel, a slot or a K step further is
         // an addition (16-byte units) that never leaves the address field.  The
         // issuing warp shares its scheduler with softmax warps: building each

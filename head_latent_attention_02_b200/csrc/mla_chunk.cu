@@ -575,7 +575,8 @@ int generic_groups(int d_c, bool vec) {
 bool generic_vec(const mla_dims_t* d) { return d->d_c % 4 == 0 && d->d_r % 4 == 0; }
 
 size_t generic_smem(const mla_dims_t* d, int n_ver) {
-  return sizeof(float) * ((size_t)(n_ver * (d->d_c + d->d_r) + d->d_n + d->d_r + 3) / 4 * 4 +
+  const size_t row = (size_t)d->d_c + d->d_r, query = n_ver * row + d->d_n + d->d_r;
+  return sizeof(float) * ((query + 3) / 4 * 4 +
                           (size_t)generic_groups(d->d_c, generic_vec(d)) * d->d_c + 2 * kGenThreads + 8) +
          sizeof(int) * kGenThreads;
 }
@@ -1088,7 +1089,7 @@ extern "C" mla_status_t mla_chunk_attn(const mla_dims_t* dims, int32_t B, int32_
   if (!chunk_dims_ok(dims) || B < 0 || n_tok < 0 || n_ver < 1 || !delta || n_pages < 1 ||
       max_pages < 1 || max_segs < 1 || max_rows < 0)
     return MLA_ERR_INVALID_ARG;
-  if (dims->page_size != kPage || n_ver > kMaxVersions || n_pages * kPage + 2 * kPage > INT32_MAX ||
+  if (dims->page_size != kPage || n_ver > kMaxVersions || n_pages > INT32_MAX / kPage - 2 ||
       (long long)max_pages * kPage > INT32_MAX || max_rows > INT32_MAX)
     return MLA_ERR_UNSUPPORTED;
   if (B == 0 || n_tok == 0) return MLA_OK;

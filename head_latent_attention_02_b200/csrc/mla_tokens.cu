@@ -338,7 +338,8 @@ __global__ void __launch_bounds__(kTokThreads) append_tokens_kernel(
     inv = (A)1 / sqrt(ss / (A)a.d_c + (A)a.eps);
   }
   const size_t row = (size_t)page * kPage + slot;
-  const int row_bytes = kLow ? (a.d_c * a.bits_c + a.d_r * 4) / 8 : (a.d_c + a.d_r) * (int)sizeof(T);
+  const size_t row_bytes = kLow ? (size_t)(a.d_c * a.bits_c + a.d_r * 4) / 8
+                                : ((size_t)a.d_c + a.d_r) * sizeof(T);
   uint8_t* dst = static_cast<uint8_t*>(a.cache) + row * row_bytes;
   T* dst_t = reinterpret_cast<T*>(dst);
   const bool vec_out = a.d_c % 8 == 0 && (reinterpret_cast<uintptr_t>(dst) & 15) == 0;
@@ -484,14 +485,14 @@ extern "C" mla_status_t mla_append_tokens(const mla_dims_t* dims, int32_t B, int
                                           int64_t n_pages, const int32_t* block_table,
                                           int32_t max_pages, mla_stream_t stream) {
   if (!rotary_dims_ok(dims) || dims->d_c < 1 || B < 0 || n_tok < 0 || n_axes < 1 || !sections ||
-      n_pages < 1 || max_pages < 1 || kv_stride < dims->d_c + dims->d_r)
+      n_pages < 1 || max_pages < 1 || kv_stride < (int64_t)dims->d_c + dims->d_r)
     return MLA_ERR_INVALID_ARG;
   if (norm_weight && !(norm_eps >= 0.f)) return MLA_ERR_INVALID_ARG;
   if (dims->page_size != kPage || n_axes > kMaxAxes || dims->d_r > 2 * kMaxPairs)
     return MLA_ERR_UNSUPPORTED;
   const bool low = bits_c != 0 || bits_r != 0;
-  if (low && (!((bits_c == 4 || bits_c == 2) && bits_r == 4) || (dims->d_c * bits_c) % 32 != 0 ||
-              (dims->d_r * bits_r) % 32 != 0))
+  if (low && (!((bits_c == 4 || bits_c == 2) && bits_r == 4) || dims->d_c % (32 / bits_c) != 0 ||
+              dims->d_r % 8 != 0 || dims->d_c > INT32_MAX / 8))
     return MLA_ERR_UNSUPPORTED;
   if (low != (scale_c != nullptr) || low != (scale_r != nullptr)) return MLA_ERR_INVALID_ARG;
   Axes ax;

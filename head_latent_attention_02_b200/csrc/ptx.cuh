@@ -422,17 +422,6 @@ __device__ __forceinline__ void mma_pair_bf16_ss(uint32_t d_tmem, uint64_t a_des
       ::"r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate) : "memory");
 }
 
-// The pair's product with A read from tensor memory (each CTA's 128 rows from
-// its own) and B's columns from both CTAs' shared memory.
-__device__ __forceinline__ void mma_pair_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
-                                                 uint32_t idesc, uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
-      ::"r"(d_tmem), "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate) : "memory");
-}
-
 // Arrive on the barrier at this shared-memory offset in both CTAs of the pair
 // once every tcgen05 op issued so far by this thread has completed.
 __device__ __forceinline__ void mma_pair_commit_both(uint64_t* bar) {
@@ -588,6 +577,8 @@ __device__ __forceinline__ void mma_pair_bf16_ss_elect(uint32_t d_tmem, uint64_t
       "@q tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}"
       ::"r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate) : "memory");
 }
+// The pair's product with A read from tensor memory (each CTA's 128 rows from
+// its own) and B's columns from both CTAs' shared memory.
 __device__ __forceinline__ void mma_pair_bf16_ts_elect(uint32_t d_tmem, uint32_t a_tmem,
                                                        uint64_t b_desc, uint32_t idesc,
                                                        uint32_t accumulate) {

@@ -134,6 +134,15 @@ def test_chunk_limits_and_empty_call(L):
     assert _chunk(L, B=0, q=None, ts=None, q_pos=None, v=None, ws=None) == OK
 
 
+def test_sizes_whose_products_overflow(L):
+    assert _chunk(L, n_pages=1 << 58) == UNSUPPORTED
+    assert _chunk(L, n_pages=(1 << 63) - 1) == UNSUPPORTED
+    assert _append(L, dims=_dims(d_c=2 ** 31 - 8)) == INVALID      # rows longer than their stride
+    assert _append(L, dims=_dims(d_c=1 << 30), stride=1 << 31, bc=4, br=4, sc=FAKE, sr=FAKE) == UNSUPPORTED
+    f32 = dict(dtype=mla.MLA_F32, d_c=32)
+    assert _chunk(L, dims=_dims(**f32, d_r=1 << 30), n_ver=4, delta=_ints(0, 0, 0, 0)) == UNSUPPORTED
+
+
 def test_chunk_workspace_size(L):
     size = lambda d, B, n, rows, n_ver=1, mp=64, ms=1: L.mla_chunk_workspace_size(
         ctypes.byref(d), B, n, n_ver, mp, ms, rows)
