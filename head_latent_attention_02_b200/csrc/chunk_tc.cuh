@@ -77,6 +77,9 @@ struct Item {
   int tok0, n;   // tokens [tok0, tok0 + n), n <= 512
   int entry;     // first page entry of the sequence (even)
   int tiles;     // 128-row tiles of the sequence; -1: the sequence is invalid
+  // of each query tile: the tiles up to the last one that any of its queries
+  // sees, and the leading ones that every query sees whole
+  int need[2], full[2];
 };
 
 struct Params {
@@ -106,9 +109,6 @@ struct Bars {
   uint64_t s_full[2], o_full[2];
   uint64_t p_full[2][2];                       // query tile, half of the weights' columns
   uint32_t tmem_base;
-  int n_tiles[2];
-  int q_max[2], q_min[2];
-  int n_full[2];               // leading tiles that every query of the tile sees whole
 };
 static_assert(sizeof(Bars) <= 512, "barrier block too large");
 
@@ -153,10 +153,6 @@ chunk_attn_kernel(const __grid_constant__ Params p, const __grid_constant__ Maps
       mbar_init(&bar->p_full[t][0], 8);    // four softmax warps of each CTA
       mbar_init(&bar->p_full[t][1], 8);
       mbar_init(&bar->o_full[t], 1);
-      bar->n_tiles[t] = 0;
-      bar->q_max[t] = INT32_MIN;
-      bar->q_min[t] = INT32_MAX;
-      bar->n_full[t] = INT32_MAX;
     }
     for (int i = 0; i < kKeySlots; ++i) {
       mbar_init(&bar->k_full[i], 1);
@@ -169,32 +165,12 @@ chunk_attn_kernel(const __grid_constant__ Params p, const __grid_constant__ Maps
     fence_mbar_init();
   }
   if (warp == 1) tmem_alloc_pair(&bar->tmem_base, kTmemCols);
-  __syncthreads();
-  // the tiles that each query tile needs (up to the last one that any of its
-  // queries sees) and the leading ones that need no mask
-  for (int i = threadIdx.x; i < it.n; i += kThreads) {
-    const int qp = p.q_pos[it.tok0 + i];
-    atomicMax(&bar->q_max[i / kPairTile], qp);
-    atomicMin(&bar->q_min[i / kPairTile], qp);
-  }
-  __syncthreads();
-  for (int j = threadIdx.x; j < it.tiles; j += kThreads) {
-    const PageEntry e0 = p.pages[it.entry + 2 * j], e1 = p.pages[it.entry + 2 * j + 1];
-#pragma unroll
-    for (int t = 0; t < 2; ++t) {
-      if (t * kPairTile >= it.n) continue;
-      if (visible(e0, bar->q_max[t]) > 0 || visible(e1, bar->q_max[t]) > 0)
-        atomicMax(&bar->n_tiles[t], j + 1);
-      if (visible(e0, bar->q_min[t]) < kPage || visible(e1, bar->q_min[t]) < kPage)
-        atomicMin(&bar->n_full[t], j);
-    }
-  }
   tc_fence_before();
   __syncthreads();
   cluster_sync();       // the peer's barriers are ready
   tc_fence_after();
   const uint32_t tmem = bar->tmem_base;
-  const int nt0 = uniform(bar->n_tiles[0]), nt1 = uniform(bar->n_tiles[1]);
+  const int nt0 = uniform(it.need[0]), nt1 = uniform(it.need[1]);
   const int nt = max(nt0, nt1);
 
   if (warp < 4) {
@@ -322,7 +298,7 @@ chunk_attn_kernel(const __grid_constant__ Params p, const __grid_constant__ Maps
     bool ok = true;
     if (mine > 0) {
       const PageEntry* pe = p.pages + it.entry;
-      const int n_full = bar->n_full[t];
+      const int n_full = it.full[t];
       for (int j = 0; j < mine; ++j) {
         int v0 = kPage, v1 = kPage;
         if (j >= n_full) {

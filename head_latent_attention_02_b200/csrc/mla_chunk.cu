@@ -367,22 +367,60 @@ __device__ __forceinline__ float row_norm_sq(const __nv_bfloat16* row, int part)
   return a + __shfl_xor_sync(0xffffffffu, a, 2);
 }
 
+// need and full of query tile t of an item, by 256 threads.
+__device__ void item_tiles(const ChunkArgs& a, ck::Item& item, int t, const PageEntry* pages) {
+  __shared__ int q_max, q_min, need, full;
+  if (threadIdx.x == 0) {
+    q_max = INT32_MIN;
+    q_min = INT32_MAX;
+    need = 0;
+    full = INT32_MAX;
+  }
+  __syncthreads();
+  const int first = t * ck::kPairTile, n = min(item.n - first, ck::kPairTile);
+  for (int i = threadIdx.x; i < n; i += 256) {
+    const int qp = a.q_pos[item.tok0 + first + i];
+    atomicMax(&q_max, qp);
+    atomicMin(&q_min, qp);
+  }
+  __syncthreads();
+  if (n > 0)
+    for (int j = threadIdx.x; j < item.tiles; j += 256) {
+      const PageEntry e0 = pages[item.entry + 2 * j], e1 = pages[item.entry + 2 * j + 1];
+      if (ck::visible(e0, q_max) > 0 || ck::visible(e1, q_max) > 0) atomicMax(&need, j + 1);
+      if (ck::visible(e0, q_min) < kPage || ck::visible(e1, q_min) < kPage) atomicMin(&full, j);
+    }
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    item.need[t] = need;
+    item.full[t] = full;
+  }
+}
+
 // Blocks [0, cap): rotary keys of the listed pages at their request positions,
 // kr[64 e + r] = R(delta[version]) k_rope of page entry e's row r (a plain copy
 // where delta is zero; rows without data are zeros), and the largest norm of
 // the rows' latents.  The blocks after them: the largest norm of 64 rows of
 // W_UV each.  The latents and weights read here are read again by the expansion,
-// from L2.  256 threads, four a row.  (Without kNorms, the rotary keys alone.)
+// from L2.  256 threads, four a row.  The last blocks: what each query tile of an
+// item sees (ck::Item::need and full), once for all heads: as a part of the
+// attention's own prologue it took 2 us of every 30 us item of a short context.
+// (Without kNorms, the rotary keys alone.)
 template <bool kNorms>
 __global__ void __launch_bounds__(256) chunk_rotary_kernel(const __grid_constant__ ChunkArgs a,
                                                            int cap, ChunkPlan* plan,
                                                            const PageEntry* pages,
                                                            const __nv_bfloat16* w_uv,
-                                                           __nv_bfloat16* kr) {
+                                                           __nv_bfloat16* kr, ck::Item* items) {
   asm volatile("griddepcontrol.launch_dependents;");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   __shared__ double2 cs[ck::kDr / 2];
   const int r = threadIdx.x >> 2, part = threadIdx.x & 3;
+  if (kNorms && (int)blockIdx.x >= cap + a.H * ck::kDv / 64) {
+    const int k = blockIdx.x - cap - a.H * ck::kDv / 64;
+    if (k / 2 < plan->n_items) item_tiles(a, items[k / 2], k & 1, pages);
+    return;
+  }
   if ((int)blockIdx.x >= cap) {
     const float sq =
         row_norm_sq(w_uv + ((size_t)(blockIdx.x - cap) * 64 + r) * ck::kDc, part);
@@ -909,9 +947,11 @@ mla_status_t run_expanded(const mla_dims_t* d, const ChunkArgs& a, const Layout&
   chunk_plan_kernel<false><<<1, kPlanThreads, 0, st>>>(
       a, FewPlan{}, l.cap, plan, reinterpret_cast<int*>(ws + l.seq), items, pages);
   if (cudaGetLastError() != cudaSuccess) return MLA_ERR_CUDA;
-  if (launch_dependent(chunk_rotary_kernel<true>, dim3(l.cap + d->H * ck::kDv / 64), dim3(256), 0, st, true,
-                       a, l.cap, plan, static_cast<const PageEntry*>(pages),
-                       static_cast<const __nv_bfloat16*>(w_uv), kr) != cudaSuccess)
+  const int max_items = a.n_tok / ck::kItemTokens + a.B;
+  if (launch_dependent(chunk_rotary_kernel<true>,
+                       dim3(l.cap + d->H * ck::kDv / 64 + 2 * max_items), dim3(256), 0, st, true, a,
+                       l.cap, plan, static_cast<const PageEntry*>(pages),
+                       static_cast<const __nv_bfloat16*>(w_uv), kr, items) != cudaSuccess)
     return MLA_ERR_CUDA;
 
   ex::Params g;
@@ -929,7 +969,6 @@ mla_status_t run_expanded(const mla_dims_t* d, const ChunkArgs& a, const Layout&
   p.scale_log2 = d->scale * ck::kLog2e;
   p.v = static_cast<__nv_bfloat16*>(v);
   p.lse = lse;
-  const int max_items = a.n_tok / ck::kItemTokens + a.B;
   for (int h0 = 0; h0 < d->H; h0 += l.heads) {
     const int nh = std::min(l.heads, d->H - h0);
     const uint64_t w_rows = (uint64_t)nh * ck::kDn;
@@ -1027,7 +1066,8 @@ mla_status_t run_absorbed(const mla_dims_t* d, const ChunkArgs& a, const Layout&
         return MLA_ERR_CUDA;
       if (p.rotary_moved &&
           launch_dependent(chunk_rotary_kernel<false>, dim3(l.cap), dim3(256), 0, st, true, a, l.cap,
-                           cplan, static_cast<const PageEntry*>(pages), wv, kr) != cudaSuccess)
+                           cplan, static_cast<const PageEntry*>(pages), wv, kr,
+                           static_cast<ck::Item*>(nullptr)) != cudaSuccess)
         return MLA_ERR_CUDA;
     } else {
       few_plan_kernel<<<1, kPlanThreads, 0, st>>>(a, few, seq, pages);
