@@ -229,7 +229,7 @@ def chunk_problem(dims: mla.Dims, w_uk, w_uv, w_o, cache, block_table, segs, del
     """Allocates the outputs and workspaces of run_chunk for these sizes."""
     n_tok, B = q_pos.shape[0], row0.shape[0]
     dev, dt = cache.device, cache.dtype
-    v = torch.zeros((n_tok, dims.H, dims.d_v), dtype=dt, device=dev)   # padded tokens stay zero
+    v = torch.empty((n_tok, dims.H, dims.d_v), dtype=dt, device=dev)
     out = torch.empty((n_tok, w_o.shape[0]), dtype=dt, device=dev)
     size = mla.chunk_workspace_size(dims, B, n_tok, len(deltas), block_table.shape[1], segs.shape[1],
                                     max_rows)
@@ -240,6 +240,12 @@ def chunk_problem(dims: mla.Dims, w_uk, w_uv, w_o, cache, block_table, segs, del
                         list(deltas), max_rows, tok_start, row0, q_pos, pos, list(sections), v, out,
                         torch.empty(size, dtype=torch.uint8, device=dev),
                         torch.empty(max(linear, 256), dtype=torch.uint8, device=dev))
+
+
+def _torch_stream(stream) -> torch.cuda.Stream:
+    if stream is None:
+        return torch.cuda.current_stream()
+    return stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(mla._s(stream))
 
 
 def run_chunk(p: ChunkProblem, q: torch.Tensor, kv: torch.Tensor, residual=None, stream=None):
@@ -255,6 +261,9 @@ def run_chunk(p: ChunkProblem, q: torch.Tensor, kv: torch.Tensor, residual=None,
         mla.append_tokens(p.dims, kv, p.tok_start, p.row0, p.pos, p.sections, p.cache, p.block_table,
                           norm_weight=p.norm_weight, norm_eps=p.norm_eps, stream=stream)
     with _nvtx("mla_chunk_attn"):
+        # rows that no sequence owns now may hold the values of an earlier batch
+        with torch.cuda.stream(_torch_stream(stream)):
+            p.v.zero_()
         mla.chunk_attn(p.dims, q, p.tok_start, p.q_pos, p.w_uk, p.w_uv, p.cache, p.block_table, p.segs,
                        p.deltas, p.max_rows, p.v, p.workspace, stream=stream)
     with _nvtx("mla_linear"):

@@ -449,3 +449,24 @@ def test_a_layer_over_two_chunks(kind, lens, past, sections):
             pos += 5
             p = runner.chunk_problem(c.dims, c.w_uk, c.w_uv, w_o, c.cache, c.bt, c.segs, c.deltas, c.max_rows,
                                      c.ts, _i32(past), c.q_pos, pos, sections, norm_weight=norm)
+
+
+@pytest.mark.parametrize("side", [False, True])
+def test_a_padded_batch_after_a_full_one(side):
+    """The same problem with fewer live tokens: those left out project zeros, not the values that the
+    batch before left in their rows."""
+    c = Case("f32", 2, [20, 12], [70, 3])
+    g = torch.Generator(device="cuda").manual_seed(5)
+    rn = lambda *s: torch.randn(*s, device="cuda", generator=g)
+    p = runner.chunk_problem(c.dims, c.w_uk, c.w_uv, rn(48, 2 * c.d["d_v"]), c.cache, c.bt, c.segs, c.deltas,
+                             c.max_rows, c.ts, _i32([70, 3]), c.q_pos, c.q_pos[None].clone(), [8])
+    stream = torch.cuda.Stream() if side else None
+    for live in (32, 24):
+        c.ts[2] = live
+        q, kv, res = rn(c.n, 2, 32), rn(c.n, 48), rn(c.n, 48)
+        torch.cuda.synchronize()
+        out = runner.run_chunk(p, q, kv, residual=res, stream=stream)
+        torch.cuda.synchronize()
+        assert mla.get_status() == 0
+        assert torch.equal(out[live:], res[live:])
+        assert not torch.equal(out[live - 1], res[live - 1])
