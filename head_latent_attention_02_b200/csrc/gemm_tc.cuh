@@ -30,6 +30,9 @@
 // this one's MMAs are issued (850 clocks a step before, 640 after, where the
 // step's MMAs take 128 for 64 columns: 256 x 2048 x 2048 18.7 to 14.8 us).
 //
+// Measured: 4096 x 7168 x 16384 with residual 606 us alone (1.59 PFLOP/s); 16 x
+// 7168 x 16384 42 us (5.6 TB/s of weights) and 6 us for the second launch.
+//
 // Every wait is bounded and records MLA_ERR_TIMEOUT when it gives up.
 #pragma once
 #include <cuda.h>
