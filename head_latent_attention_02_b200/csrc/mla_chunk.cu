@@ -7,7 +7,7 @@
 //              rotary keys moved to their request positions, and the direct
 //              form attends over them (chunk_tc.cuh).  For chunks.
 //   absorbed   few tokens over those rows (few_tc.cuh), between mla_absorb_q and
-//              the value expansion of mla_out_proj.
+//              a value expansion that joins the shares of split sequences.
 //   generic    fp32 and other widths: one kernel on the CUDA cores.
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -54,7 +54,8 @@ __device__ int sequence_pages(const ChunkArgs& a, int b) {
   for (int s = 0; s < a.max_segs; ++s) {
     const int rb = sg[s].row_begin, re = sg[s].row_end;
     if (re == rb) continue;
-    if (rb < prev_end || re < rb || rb % kPage != 0 || (long long)re > (long long)a.max_pages * kPage ||
+    if (rb < prev_end || re < rb || rb % kPage != 0 ||
+        (long long)re > (long long)a.max_pages * kPage ||
         sg[s].q_version < 0 || sg[s].q_version >= a.n_ver ||
         (long long)sg[s].key_pos_base + (re - rb) > (long long)INT32_MAX + 1)
       return -1;
@@ -175,7 +176,8 @@ struct FewPlan {
   int* state;
 };
 
-__device__ void plan_few(const ChunkArgs& a, const FewPlan& f, const int* seq, const PageEntry* pages) {
+__device__ void plan_few(const ChunkArgs& a, const FewPlan& f, const int* seq,
+                         const PageEntry* pages) {
   const int slab0 = f.slab0, slab_n = f.slab_n, pairs = f.pairs;
   fw::Plan* plan = f.plan;
   fw::Stream* streams = f.streams;
@@ -487,106 +489,181 @@ __global__ void __launch_bounds__(256) few_split_kernel(int H, int w_n, int w_r,
   for (int k = lane; k < w_r; k += 32) q_rope[at * w_r + k] = src[w_n + k];
 }
 
-// The shares of every (token, head) row merged by log-sum-exp, and what the
-// rounding to bf16 leaves of the result: o [n, H, 512], then the rest [n, H,
-// 512], so that the value expansion, which rounds its input, takes both.
-// grid (streams at most, 16), 256 threads: eight rows of a stream, a thread per
-// (row, four columns) and 128-column block; the shares of eight rows of one
-// column group are 128 contiguous bytes.  Rows that no stream holds are left
-// out: their results are not stored.
-__global__ void __launch_bounds__(256) few_combine_kernel(int n_rows, const fw::Plan* plan,
-                                                          const fw::Stream* streams,
-                                                          const float* partial,
-                                                          const float* partial_lse, float* o,
-                                                          float* lse) {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  __shared__ float4 stage[8][33];
-  const int si = blockIdx.x;
-  if (si >= plan->n_streams) return;
-  const fw::Stream s = streams[si];
-  const int r = threadIdx.x & 7, in = blockIdx.y * 8 + r, c = threadIdx.x >> 3;
-  if ((int)blockIdx.y * 8 >= s.rows) return;
-  const int g0 = s.tiles > 0 ? s.off / plan->chunk : 0;
-  const int g1 = s.tiles > 0 ? (s.off + s.tiles - 1) / plan->chunk : -1;
-  float top = kNegInf;
-  bool nan = false;
-  for (int g = g0; g <= g1; ++g) {
-    const float x = partial_lse[(size_t)(g + si) * fw::kRows + in];
-    nan = nan || x != x;
-    top = fmaxf(top, x);
-  }
-  if (nan) top = kNaN;
-  float4 acc[4] = {};
-  float tot = 0.f;
-  if (top != kNegInf && in < s.rows) {
-#pragma unroll 4
-    for (int g = g0; g <= g1; ++g) {
-      const float w = __expf(partial_lse[(size_t)(g + si) * fw::kRows + in] - top);
-      const float4* src = reinterpret_cast<const float4*>(partial) +
-                          (size_t)(g + si) * (fw::kDc / 4) * fw::kRows + in;
-      tot += w;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float4 v = src[(size_t)(32 * i + c) * fw::kRows];
-        acc[i].x = fmaf(w, v.x, acc[i].x);
-        acc[i].y = fmaf(w, v.y, acc[i].y);
-        acc[i].z = fmaf(w, v.z, acc[i].z);
-        acc[i].w = fmaf(w, v.w, acc[i].w);
-      }
-    }
-  }
-  const float inv = tot == 0.f ? 0.f : 1.f / tot;
-  if (c == 0 && in < s.rows) lse[s.q_row + in] = tot == 0.f ? kNegInf : top + logf(tot);
-  // 128 columns of the eight rows at a time, turned so that a row's are written
-  // together
-  const int wr = threadIdx.x >> 5, lane = threadIdx.x & 31, w_in = blockIdx.y * 8 + wr;
-  float4* d0 = reinterpret_cast<float4*>(o + (size_t)(s.q_row + w_in) * fw::kDc) + lane;
-  float4* d1 = d0 + (size_t)n_rows * (fw::kDc / 4);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    stage[r][c] = make_float4(acc[i].x * inv, acc[i].y * inv, acc[i].z * inv, acc[i].w * inv);
-    __syncthreads();
-    const float4 v = stage[wr][lane];
-    if (w_in < s.rows) {
-      d0[32 * i] = v;
-      d1[32 * i] = make_float4(v.x - round_bf16(v.x), v.y - round_bf16(v.y),
-                               v.z - round_bf16(v.z), v.w - round_bf16(v.w));
-    }
-    __syncthreads();
-  }
+// The shares of a row merged by log-sum-exp and the value expansion, in one
+// launch: block (head, 16 tokens), 512 threads.
+//   Join, a warp per token: a lane per share for the weights, then a lane per four
+//   columns of 128.  o is kept as two bf16 (its rounding and what that leaves).
+//   v = W_UV[h] o: 16 x 8 products of 16 (mma.sync: with 16 rows the weights'
+//   stream is what they cost), a warp for two groups of eight value channels and
+//   half of the latent's.  The order of the 32 channels of a step does not matter as
+//   long as both operands have the same: a lane takes eight consecutive ones of its
+//   row of either, so that a load is 16 bytes and feeds two products; a pitch of 16
+//   words modulo 32 keeps the rows of a load of shared memory apart.
+// Tokens of no sequence keep what their rows held.  Join, library-wide value product
+// and store as three launches took 424 us for 512 tokens of 64 heads over 1000 rows
+// each, attention included, where this takes 286, and 43 for 16 where it takes 38.
+constexpr int kFvTokens = 16, kFvThreads = 512, kFvPitch = fw::kDc + 32;
+
+// o in two parts; weights of the shares, later the sums of eight warps
+size_t few_value_smem(int pairs) {
+  return sizeof(__nv_bfloat16) * 2 * kFvTokens * kFvPitch +
+         std::max(sizeof(float) * kFvTokens * (size_t)pairs, sizeof(float4) * 16 * 32);
 }
 
-// Results of the slab's tokens in the storage type; tokens of no sequence keep
-// what their rows held.  x: v of both parts of o where the tensor-core product
-// takes these widths, else (kValue) o itself, expanded here.  grid (tokens, head
-// blocks of eight), a warp per head.
-template <bool kValue>
-__global__ void __launch_bounds__(256) few_store_kernel(int n, int H, int d_v, const int* state,
-                                                        const float* x, const __nv_bfloat16* w_uv,
-                                                        const float* lse_in, __nv_bfloat16* out,
-                                                        float* lse) {
+__device__ __forceinline__ void mma_16x8x16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                            uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__global__ void __launch_bounds__(kFvThreads) few_value_kernel(
+    int n, int H, int d_v, int pairs, const fw::Plan* plan, const fw::Stream* streams,
+    const int* state, const float* partial, const float* partial_lse, const __nv_bfloat16* w_uv,
+    __nv_bfloat16* out, float* lse) {
+  extern __shared__ __align__(16) uint8_t sm_fv[];
+  __nv_bfloat16* o_hi = reinterpret_cast<__nv_bfloat16*>(sm_fv);       // [16][pitch]
+  __nv_bfloat16* o_lo = o_hi + kFvTokens * kFvPitch;
+  float* weight = reinterpret_cast<float*>(o_lo + kFvTokens * kFvPitch);   // [16][pairs]
+  const int h = blockIdx.x, t0 = blockIdx.y * kFvTokens;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int t = blockIdx.x, st = state[t];
-  const int h = blockIdx.y * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-  if (st == kNone || h >= H) return;
-  const size_t at = (size_t)t * H + h;
-  if (lse && lane == 0) lse[at] = st == kBad ? kNaN : lse_in[at];
-  if (st == kBad) {
-    for (int d = lane; d < d_v; d += 32) out[at * d_v + d] = __float2bfloat16_rn(kNaN);
-  } else if (kValue) {
-    const float* o = x + at * fw::kDc;
-    for (int d = 0; d < d_v; ++d) {
-      const __nv_bfloat16* w = w_uv + ((size_t)h * d_v + d) * fw::kDc;
-      float s = 0.f;
-      for (int c = lane; c < fw::kDc; c += 32) s = fmaf(to_f(w[c]), o[c], s);
+  const int n_streams = plan->n_streams, run = plan->chunk;
+  {
+    const int i = warp, t = t0 + i;
+    float4 acc[4] = {};
+    if (t < n && state[t] == kLive) {
+      const int r = t * H + h;
+      // the last stream that starts at or before the row holds it
+      int si = -1, of_these = 32;
+      for (int j = 0; j < n_streams && of_these == 32; j += 32) {
+        of_these = __popc(__ballot_sync(
+            0xffffffffu, j + lane < n_streams && streams[min(j + lane, n_streams - 1)].q_row <= r));
+        si += of_these;
+      }
+      const fw::Stream s = streams[si];
+      const int in = r - s.q_row;
+      const int g0 = s.tiles > 0 ? s.off / run : 0;
+      const int ng = s.tiles > 0 ? (s.off + s.tiles - 1) / run - g0 + 1 : 0;
+      const float* ls = partial_lse + (size_t)(g0 + si) * fw::kRows + in;
+      float top = kNegInf;
+      bool nan = false;
+      for (int g = lane; g < ng; g += 32) {
+        const float x = ls[(size_t)g * fw::kRows];
+        nan = nan || x != x;
+        top = fmaxf(top, x);
+      }
 #pragma unroll
-      for (int k = 16; k; k >>= 1) s += __shfl_xor_sync(0xffffffffu, s, k);
-      if (lane == 0) out[at * d_v + d] = __float2bfloat16_rn(s);
+      for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+      if (__any_sync(0xffffffffu, nan)) top = kNaN;
+      float tot = 0.f;
+      if (top != kNegInf)
+        for (int g = lane; g < ng; g += 32) {
+          const float w = __expf(ls[(size_t)g * fw::kRows] - top);
+          weight[i * pairs + g] = w;
+          tot += w;
+        }
+#pragma unroll
+      for (int d = 16; d; d >>= 1) tot += __shfl_xor_sync(0xffffffffu, tot, d);
+      __syncwarp();
+      if (lse && lane == 0) lse[r] = tot == 0.f ? kNegInf : top + logf(tot);
+      if (tot != 0.f) {
+        const float4* src = reinterpret_cast<const float4*>(partial) +
+                            ((size_t)(g0 + si) * (fw::kDc / 4) + lane) * fw::kRows + in;
+#pragma unroll 4
+        for (int g = 0; g < ng; ++g) {
+          const float w = weight[i * pairs + g];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const float4 x = src[((size_t)g * (fw::kDc / 4) + 32 * c) * fw::kRows];
+            acc[c].x = fmaf(w, x.x, acc[c].x);
+            acc[c].y = fmaf(w, x.y, acc[c].y);
+            acc[c].z = fmaf(w, x.z, acc[c].z);
+            acc[c].w = fmaf(w, x.w, acc[c].w);
+          }
+        }
+        const float inv = 1.f / tot;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          acc[c].x *= inv;
+          acc[c].y *= inv;
+          acc[c].z *= inv;
+          acc[c].w *= inv;
+        }
+      }
+    } else if (t < n && state[t] == kBad && lse && lane == 0) {
+      lse[(size_t)t * H + h] = kNaN;
     }
-  } else {
-    const float* rest = x + (size_t)n * H * d_v;
-    for (int d = lane; d < d_v; d += 32)
-      out[at * d_v + d] = __float2bfloat16_rn(x[at * d_v + d] + rest[at * d_v + d]);
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      const float4 x = acc[c];
+      const uint32_t w0 = pack2(x.x, x.y), w1 = pack2(x.z, x.w);
+      const int at = i * kFvPitch + 128 * c + 4 * lane;
+      *reinterpret_cast<uint2*>(o_hi + at) = make_uint2(w0, w1);
+      *reinterpret_cast<uint2*>(o_lo + at) =
+          make_uint2(pack2(x.x - lo_f(w0), x.y - hi_f(w0)), pack2(x.z - lo_f(w1), x.w - hi_f(w1)));
+    }
+  }
+  __syncthreads();
+
+  const int row = lane >> 2, part = lane & 3;
+  const __nv_bfloat16* a_hi = o_hi + row * kFvPitch + 8 * part;
+  const __nv_bfloat16* a_lo = o_lo + row * kFvPitch + 8 * part;
+  auto words = [](const __nv_bfloat16* p) { return *reinterpret_cast<const uint4*>(p); };
+  const int first = warp >> 3 ? fw::kDc / 2 : 0;      // latent channels of this warp
+  float4* other = reinterpret_cast<float4*>(weight);  // the upper half's sums
+  for (int j0 = 0; j0 < (d_v + 7) / 8; j0 += 16) {
+    const int c0 = 8 * (j0 + (warp & 7));             // value channels c0 .. + 7, c0 + 64 .. + 7
+    const __nv_bfloat16* w[2];
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+      w[u] = w_uv + ((size_t)h * d_v + min(c0 + 64 * u + row, d_v - 1)) * fw::kDc + 8 * part;
+    float d[2][4] = {};
+    if (c0 < d_v) {
+#pragma unroll 4
+      for (int k = first; k < first + fw::kDc / 2; k += 32) {
+        const uint4 b[2] = {words(w[0] + k), words(w[1] + k)};
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          const __nv_bfloat16* a = (half ? a_lo : a_hi) + k;
+          const uint4 x = words(a), y = words(a + 8 * kFvPitch);
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            mma_16x8x16(d[u], x.x, y.x, x.y, y.y, b[u].x, b[u].y);
+            mma_16x8x16(d[u], x.z, y.z, x.w, y.w, b[u].z, b[u].w);
+          }
+        }
+      }
+    }
+    __syncthreads();
+    if (warp >= 8) {
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+        other[(2 * (warp & 7) + u) * 32 + lane] = make_float4(d[u][0], d[u][1], d[u][2], d[u][3]);
+    }
+    __syncthreads();
+    if (warp >= 8) continue;
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const float4 x = other[(2 * warp + u) * 32 + lane];
+      const float y[4] = {d[u][0] + x.x, d[u][1] + x.y, d[u][2] + x.z, d[u][3] + x.w};
+      const int c = c0 + 64 * u + 2 * part;
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        const int t = t0 + row + 8 * half;
+        const int st = t < n ? state[t] : kNone;
+        if (st == kNone) continue;
+        __nv_bfloat16* o = out + ((size_t)t * H + h) * d_v + c;
+        const float y0 = st == kBad ? kNaN : y[2 * half], y1 = st == kBad ? kNaN : y[2 * half + 1];
+        if (c + 1 < d_v && d_v % 2 == 0) *reinterpret_cast<uint32_t*>(o) = pack2(y0, y1);
+        else if (c < d_v) {
+          o[0] = __float2bfloat16_rn(y0);
+          if (c + 1 < d_v) o[1] = __float2bfloat16_rn(y1);
+        }
+      }
+    }
   }
 }
 
@@ -615,7 +692,8 @@ bool generic_vec(const mla_dims_t* d) { return d->d_c % 4 == 0 && d->d_r % 4 == 
 size_t generic_smem(const mla_dims_t* d, int n_ver) {
   const size_t row = (size_t)d->d_c + d->d_r, query = n_ver * row + d->d_n + d->d_r;
   return sizeof(float) * ((query + 3) / 4 * 4 +
-                          (size_t)generic_groups(d->d_c, generic_vec(d)) * d->d_c + 2 * kGenThreads + 8) +
+                          (size_t)generic_groups(d->d_c, generic_vec(d)) * d->d_c +
+                          2 * kGenThreads + 8) +
          sizeof(int) * kGenThreads;
 }
 
@@ -800,11 +878,6 @@ bool expandable(const mla_dims_t* d) {
          d->d_v == ck::kDv;
 }
 
-// widths of the tensor-core value product (mla_out_proj)
-bool value_tc(const mla_dims_t* d) {
-  return d->dtype == MLA_BF16 && d->d_v % 128 == 0 && d->d_c % 64 == 0;
-}
-
 // rows of the absorbed route; query parts in 16-byte words
 bool decodable(const mla_dims_t* d) {
   return d->dtype == MLA_BF16 && d->d_c == ck::kDc && d->d_r == ck::kDr && d->d_n % 8 == 0;
@@ -820,7 +893,7 @@ struct Layout {
   size_t plan, seq, items, pages, kr;
   // absorbed
   int slab, max_streams;       // tokens of a pass; streams of a pass at most
-  size_t few_plan, streams, state, q_nope, q_rope, rot, q_abs, partial, partial_lse, o, lse, vf;
+  size_t few_plan, streams, state, q_nope, q_rope, rot, q_abs, partial, partial_lse;
   size_t total;
 };
 
@@ -828,20 +901,21 @@ struct Layout {
 //   Expanded: a row's expansion costs 2 * 512 * 256 flops a head at 1.15 PFLOP/s;
 //   a query, row and head 2 * 320 at 0.7, in query tiles of 256, but no less than
 //   one item's way through a sequence, 1.9 us per 128 rows.
-//   Absorbed: a query, row and head 2 * 1088 at 0.65 PFLOP/s, 6 ns a query and
-//   head for partial sums and projections, 0.2 us a query for its own work.
+//   Absorbed: a query, row and head 2 * 1088 at 0.76 PFLOP/s, 6 ns a query and
+//   head for partial sums and projections, 0.04 us a query for its own work.
 // Tokens a sequence at which the two take the same time, measured and by this
 // estimate, and that time (sequences x cached rows):
 //                1 x 4096        4 x 2048        16 x 1024       1 x 16384
-//   16 heads     80, 121;  93    25, 29;   88    18, 21;   168   200, 247; 304
-//   64 heads     64, 74;  138    53, 57;  269    37, 39;   560   114, 115; 470
-//   128 heads    78, 85;  271    63, 66;  510    48, 45;  1180   129, 120; 985
+//   16 heads     150, 202; 93    63, 54; 88      48, 39; 165     288, 329; 302
+//   64 heads     82, 94; 137     76, 75; 264     55, 51; 545     125, 138; 458
+//   128 heads    90, 101; 268    73, 79; 500     57, 53; 1150    135, 141; 970
 bool chunk_route(const mla_dims_t* d, int B, int n_tok, long long max_rows) {
   if (!expandable(d)) return false;
   const double rows = (double)max_rows, heads = d->H, per = std::ceil((double)n_tok / B);
   const double e = 25 + rows * heads * 262144.0 / 1.15e9 +
-                   std::max(rows * heads * std::ceil(per / 256) * 256 * 640.0 / 0.7e9, rows / B / 128 * 1.9);
-  const double s = 40 + rows * per * heads * 2176.0 / 0.65e9 + n_tok * (heads * 0.006 + 0.2);
+                   std::max(rows * heads * std::ceil(per / 256) * 256 * 640.0 / 0.7e9,
+                            rows / B / 128 * 1.9);
+  const double s = 38 + rows * per * heads * 2176.0 / 0.76e9 + n_tok * (heads * 0.006 + 0.04);
   return e < s;
 }
 
@@ -897,9 +971,6 @@ bool make_layout(const mla_dims_t* d, int B, int n_tok, int n_ver, int max_pages
     const size_t slots = (size_t)pairs + l->max_streams;
     l->partial = take(slots * fw::kRows * fw::kDc * 4);
     l->partial_lse = take(slots * fw::kRows * 4);
-    l->o = take(2 * rows * fw::kDc * 4);
-    l->lse = take(rows * 4);
-    l->vf = take(value_tc(d) ? 2 * rows * d->d_v * 4 : 0);
   }
   l->total = at;
   return true;
@@ -1016,9 +1087,6 @@ mla_status_t run_absorbed(const mla_dims_t* d, const ChunkArgs& a, const Layout&
   fw::Stream* streams = reinterpret_cast<fw::Stream*>(ws + l.streams);
   int* state = reinterpret_cast<int*>(ws + l.state);
   int32_t* rot = reinterpret_cast<int32_t*>(ws + l.rot);
-  float* o = reinterpret_cast<float*>(ws + l.o);
-  float* lse_t = reinterpret_cast<float*>(ws + l.lse);
-  float* vf = reinterpret_cast<float*>(ws + l.vf);
   mla_stream_t ms = reinterpret_cast<mla_stream_t>(st);
 
   fw::Params p;
@@ -1074,26 +1142,18 @@ mla_status_t run_absorbed(const mla_dims_t* d, const ChunkArgs& a, const Layout&
       if (cudaGetLastError() != cudaSuccess) return MLA_ERR_CUDA;
     }
     p.q_pos = a.q_pos + t0;
-    if (!map_rows(&mp.q, ws + l.q_abs, fw::kWidth, rows, fw::kWidth, fw::kRows)) return MLA_ERR_CUDA;
+    if (!map_rows(&mp.q, ws + l.q_abs, fw::kWidth, rows, fw::kWidth, fw::kRows))
+      return MLA_ERR_CUDA;
     if (launch_dependent(fw::few_attn_kernel, dim3(2 * pairs), dim3(fw::kThreads), fw::kSmemBytes,
-                         st, true, p, mp) != cudaSuccess ||
-        launch_dependent(few_combine_kernel, dim3(l.max_streams, fw::kRows / 8), dim3(256), 0, st, true,
-                         rows,
-                         static_cast<const fw::Plan*>(plan),
-                         static_cast<const fw::Stream*>(streams),
-                         static_cast<const float*>(p.partial),
-                         static_cast<const float*>(p.partial_lse), o, lse_t) != cudaSuccess)
+                         st, true, p, mp) != cudaSuccess)
       return MLA_ERR_CUDA;
     __nv_bfloat16* out = static_cast<__nv_bfloat16*>(v) + (size_t)t0 * d->H * d->d_v;
     float* lse_out = lse ? lse + (size_t)t0 * d->H : nullptr;
-    if (value_tc(d)) {
-      rc = mla_out_proj(d, 2 * n, o, w_uv, nullptr, vf, nullptr, ms);
-      if (rc != MLA_OK) return rc;
-    }
-    const float* x = value_tc(d) ? vf : o;
-    if (launch_dependent(value_tc(d) ? few_store_kernel<false> : few_store_kernel<true>, by_head, dim3(256), 0,
-                         st, true, n, d->H, d->d_v, static_cast<const int*>(state), x, wv,
-                         static_cast<const float*>(lse_t), out, lse_out) != cudaSuccess)
+    if (launch_dependent(few_value_kernel, dim3(d->H, (n + kFvTokens - 1) / kFvTokens),
+                         dim3(kFvThreads), (int)few_value_smem(pairs), st, true, n, d->H, d->d_v, pairs,
+                         static_cast<const fw::Plan*>(plan), static_cast<const fw::Stream*>(streams),
+                         static_cast<const int*>(state), static_cast<const float*>(p.partial),
+                         static_cast<const float*>(p.partial_lse), wv, out, lse_out) != cudaSuccess)
       return MLA_ERR_CUDA;
   }
   return MLA_OK;
