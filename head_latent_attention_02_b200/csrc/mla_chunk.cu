@@ -6,8 +6,9 @@
 //              expanded once per call into the workspace (expand_tc.cuh), the
 //              rotary keys moved to their request positions, and the direct
 //              form attends over them (chunk_tc.cuh).  For chunks.
-//   absorbed   few tokens over those rows (few_tc.cuh), between mla_absorb_q and
-//              a value expansion that joins the shares of split sequences.
+//   absorbed   few tokens over those rows (few_tc.cuh), between the
+//              absorption of the queries and a value expansion that joins the
+//              shares of split sequences.
 //   generic    fp32 and other widths: one kernel on the CUDA cores.
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -474,19 +475,124 @@ __global__ void __launch_bounds__(256) chunk_rotary_kernel(const __grid_constant
 }
 
 // ------------------------------------------------------------ absorbed route
-// The queries' two parts as the absorption takes them, a zero rotation position
-// (they are rotated already).  grid (tokens, head blocks of eight), a warp
-// per head; w_n and w_r count 16-byte words.
-__global__ void __launch_bounds__(256) few_split_kernel(int H, int w_n, int w_r, const uint4* q,
-                                                        uint4* q_nope, uint4* q_rope,
-                                                        int32_t* rot_pos) {
-  const int t = blockIdx.x, h = blockIdx.y * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-  if (blockIdx.y == 0 && threadIdx.x == 0) rot_pos[t] = 0;
-  if (h >= H) return;
-  const size_t at = (size_t)t * H + h;
-  const uint4* src = q + at * (w_n + w_r);
-  for (int k = lane; k < w_n; k += 32) q_nope[at * w_n + k] = src[k];
-  for (int k = lane; k < w_r; k += 32) q_rope[at * w_r + k] = src[w_n + k];
+__device__ __forceinline__ void mma_16x8x16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                            uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// Four 8 x 8 tiles of 16-bit elements, a row address per lane (tile lane / 8).
+template <bool kTurned>
+__device__ __forceinline__ void load_tiles(const __nv_bfloat16* p, uint32_t (&x)[4]) {
+  if constexpr (kTurned)
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3]) : "r"(smem_u32(p)) : "memory");
+  else
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3]) : "r"(smem_u32(p)) : "memory");
+}
+
+// Absorbed queries q_abs[t, h] = [W_UK[h]^T q_nope | q_rope] (Day 27 tutorial "Move
+// the Key Projection Into the Query"; the rotary part is rotated already).  Block
+// (64 latent channels, head, 64 tokens), four warps of 16 channels each; W_UK[h]'s
+// rows are channels, so its tiles are turned on their way from shared memory
+// (mma.sync: for few tokens the weights' stream is what the product costs).  All
+// loads of a block are under way at once, and the small blocks of 16 tokens
+// and 128 heads fill every SM several times.  The decode's absorption takes its
+// queries in two arrays, which a launch before it had to split, and 128 tokens a
+// launch: with it a call over 1000 rows took 286 us for 512 tokens of 64 heads, 48
+// for 256 of 8 and 32 for one of 128 heads, this way 260, 37 and 34.
+constexpr int kFaThreads = 128, kFaTokens = 64, kFaCols = 64, kFaK = 128;
+constexpr int kFaPitchW = kFaCols + 8, kFaPitchQ = kFaK + 8;
+
+__global__ void __launch_bounds__(kFaThreads) few_absorb_kernel(int n, int H, int d_n,
+                                                                const __nv_bfloat16* q,
+                                                                const __nv_bfloat16* w_uk,
+                                                                __nv_bfloat16* q_abs) {
+  asm volatile("griddepcontrol.launch_dependents;");
+  __shared__ __align__(16) __nv_bfloat16 sw[kFaK * kFaPitchW], sq[kFaTokens * kFaPitchQ];
+  const int part = blockIdx.x, h = blockIdx.y, t0 = blockIdx.z * kFaTokens;
+  const int nt = min(kFaTokens, n - t0), mt = (nt + 15) / 16;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int width = d_n + fw::kDr;
+  const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+  float d[kFaTokens / 16][2][4] = {};
+  for (int k0 = 0; k0 < d_n; k0 += kFaK) {
+    const int kc = min(kFaK, d_n - k0), ks = (kc + 15) / 16;
+    // every load before the first store, which the compiler may not pass
+    constexpr int kW = kFaK * (kFaCols / 8) / kFaThreads, kQ = kFaTokens * (kFaK / 8) / kFaThreads;
+    uint4 xw[kW], xq[kQ];
+#pragma unroll
+    for (int u = 0; u < kW; ++u) {
+      const int i = threadIdx.x + u * kFaThreads, k = i / (kFaCols / 8), c = i % (kFaCols / 8) * 8;
+      xw[u] = k < kc ? *reinterpret_cast<const uint4*>(w_uk + ((size_t)h * d_n + k0 + k) * fw::kDc +
+                                                       part * kFaCols + c)
+                     : zero;
+    }
+#pragma unroll
+    for (int u = 0; u < kQ; ++u) {
+      const int i = threadIdx.x + u * kFaThreads, t = i / (kFaK / 8), k = i % (kFaK / 8) * 8;
+      xq[u] = t < nt && k < kc ? *reinterpret_cast<const uint4*>(
+                                     q + ((size_t)(t0 + t) * H + h) * width + k0 + k)
+                               : zero;
+    }
+    if (k0) __syncthreads();
+#pragma unroll
+    for (int u = 0; u < kW; ++u) {
+      const int i = threadIdx.x + u * kFaThreads, k = i / (kFaCols / 8), c = i % (kFaCols / 8) * 8;
+      *reinterpret_cast<uint4*>(sw + k * kFaPitchW + c) = xw[u];
+    }
+#pragma unroll
+    for (int u = 0; u < kQ; ++u) {
+      const int i = threadIdx.x + u * kFaThreads, t = i / (kFaK / 8), k = i % (kFaK / 8) * 8;
+      *reinterpret_cast<uint4*>(sq + t * kFaPitchQ + k) = xq[u];
+    }
+    __syncthreads();
+    const int in = lane & 7, lo = lane >> 3 & 1, hi = lane >> 4;
+#pragma unroll
+    for (int s = 0; s < kFaK / 16; ++s) {
+      if (s >= ks) break;
+      uint32_t b[4];
+      load_tiles<true>(sw + (16 * s + 8 * lo + in) * kFaPitchW + 16 * warp + 8 * hi, b);
+#pragma unroll
+      for (int m = 0; m < kFaTokens / 16; ++m) {
+        if (m >= mt) break;
+        uint32_t a[4];
+        load_tiles<false>(sq + (16 * m + 8 * lo + in) * kFaPitchQ + 16 * s + 8 * hi, a);
+        mma_16x8x16(d[m][0], a[0], a[1], a[2], a[3], b[0], b[1]);
+        mma_16x8x16(d[m][1], a[0], a[1], a[2], a[3], b[2], b[3]);
+      }
+    }
+  }
+  // through shared memory, so that a row's 128 bytes are written together
+  __syncthreads();
+#pragma unroll
+  for (int m = 0; m < kFaTokens / 16; ++m)
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      uint32_t* o = reinterpret_cast<uint32_t*>(
+          sw + (16 * m + 8 * half + (lane >> 2)) * kFaPitchW + 16 * warp + 2 * (lane & 3));
+      o[0] = pack2(d[m][0][2 * half], d[m][0][2 * half + 1]);
+      o[4] = pack2(d[m][1][2 * half], d[m][1][2 * half + 1]);
+    }
+  __syncthreads();
+#pragma unroll
+  for (int i = threadIdx.x; i < kFaTokens * (kFaCols / 8); i += kFaThreads) {
+    const int t = i / (kFaCols / 8), c = i % (kFaCols / 8) * 8;
+    if (t < nt)
+      *reinterpret_cast<uint4*>(q_abs + ((size_t)(t0 + t) * H + h) * fw::kWidth + part * kFaCols + c) =
+          *reinterpret_cast<const uint4*>(sw + t * kFaPitchW + c);
+  }
+  if (part == 0)
+    for (int i = threadIdx.x; i < nt * (fw::kDr / 8); i += kFaThreads) {
+      const size_t at = (size_t)(t0 + i / (fw::kDr / 8)) * H + h;
+      const int c = i % (fw::kDr / 8) * 8;
+      *reinterpret_cast<uint4*>(q_abs + at * fw::kWidth + fw::kDc + c) =
+          *reinterpret_cast<const uint4*>(q + at * width + d_n + c);
+    }
 }
 
 // The shares of a row merged by log-sum-exp and the value expansion, in one
@@ -508,15 +614,6 @@ constexpr int kFvTokens = 16, kFvThreads = 512, kFvPitch = fw::kDc + 32;
 size_t few_value_smem(int pairs) {
   return sizeof(__nv_bfloat16) * 2 * kFvTokens * kFvPitch +
          std::max(sizeof(float) * kFvTokens * (size_t)pairs, sizeof(float4) * 16 * 32);
-}
-
-__device__ __forceinline__ void mma_16x8x16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
-                                            uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
-      "{%8, %9}, {%0, %1, %2, %3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
 __global__ void __launch_bounds__(kFvThreads) few_value_kernel(
@@ -893,7 +990,7 @@ struct Layout {
   size_t plan, seq, items, pages, kr;
   // absorbed
   int slab, max_streams;       // tokens of a pass; streams of a pass at most
-  size_t few_plan, streams, state, q_nope, q_rope, rot, q_abs, partial, partial_lse;
+  size_t few_plan, streams, state, q_abs, partial, partial_lse;
   size_t total;
 };
 
@@ -901,27 +998,28 @@ struct Layout {
 //   Expanded: a row's expansion costs 2 * 512 * 256 flops a head at 1.15 PFLOP/s;
 //   a query, row and head 2 * 320 at 0.7, in query tiles of 256, but no less than
 //   one item's way through a sequence, 1.9 us per 128 rows.
-//   Absorbed: a query, row and head 2 * 1088 at 0.76 PFLOP/s, 6 ns a query and
-//   head for partial sums and projections, 0.04 us a query for its own work.
+//   Absorbed: a query, row and head 2 * 1088 at 0.76 PFLOP/s, 5.5 ns a query and
+//   head for absorption, partial sums and value expansion.
 // Tokens a sequence at which the two take the same time, measured and by this
 // estimate, and that time (sequences x cached rows):
 //                1 x 4096        4 x 2048        16 x 1024       1 x 16384
-//   16 heads     150, 202; 93    63, 54; 88      48, 39; 165     288, 329; 302
-//   64 heads     82, 94; 137     76, 75; 264     55, 51; 545     125, 138; 458
-//   128 heads    90, 101; 268    73, 79; 500     57, 53; 1150    135, 141; 970
+//   16 heads     172, 235; 93    82, 69; 88      69, 53; 165     310, 347; 302
+//   64 heads     82, 100; 137    79, 82; 264     61, 57; 545     127, 141; 458
+//   128 heads    90, 106; 268    75, 84; 500     61, 58; 1150    135, 143; 970
 bool chunk_route(const mla_dims_t* d, int B, int n_tok, long long max_rows) {
   if (!expandable(d)) return false;
   const double rows = (double)max_rows, heads = d->H, per = std::ceil((double)n_tok / B);
   const double e = 25 + rows * heads * 262144.0 / 1.15e9 +
                    std::max(rows * heads * std::ceil(per / 256) * 256 * 640.0 / 0.7e9,
                             rows / B / 128 * 1.9);
-  const double s = 38 + rows * per * heads * 2176.0 / 0.76e9 + n_tok * (heads * 0.006 + 0.04);
+  const double s = 38 + rows * per * heads * 2176.0 / 0.76e9 + n_tok * heads * 0.0055;
   return e < s;
 }
 
 bool make_layout(const mla_dims_t* d, int B, int n_tok, int n_ver, int max_pages, int max_segs,
                  long long max_rows, Layout* l) {
   *l = Layout{};
+  if (d->H > 65535) return false;       // grid limit
   size_t at = 0;
   auto take = [&](size_t bytes) {
     const size_t here = at;
@@ -930,9 +1028,8 @@ bool make_layout(const mla_dims_t* d, int B, int n_tok, int n_ver, int max_pages
   };
   l->expanded = chunk_route(d, B, n_tok, max_rows);
   l->generic = !decodable(d);
-  const size_t es = d->dtype == MLA_BF16 ? 2 : 4;
   if (l->generic) {        // 48 KB of shared memory, a little of it static
-    if (generic_smem(d, n_ver) > 48 * 1024 - 256 || d->H > 65535) return false;
+    if (generic_smem(d, n_ver) > 48 * 1024 - 256) return false;
     take(256);        // it needs none; an empty workspace is not told from an error
     l->total = at;
     return true;
@@ -964,10 +1061,7 @@ bool make_layout(const mla_dims_t* d, int B, int n_tok, int n_ver, int max_pages
     l->few_plan = take(sizeof(fw::Plan));
     l->streams = take(sizeof(fw::Stream) * (size_t)l->max_streams);
     l->state = take(n * 4);
-    l->q_nope = take(rows * d->d_n * es);
-    l->q_rope = take(rows * d->d_r * es);
-    l->rot = take(n * 4);
-    l->q_abs = take(rows * fw::kWidth * es);
+    l->q_abs = take(rows * fw::kWidth * 2);
     const size_t slots = (size_t)pairs + l->max_streams;
     l->partial = take(slots * fw::kRows * fw::kDc * 4);
     l->partial_lse = take(slots * fw::kRows * 4);
@@ -1086,8 +1180,6 @@ mla_status_t run_absorbed(const mla_dims_t* d, const ChunkArgs& a, const Layout&
   fw::Plan* plan = reinterpret_cast<fw::Plan*>(ws + l.few_plan);
   fw::Stream* streams = reinterpret_cast<fw::Stream*>(ws + l.streams);
   int* state = reinterpret_cast<int*>(ws + l.state);
-  int32_t* rot = reinterpret_cast<int32_t*>(ws + l.rot);
-  mla_stream_t ms = reinterpret_cast<mla_stream_t>(st);
 
   fw::Params p;
   p.plan = plan;
@@ -1115,17 +1207,12 @@ mla_status_t run_absorbed(const mla_dims_t* d, const ChunkArgs& a, const Layout&
   const __nv_bfloat16* wv = static_cast<const __nv_bfloat16*>(w_uv);
   for (int t0 = 0; t0 < a.n_tok; t0 += l.slab) {
     const int n = std::min(l.slab, a.n_tok - t0), rows = n * d->H;
-    const dim3 by_head(n, (d->H + 7) / 8);
     const __nv_bfloat16* q =
         static_cast<const __nv_bfloat16*>(a.q) + (size_t)t0 * d->H * (d->d_n + d->d_r);
-    few_split_kernel<<<by_head, 256, 0, st>>>(
-        d->H, d->d_n / 8, d->d_r / 8, reinterpret_cast<const uint4*>(q),
-        reinterpret_cast<uint4*>(ws + l.q_nope), reinterpret_cast<uint4*>(ws + l.q_rope), rot);
+    few_absorb_kernel<<<dim3(fw::kDc / kFaCols, d->H, (n + kFaTokens - 1) / kFaTokens), kFaThreads,
+                        0, st>>>(n, d->H, d->d_n, q, static_cast<const __nv_bfloat16*>(w_uk),
+                                 reinterpret_cast<__nv_bfloat16*>(ws + l.q_abs));
     if (cudaGetLastError() != cudaSuccess) return MLA_ERR_CUDA;
-    const int32_t zero = 0;
-    mla_status_t rc =
-        mla_absorb_q(d, n, ws + l.q_nope, ws + l.q_rope, rot, &zero, 1, w_uk, ws + l.q_abs, ms);
-    if (rc != MLA_OK) return rc;
     const FewPlan few = {t0, n, pairs, plan, streams, state};
     if (t0 == 0) {
       if (launch_dependent(chunk_plan_kernel<true>, dim3(1), dim3(kPlanThreads), 0, st, true, a, few,
