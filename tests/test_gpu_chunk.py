@@ -485,3 +485,13 @@ def test_few_tokens_of_any_value_width(d_n, d_v, lens, past):
     """Value widths that end inside a group of eight, of 64 and of 128 channels; one long sequence
     split over every pair of SMs."""
     Case("bf16", 3, lens, past, tail=2, d=dict(d_c=512, d_r=64, d_n=d_n, d_v=d_v)).run().check()
+
+
+@pytest.mark.parametrize("lens,past,doc", [([5] * 60, [300] * 60, 0), ([7, 0, 9] * 18, [90, 64, 500] * 18, 128),
+                                           ([37] * 8, [1000] * 8, 0)])
+def test_more_few_tokens_than_one_pass_takes(lens, past, doc):
+    """The absorbed route in passes of 256 tokens of 128 heads, cut inside sequences."""
+    c = Case("bf16", 128, lens, past, doc, tail=2)
+    assert c.total > 256
+    assert c.workspace().numel() < c.max_rows * 128 * 512 + 2 ** 28
+    c.run().check(heads=[0, 63, 127])
