@@ -170,11 +170,16 @@ enum TokState : int { kNone = 0, kLive = 1, kBad = 2 };
 // into saves a pair its second set of partial sums: with equal streams, a
 // divisor or multiple of their length is taken if it costs at most a quarter
 // more tiles a pair.
+struct FewToken {
+  int state;              // TokState
+  int stream, row;        // first stream of its sequence, and that stream's first row
+};
+
 struct FewPlan {
   int slab0, slab_n, pairs;
   fw::Plan* plan;
   fw::Stream* streams;
-  int* state;
+  FewToken* tokens;
 };
 
 __device__ void plan_few(const ChunkArgs& a, const FewPlan& f, const int* seq,
@@ -182,7 +187,7 @@ __device__ void plan_few(const ChunkArgs& a, const FewPlan& f, const int* seq,
   const int slab0 = f.slab0, slab_n = f.slab_n, pairs = f.pairs;
   fw::Plan* plan = f.plan;
   fw::Stream* streams = f.streams;
-  int* state = f.state;
+  FewToken* tokens = f.tokens;
   __shared__ int scratch[33], n_st, units, longest, shortest;
   const int* pg = seq;
   const int* bad = seq + 2 * (a.B + 1);
@@ -190,7 +195,7 @@ __device__ void plan_few(const ChunkArgs& a, const FewPlan& f, const int* seq,
     n_st = units = longest = 0;
     shortest = INT32_MAX;
   }
-  for (int t = threadIdx.x; t < slab_n; t += kPlanThreads) state[t] = kNone;
+  for (int t = threadIdx.x; t < slab_n; t += kPlanThreads) tokens[t].state = kNone;
   __syncthreads();
   // streams, in the order of the sequences
   for (int b0 = 0; b0 < a.B; b0 += kPlanThreads) {
@@ -199,10 +204,10 @@ __device__ void plan_few(const ChunkArgs& a, const FewPlan& f, const int* seq,
     if (b < a.B && bad[b] != kNoRange) {
       t0 = max(a.tok_start[b] - slab0, 0);           // tokens of the slab
       t1 = min(a.tok_start[b + 1] - slab0, slab_n);
-      for (int t = t0; t < t1; ++t) state[t] = bad[b] ? kBad : kLive;
       if (!bad[b] && t1 > t0) ns = ((t1 - t0) * a.H + fw::kRows - 1) / fw::kRows;
     }
     const int at = block_scan(ns, scratch, &n_st);
+    for (int t = t0; t < t1; ++t) tokens[t] = {bad[b] ? kBad : kLive, at, t0 * a.H};
     for (int k = 0; k < ns; ++k) {
       fw::Stream s;
       s.q_row = t0 * a.H + k * fw::kRows;
@@ -618,7 +623,7 @@ size_t few_value_smem(int pairs) {
 
 __global__ void __launch_bounds__(kFvThreads) few_value_kernel(
     int n, int H, int d_v, int pairs, const fw::Plan* plan, const fw::Stream* streams,
-    const int* state, const float* partial, const float* partial_lse, const __nv_bfloat16* w_uv,
+    const FewToken* tokens, const float* partial, const float* partial_lse, const __nv_bfloat16* w_uv,
     __nv_bfloat16* out, float* lse) {
   extern __shared__ __align__(16) uint8_t sm_fv[];
   __nv_bfloat16* o_hi = reinterpret_cast<__nv_bfloat16*>(sm_fv);       // [16][pitch]
@@ -627,19 +632,14 @@ __global__ void __launch_bounds__(kFvThreads) few_value_kernel(
   const int h = blockIdx.x, t0 = blockIdx.y * kFvTokens;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int n_streams = plan->n_streams, run = plan->chunk;
+  const int run = plan->chunk;
   {
     const int i = warp, t = t0 + i;
     float4 acc[4] = {};
-    if (t < n && state[t] == kLive) {
+    const FewToken tok = t < n ? tokens[t] : FewToken{kNone, 0, 0};
+    if (tok.state == kLive) {
       const int r = t * H + h;
-      // the last stream that starts at or before the row holds it
-      int si = -1, of_these = 32;
-      for (int j = 0; j < n_streams && of_these == 32; j += 32) {
-        of_these = __popc(__ballot_sync(
-            0xffffffffu, j + lane < n_streams && streams[min(j + lane, n_streams - 1)].q_row <= r));
-        si += of_these;
-      }
+      const int si = tok.stream + (r - tok.row) / fw::kRows;
       const fw::Stream s = streams[si];
       const int in = r - s.q_row;
       const int g0 = s.tiles > 0 ? s.off / run : 0;
@@ -690,7 +690,7 @@ __global__ void __launch_bounds__(kFvThreads) few_value_kernel(
           acc[c].w *= inv;
         }
       }
-    } else if (t < n && state[t] == kBad && lse && lane == 0) {
+    } else if (tok.state == kBad && lse && lane == 0) {
       lse[(size_t)t * H + h] = kNaN;
     }
 #pragma unroll
@@ -750,7 +750,7 @@ __global__ void __launch_bounds__(kFvThreads) few_value_kernel(
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
         const int t = t0 + row + 8 * half;
-        const int st = t < n ? state[t] : kNone;
+        const int st = t < n ? tokens[t].state : kNone;
         if (st == kNone) continue;
         __nv_bfloat16* o = out + ((size_t)t * H + h) * d_v + c;
         const float y0 = st == kBad ? kNaN : y[2 * half], y1 = st == kBad ? kNaN : y[2 * half + 1];
@@ -990,7 +990,7 @@ struct Layout {
   size_t plan, seq, items, pages, kr;
   // absorbed
   int slab, max_streams;       // tokens of a pass; streams of a pass at most
-  size_t few_plan, streams, state, q_abs, partial, partial_lse;
+  size_t few_plan, streams, tokens, q_abs, partial, partial_lse;
   size_t total;
 };
 
@@ -1060,7 +1060,7 @@ bool make_layout(const mla_dims_t* d, int B, int n_tok, int n_ver, int max_pages
     l->max_streams = (int)(rows / fw::kRows) + B;
     l->few_plan = take(sizeof(fw::Plan));
     l->streams = take(sizeof(fw::Stream) * (size_t)l->max_streams);
-    l->state = take(n * 4);
+    l->tokens = take(n * sizeof(FewToken));
     l->q_abs = take(rows * fw::kWidth * 2);
     const size_t slots = (size_t)pairs + l->max_streams;
     l->partial = take(slots * fw::kRows * fw::kDc * 4);
@@ -1179,7 +1179,7 @@ mla_status_t run_absorbed(const mla_dims_t* d, const ChunkArgs& a, const Layout&
   __nv_bfloat16* kr = reinterpret_cast<__nv_bfloat16*>(ws + l.kr);
   fw::Plan* plan = reinterpret_cast<fw::Plan*>(ws + l.few_plan);
   fw::Stream* streams = reinterpret_cast<fw::Stream*>(ws + l.streams);
-  int* state = reinterpret_cast<int*>(ws + l.state);
+  FewToken* tokens = reinterpret_cast<FewToken*>(ws + l.tokens);
 
   fw::Params p;
   p.plan = plan;
@@ -1213,7 +1213,7 @@ mla_status_t run_absorbed(const mla_dims_t* d, const ChunkArgs& a, const Layout&
                         0, st>>>(n, d->H, d->d_n, q, static_cast<const __nv_bfloat16*>(w_uk),
                                  reinterpret_cast<__nv_bfloat16*>(ws + l.q_abs));
     if (cudaGetLastError() != cudaSuccess) return MLA_ERR_CUDA;
-    const FewPlan few = {t0, n, pairs, plan, streams, state};
+    const FewPlan few = {t0, n, pairs, plan, streams, tokens};
     if (t0 == 0) {
       if (launch_dependent(chunk_plan_kernel<true>, dim3(1), dim3(kPlanThreads), 0, st, true, a, few,
                            l.cap, cplan, seq, reinterpret_cast<ck::Item*>(ws + l.items),
@@ -1239,7 +1239,7 @@ mla_status_t run_absorbed(const mla_dims_t* d, const ChunkArgs& a, const Layout&
     if (launch_dependent(few_value_kernel, dim3(d->H, (n + kFvTokens - 1) / kFvTokens),
                          dim3(kFvThreads), (int)few_value_smem(pairs), st, true, n, d->H, d->d_v, pairs,
                          static_cast<const fw::Plan*>(plan), static_cast<const fw::Stream*>(streams),
-                         static_cast<const int*>(state), static_cast<const float*>(p.partial),
+                         static_cast<const FewToken*>(tokens), static_cast<const float*>(p.partial),
                          static_cast<const float*>(p.partial_lse), wv, out, lse_out) != cudaSuccess)
       return MLA_ERR_CUDA;
   }
