@@ -525,7 +525,7 @@ mla_status_t mla_append_tokens(const mla_dims_t* dims, int32_t B, int32_t n_tok,
  * range, else bf16); for few, the absorbed query (bf16), weights and weighted
  * latents in two bf16 parts each.
  * Errors: INVALID_ARG (scale must be > 0), UNSUPPORTED (page_size != 64,
- * n_ver > 8, row counts beyond 2^31 - 1; outside bf16 rows of 512 + 64, a query
+ * n_ver > 8, H > 65535, row counts beyond 2^31 - 1; outside bf16 rows of 512 + 64, a query
  * of n_ver (d_c + d_r) and a latent of d_c floats that 48 KB do not hold),
  * WORKSPACE. */
 mla_status_t mla_chunk_attn(const mla_dims_t* dims, int32_t B, int32_t n_tok, const void* q,

@@ -139,6 +139,7 @@ def test_sizes_whose_products_overflow(L):
     assert _chunk(L, n_pages=(1 << 63) - 1) == UNSUPPORTED
     assert _append(L, dims=_dims(d_c=2 ** 31 - 8)) == INVALID      # rows longer than their stride
     assert _append(L, dims=_dims(d_c=1 << 30), stride=1 << 31, bc=4, br=4, sc=FAKE, sr=FAKE) == UNSUPPORTED
+    assert _chunk(L, dims=_dims(H=65536)) == UNSUPPORTED
     f32 = dict(dtype=mla.MLA_F32, d_c=32)
     assert _chunk(L, dims=_dims(**f32, d_r=1 << 30), n_ver=4, delta=_ints(0, 0, 0, 0)) == UNSUPPORTED
 
