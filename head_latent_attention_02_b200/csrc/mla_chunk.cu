@@ -509,7 +509,8 @@ __device__ __forceinline__ void load_tiles(const __nv_bfloat16* p, uint32_t (&x)
 // and 128 heads fill every SM several times.  The decode's absorption takes its
 // queries in two arrays, which a launch before it had to split, and 128 tokens a
 // launch: with it a call over 1000 rows took 286 us for 512 tokens of 64 heads, 48
-// for 256 of 8 and 32 for one of 128 heads, this way 260, 37 and 34.
+// for 256 of 8 and 32 for one of 128 heads, this way 260, 37 and 34.  16 tokens of
+// 128 heads: 8.6 us (17 MB of weights, 2 TB/s).
 constexpr int kFaThreads = 128, kFaTokens = 64, kFaCols = 64, kFaK = 128;
 constexpr int kFaPitchW = kFaCols + 8, kFaPitchQ = kFaK + 8;
 
@@ -610,9 +611,10 @@ __global__ void __launch_bounds__(kFaThreads) few_absorb_kernel(int n, int H, in
 //   long as both operands have the same: a lane takes eight consecutive ones of its
 //   row of either, so that a load is 16 bytes and feeds two products; a pitch of 16
 //   words modulo 32 keeps the rows of a load of shared memory apart.
-// Tokens of no sequence keep what their rows held.  Join, library-wide value product
-// and store as three launches took 424 us for 512 tokens of 64 heads over 1000 rows
-// each, attention included, where this takes 286, and 43 for 16 where it takes 38.
+// Tokens of no sequence keep what their rows held.  A join, the value product of
+// mla_out_proj and a store as three launches took 424 us for 512 tokens of 64 heads
+// over 1000 rows each, the whole call, where this took 286, and 43 for 16 tokens
+// where it took 38.  16 tokens of 128 heads: 17 us from memory (34 MB, 2 TB/s).
 constexpr int kFvTokens = 16, kFvThreads = 512, kFvPitch = fw::kDc + 32;
 
 // o in two parts; weights of the shares, later the sums of eight warps
@@ -1057,7 +1059,7 @@ bool make_layout(const mla_dims_t* d, int B, int n_tok, int n_ver, int max_pages
     const size_t n = l->slab, rows = n * d->H;
     const int pairs = current_sms() / 2;
     if (pairs == 0) return false;
-    l->max_streams = (int)(rows / fw::kRows) + B;
+    l->max_streams = (int)(rows / fw::kRows) + std::min(B, l->slab);   // with a token in it
     l->few_plan = take(sizeof(fw::Plan));
     l->streams = take(sizeof(fw::Stream) * (size_t)l->max_streams);
     l->tokens = take(n * sizeof(FewToken));

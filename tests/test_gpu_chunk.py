@@ -495,3 +495,10 @@ def test_more_few_tokens_than_one_pass_takes(lens, past, doc):
     assert c.total > 256
     assert c.workspace().numel() < c.max_rows * 128 * 512 + 2 ** 28
     c.run().check(heads=[0, 63, 127])
+
+
+def test_thousands_of_sequences():
+    """Shares are kept for the sequences of one pass, not for all; 700 sequences of a token each."""
+    dims = mla.Dims(128, 512, 64, 128, 128, 256, 64, mla.MLA_BF16, 0.07, BASE)
+    assert 0 < mla.chunk_workspace_size(dims, 4096, 4096, 1, 64, 1, 4096 * 64) < 2 ** 28
+    Case("bf16", 128, [1, 0, 1, 1] * 175, [3, 64, 70, 0] * 175).run().check(heads=[0, 127])
