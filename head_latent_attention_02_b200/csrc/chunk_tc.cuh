@@ -17,8 +17,8 @@
 // cores read both halves, so a CTA loads 40 KB a tile instead of 80 KB.  With one
 // CTA per 256 tokens the ring held a tile and a half and its loads, 1.5 us
 // from issue to landing, stalled the products.  S and O of both query tiles
-// fill the 512 tensor-memory columns; P (16 bits, half or bf16 as the values
-// are: values_as_half) overwrites its S.  The
+// fill the 512 tensor-memory columns; P (16 bits, half or bf16 as the tile's
+// values are) overwrites its S.  The
 // tensor core works on one query tile while the other one's softmax runs:
 //     ... P0 V | S0 | P1 V | S1 | P0 V | S0 ...
 // At 192 + 128 columns a tile costs the tensor core 1280 clocks and its
@@ -91,6 +91,9 @@ struct Params {
   const int32_t* q_pos;
   int H, h0, n_heads;          // heads of the call; first head and heads of this launch
   long long rows_cap;          // rows per head of the key and value scratch
+  const int* norm_c;           // [sequences], see value_exponent
+  const int* norm_w;           // [heads of this launch]
+  const uint8_t* as_half;      // [heads of this launch][rows_cap / 128]: the values' type
   float scale_log2, scale;
   __nv_bfloat16* v;            // [n_tok, H, 128]
   float* lse;                  // [n_tok, H] or null
@@ -131,7 +134,6 @@ chunk_attn_kernel(const __grid_constant__ Params p, const __grid_constant__ Maps
 
   // the item list and the expanded rows are complete after this wait
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const bool half = uniform(values_as_half(p.plan));
   const int item = blockIdx.x >> 1;
   const int rank = (int)cluster_ctarank();
   if (item >= p.plan->n_items) return;       // both CTAs of the pair
@@ -174,6 +176,8 @@ chunk_attn_kernel(const __grid_constant__ Params p, const __grid_constant__ Maps
   const uint32_t tmem = bar->tmem_base;
   const int nt0 = uniform(it.need[0]), nt1 = uniform(it.need[1]);
   const int nt = max(nt0, nt1);
+  // the sequence's first tile of as_half
+  const int type0 = uniform((int)((hl * p.rows_cap + (long long)it.entry * kPage) / kKTile));
 
   if (warp < 4) {
     setmaxnreg_dec<kRegsIssue>();
@@ -221,7 +225,6 @@ chunk_attn_kernel(const __grid_constant__ Params p, const __grid_constant__ Maps
       if (rank == 0 && nt > 0) {        // the whole warp, converged
         constexpr uint32_t idesc_s = idesc_bf16_f32(kPairTile, kKTile, false, false);
         constexpr uint32_t idesc_pv = idesc_bf16_f32(kPairTile, kDv, false, true);
-        const uint32_t idesc_o = half ? idesc_half_f32(idesc_pv) : idesc_pv;
         // Descriptors of the first panels; a panel, a slot or a K step further is
         // an addition (16-byte units) that never leaves the address field.  The
         // issuing warp shares its scheduler with softmax warps: building each
@@ -237,9 +240,12 @@ chunk_attn_kernel(const __grid_constant__ Params p, const __grid_constant__ Maps
             ok = false;
           }
         };
+        int half = 0;
         for (int j = 0; ok && j <= nt; ++j) {
           // P V of step j - 1, then S of step j, for each query tile; what was
           // loaded is waited for first, off the chain from weights to scores
+          const uint32_t idesc_o = uniform(half) ? idesc_half_f32(idesc_pv) : idesc_pv;
+          if (j < nt) half = p.as_half[type0 + j];
           const int ks_n = j % kKeySlots, vs_n = (j + kValSlots - 1) % kValSlots;
           if (j < nt) wait(&bar->k_full[ks_n], (j / kKeySlots) & 1);
           if (j > 0) wait(&bar->v_full[vs_n], ((j - 1) / kValSlots) & 1);
@@ -297,11 +303,13 @@ chunk_attn_kernel(const __grid_constant__ Params p, const __grid_constant__ Maps
     const uint32_t o_col = tmem + kColO + t * kDv + lanes;
     const int qp = tok < it.n ? p.q_pos[it.tok0 + tok] : INT32_MIN;
     float m = kNegInf, l = 0.f;       // running maximum (unscaled scores), sum of weights
+    float unscale = 1.f;              // of the values (value_exponent)
     bool ok = true;
     if (mine > 0) {
       const PageEntry* pe = p.pages + it.entry;
       const int n_full = it.full[t];
       for (int j = 0; j < mine; ++j) {
+        const bool half = p.as_half[type0 + j];     // under way during the wait for the scores
         int v0 = kPage, v1 = kPage;
         if (j >= n_full) {
           v0 = visible(pe[2 * j], qp);
@@ -383,6 +391,7 @@ chunk_attn_kernel(const __grid_constant__ Params p, const __grid_constant__ Maps
         unpack_f32x2(add_f32x2(sum[0], sum[1]), a0, a1);
         l += a0 + a1;
       }
+      unscale = power_of_two(-value_exponent(p.norm_c[p.items[item].b], p.norm_w[blockIdx.y]));
       if (ok && !__all_sync(0xffffffffu, mbar_wait(&bar->o_full[t], 0))) {
         if (lane == 0) set_status(MLA_ERR_TIMEOUT);
         ok = false;
@@ -409,7 +418,8 @@ chunk_attn_kernel(const __grid_constant__ Params p, const __grid_constant__ Maps
           uint32_t w[4];
 #pragma unroll
           for (int k = 0; k < 4; ++k)
-            w[k] = none ? 0u : pack2(a[8 * i + 2 * k] * inv, a[8 * i + 2 * k + 1] * inv);
+            w[k] = none ? 0u
+                        : pack2(a[8 * i + 2 * k] * inv * unscale, a[8 * i + 2 * k + 1] * inv * unscale);
           d[i] = make_uint4(w[0], w[1], w[2], w[3]);
         }
       }

@@ -65,27 +65,35 @@ __device__ __forceinline__ uint32_t pack2_half(float lo, float hi) {
 struct PageEntry {
   int row;      // physical cache row of the page's first row; past the cache: no rows
   int kpos;     // request position of that row
-  int n;        // rows that hold data (0 .. 64)
-  int ver;      // relocation version
+  short n;      // rows that hold data (0 .. 64)
+  short ver;    // relocation version
+  int seq;      // sequence it belongs to
 };
 
 // What the planner of a chunk call leaves on the device.
 struct ChunkPlan {
   int n_items;
   int n_row_tiles;      // 256-row tiles of the page list (the expansion's row tiles)
-  int c_sq, w_sq;       // float bits: largest squared norm of a latent and of a row of W_UV
 };
 
-// Whether the expanded values are held as halves.  |V| <= |c| |w| bounds every
-// value of the call; between these limits no value overflows, and typical ones
-// (the bound over sqrt(512) or less) lie far above half's smallest normal.
-// A half has three mantissa bits more than a bfloat16, and the weights, which
-// have to be of the values' type, gain them too: the error of the result falls
-// from about 3.0e-3 to 2.1e-3 (1.66e-3 of it is the result's own rounding).
-__device__ __forceinline__ bool values_as_half(const ChunkPlan* plan) {
-  const float sq = __int_as_float(plan->c_sq) * __int_as_float(plan->w_sq);
-  return sq >= 0.0625f && sq <= 3.6e9f;       // |c| |w| from 1 / 4 to 60000
+// Expanded values are kept times 2^k, k for each sequence and head, which the
+// attention takes back from its result: |V| <= |c| |w| then bounds them by 2^15,
+// whatever the size of latents and weights.  A tile of 128 rows whose values are
+// zero or lie between 2^-16 and half's largest number is held in halves (with the
+// weights that meet it, which have to be of the same type): down to 2^-16 a
+// half's rounding, a step of 2^-24 there, is no larger than a bfloat16's, and
+// above 2^-14 it is eight times smaller.  Other tiles (rows or channels 2^-31 below
+// the bound) are held in bfloat16.  The error of the result is 2.0e-3 with halves
+// and 3.0e-3 without (1.66e-3 of it is the result's own rounding).
+//
+// The norms come as the largest exponents of the squares, E with |x|^2 < 2^(E + 1).
+constexpr int kNoNorm = -10000;      // no vector, or zeros alone
+__device__ __forceinline__ int value_exponent(int norm_c, int norm_w) {
+  // |c| |w| < 2^((norm_c + norm_w + 2) / 2); values past 2^128 are infinite
+  return min(max(15 - ((norm_c + norm_w + 3) >> 1), -113), 100);
 }
+__device__ __forceinline__ float power_of_two(int k) { return __int_as_float((k + 127) << 23); }
+constexpr float kLeastHalf = 1.52587890625e-5f, kMostHalf = 65504.f;   // see above
 
 // Description of one mla_decode call as the kernels see it.
 struct DecodeArgs {

@@ -22,8 +22,6 @@
 #pragma once
 #include <cuda.h>
 
-#include <type_traits>
-
 #include "common.cuh"
 #include "ptx.cuh"
 
@@ -41,6 +39,8 @@ constexpr int kOffBar = kOffStage + 4 * kStageWarp;
 constexpr int kSmemBytes = kOffBar + 512 + 1024;
 constexpr int kThreads = 192;
 constexpr int kTmemCols = 512;
+// the largest finite bf16: what rounds past it is not finite either
+constexpr float kMostBf16 = 3.38953139e38f;
 static_assert(kSmemBytes <= 232448, "shared memory budget");
 
 struct Params {
@@ -48,6 +48,9 @@ struct Params {
   const ChunkPlan* plan;
   int n_heads;                 // heads of this launch
   long long rows_cap;          // rows per head of the scratch
+  const int* norm_c;           // [sequences], see value_exponent
+  const int* norm_w;           // [heads of this launch]
+  uint8_t* as_half;            // [heads of this launch][rows_cap / 128]: the values' type
 };
 
 // Tensor maps (64 columns, 128-byte swizzle):
@@ -62,6 +65,8 @@ struct Bars {
   uint64_t c_full[kPanels], c_empty[kPanels];
   uint64_t w_full[kStages], w_empty[kStages];
   uint64_t acc_full[2], acc_empty[2];
+  uint64_t agreed;       // the epilogue warps have looked at a tile's values
+  uint32_t fits[2];      // even and odd tiles: a byte a warp, 1: its values fit halves
   uint32_t tmem_base;
 };
 static_assert(sizeof(Bars) <= 512, "barrier block too large");
@@ -89,6 +94,7 @@ expand_kernel(const __grid_constant__ Params p, const __grid_constant__ Maps mp)
       mbar_init(&bar->acc_full[i], 1);
       mbar_init(&bar->acc_empty[i], 8);    // four epilogue warps of each CTA
     }
+    mbar_init(&bar->agreed, 4);
     fence_mbar_init();
   }
   if (warp == 1) tmem_alloc_pair(&bar->tmem_base, kTmemCols);
@@ -194,18 +200,29 @@ expand_kernel(const __grid_constant__ Params p, const __grid_constant__ Maps mp)
     // Rows without data are zeros (a weight of zero times NaN is NaN).  A value
     // that is not finite is stored as zero and marks the row's key as NaN
     // instead: queries that see the row get NaN, queries whose mask hides it
-    // are not touched by it.  So the values go first.
+    // are not touched by it.  So the values are looked at first; they are written
+    // last, when the CTA's four warps, whose 128 rows are one tile of the
+    // attention, have agreed on their type.
     const int quad = warp & 3;
     const int row = rank * 128 + quad * 32 + lane;      // row of the pair's tile
-    const bool half = values_as_half(p.plan);
     uint4* stage = reinterpret_cast<uint4*>(smem + kOffStage + quad * kStageWarp);
     if (lane == 0) {
       prefetch_tmap(&mp.k);
       prefetch_tmap(&mp.v);
     }
+    int held = -1, norm_c = 0;
+    bool live = false;
+    int norm_w = u0 < u1 ? p.norm_w[u0 % p.n_heads] : 0;      // read a tile ahead
     for (int u = u0; u < u1; ++u) {
       const int mt = u / p.n_heads, h = u % p.n_heads, ab = (u - u0) & 1;
-      const bool live = row % 64 < p.pages[4 * mt + row / 64].n;
+      if (mt != held) {
+        const PageEntry page = p.pages[4 * mt + row / 64];
+        live = row % 64 < page.n;
+        norm_c = p.norm_c[page.seq];
+        held = mt;
+      }
+      const float size = power_of_two(value_exponent(norm_c, norm_w));
+      if (u + 1 < u1) norm_w = p.norm_w[h + 1 < p.n_heads ? h + 1 : 0];
       if (!__all_sync(0xffffffffu, mbar_wait(&bar->acc_full[ab], ((u - u0) >> 1) & 1))) {
         if (lane == 0) set_status(MLA_ERR_TIMEOUT);
         break;
@@ -213,51 +230,107 @@ expand_kernel(const __grid_constant__ Params p, const __grid_constant__ Maps mp)
       tc_fence_after();
       const uint32_t acc = tmem + ab * 256 + ((uint32_t)(quad * 32) << 16);
       const int y = (int)(h * p.rows_cap) + mt * 256 + rank * 128 + quad * 32;
-      bool fine = true;
-      // 64 columns: tensor memory -> 16-bit pairs -> staging -> scratch
-      auto panel = [&](int c, auto is_value, auto as_half) {
-        float v[2][32];
-        tmem_ld64_sync(acc + 64 * c, v);
-        uint32_t w[32];
+      // The row's values, scaled, and the largest and least magnitude of those that
+      // are not zero.  Zeros and what is not finite are rare: they are looked for
+      // only where the first pass over all values shows one.
+      float val[4][32];
+      tmem_ld128_sync(acc + 128, val);
+      const uint64_t size2 = pack_f32x2(size, size);
+      float most = 0.f, least = INFINITY;
 #pragma unroll
-        for (int i = 0; i < 32; ++i) {
-          float a = v[i >> 4][2 * (i & 15)], b = v[i >> 4][2 * (i & 15) + 1];
-          if constexpr (decltype(is_value)::value) {
-            // the largest finite bf16: what rounds past it is not finite either
-            const bool fa = fabsf(a) <= 3.38953139e38f, fb = fabsf(b) <= 3.38953139e38f;
-            fine = fine && fa && fb;
-            a = fa ? a : 0.f;
-            b = fb ? b : 0.f;
-          }
-          w[i] = decltype(as_half)::value ? pack2_half(a, b) : pack2(a, b);
-          if (!live) w[i] = 0u;
+      for (int c = 0; c < 4; ++c)
+#pragma unroll
+        for (int i = 0; i < 32; i += 2) {
+          unpack_f32x2(mul_f32x2(pack_f32x2(val[c][i], val[c][i + 1]), size2), val[c][i],
+                       val[c][i + 1]);
+          most = max_abs_nan(most, val[c][i], val[c][i + 1]);
+          least = min_abs(least, val[c][i], val[c][i + 1]);
         }
-        if (c == 0 && live && !fine) w[0] = 0x7fff7fffu;        // NaN
+      bool fine = true;
+      if (__any_sync(0xffffffffu, live && (!(most <= kMostBf16) || least == 0.f))) {
+        most = 0.f;
+        least = INFINITY;
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            const float a = fabsf(val[c][i]);
+            if (!(a <= kMostBf16)) {
+              fine = false;
+              val[c][i] = 0.f;
+            } else {
+              most = fmaxf(most, a);
+              least = a > 0.f ? fminf(least, a) : least;
+            }
+          }
+      }
+      const bool fits =
+          __all_sync(0xffffffffu, !live || (most <= kMostHalf && least >= kLeastHalf));
+      if (lane == 0) {
+        reinterpret_cast<volatile uint8_t*>(&bar->fits[ab])[quad] = fits;
+        mbar_arrive(&bar->agreed);
+      }
+      // 64 columns of the warp's rows: 16-bit pairs -> staging -> scratch, 32 columns
+      // (a lane's pieces 4 k to 4 k + 3) at a time
+      auto begin = [&] {
         if (lane == 0) bulk_wait_read<0>();         // the last store has left the staging tile
         __syncwarp();
+      };
+      auto put = [&](int k, uint32_t (&w)[16]) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-          stage[lane * 8 + (i ^ (lane & 7))] =
-              make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+        for (int i = 0; i < 4; ++i)
+          stage[lane * 8 + ((4 * k + i) ^ (lane & 7))] =
+              live ? make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3])
+                   : make_uint4(0u, 0u, 0u, 0u);
+      };
+      auto end = [&](const CUtensorMap* map, int c) {
         fence_proxy_async();
         __syncwarp();
         if (lane == 0) {
-          tma_store_3d(decltype(is_value)::value ? &mp.v : &mp.k, stage, 0, y, c & 1);
+          tma_store_3d(map, stage, 0, y, c);
           bulk_commit();
         }
       };
-      if (half) {
-        panel(3, std::true_type(), std::true_type());
-        panel(2, std::true_type(), std::true_type());
-      } else {
-        panel(3, std::true_type(), std::false_type());
-        panel(2, std::true_type(), std::false_type());
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        begin();
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          float v[32];
+          uint32_t w[16];
+          tmem_ld32_sync(acc + 64 * c + 32 * k, v);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) w[i] = pack2(v[2 * i], v[2 * i + 1]);
+          if (c == 0 && k == 0 && !fine) w[0] = 0x7fff7fffu;        // NaN
+          put(k, w);
+        }
+        end(&mp.k, c);
       }
-      panel(1, std::false_type(), std::false_type());
-      panel(0, std::false_type(), std::false_type());
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive_pair(mapa(smem_u32(&bar->acc_empty[ab]), 0));
+      if (!__all_sync(0xffffffffu, mbar_wait(&bar->agreed, (u - u0) & 1))) {
+        if (lane == 0) set_status(MLA_ERR_TIMEOUT);
+        break;
+      }
+      // the next such record is the other one; this one is written again only
+      // when all four warps have passed that
+      const bool half = *reinterpret_cast<volatile uint32_t*>(&bar->fits[ab]) == 0x01010101u;
+      if (quad == 0 && lane == 0) p.as_half[(long long)h * p.rows_cap / 128 + 2 * mt + rank] = half;
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        begin();
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const float(&v)[32] = val[2 * c + k];
+          uint32_t w[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            w[i] = half ? pack2_half(v[2 * i], v[2 * i + 1]) : pack2(v[2 * i], v[2 * i + 1]);
+          put(k, w);
+        }
+        end(&mp.v, c);
+      }
     }
     if (lane == 0) bulk_wait_all();       // complete before the attention reads them
   }

@@ -85,6 +85,7 @@ __device__ bool page_at(const ChunkArgs& a, int b, int i, PageEntry* e) {
     e->kpos = sg[s].key_pos_base + i * kPage;
     e->n = min(kPage, sg[s].row_end - row);
     e->ver = sg[s].q_version;
+    e->seq = b;
     return true;
   }
   return false;
@@ -267,7 +268,8 @@ __global__ void __launch_bounds__(kPlanThreads) few_plan_kernel(
 // One CTA: validates the sequences, lists their pages (an even number each, so
 // that a 128-row tile belongs to one sequence; a multiple of four in all) and
 // their 512-token items.  seq: page offset [B + 1], item offset [B + 1], flag
-// [B].  A sequence that does not fit `cap` pages is invalid.  A token range is
+// [B].  norms: cleared, for the n_norms that the next launch finds.
+// A sequence that does not fit `cap` pages is invalid.  A token range is
 // only taken if it starts at or behind every start before it: ranges are then
 // disjoint, which the item and stream lists rely on.
 // kFew: the absorbed route's streams follow, in place of the items.  That kernel
@@ -277,9 +279,10 @@ __global__ void __launch_bounds__(kPlanThreads) few_plan_kernel(
 template <bool kFew>
 __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(
     const __grid_constant__ ChunkArgs a, const __grid_constant__ FewPlan f, int cap, ChunkPlan* plan,
-    int* seq, ck::Item* items, PageEntry* pages) {
+    int* seq, ck::Item* items, PageEntry* pages, int* norms, int n_norms) {
   asm volatile("griddepcontrol.launch_dependents;");
   __shared__ int scratch[33], n_pg, n_it, used, latest;
+  for (int i = threadIdx.x; i < n_norms; i += kPlanThreads) norms[i] = kNoNorm;
   int* pg = seq;
   int* itm = seq + a.B + 1;
   int* bad = seq + 2 * (a.B + 1);
@@ -322,11 +325,10 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(
     itm[a.B] = n_it;
     plan->n_items = n_it;
     plan->n_row_tiles = whole / 4;
-    plan->c_sq = plan->w_sq = 0;
   }
   __syncthreads();
   for (int e = threadIdx.x; e < whole; e += kPlanThreads) {
-    PageEntry pe = {INT32_MAX - 2 * kPage, INT32_MAX, 0, 0};   // no rows
+    PageEntry pe = {INT32_MAX - 2 * kPage, INT32_MAX, 0, 0, 0};   // no rows
     if (e < in_use) {
       const int b = last_at_most(pg, a.B, e);
       if (!bad[b] && e - pg[b] < sequence_pages(a, b) && !page_at(a, b, e - pg[b], &pe)) {
@@ -357,8 +359,8 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(
   }
 }
 
-// Squared norm of 512 channels, four threads a row; every thread of the four
-// gets it.  Half of the row's additions are independent of the other half.
+// Squared norm of 512 channels, four threads a row; every thread of
+// the four gets it.  Half of the row's additions are independent of the other half.
 __device__ __forceinline__ float row_norm_sq(const __nv_bfloat16* row, int part) {
   const uint4* src = reinterpret_cast<const uint4*>(row) + part;
   float a = 0.f, b = 0.f;
@@ -373,6 +375,40 @@ __device__ __forceinline__ float row_norm_sq(const __nv_bfloat16* row, int part)
   a += b;
   a += __shfl_xor_sync(0xffffffffu, a, 1);
   return a + __shfl_xor_sync(0xffffffffu, a, 2);
+}
+
+// The same of the channels times `size`, a power of two.
+__device__ __noinline__ float row_norm_sq_scaled(const __nv_bfloat16* row, int part, float size) {
+  float a = 0.f;
+  for (int i = part; i < ck::kDc; i += 4) {
+    const float x = __bfloat162float(row[i]) * size;
+    a = fmaf(x, x, a);
+  }
+  a += __shfl_xor_sync(0xffffffffu, a, 1);
+  return a + __shfl_xor_sync(0xffffffffu, a, 2);
+}
+
+// Raises *m to the largest exponent of a squared norm of a warp's eight rows.  A
+// row that is not finite has values of zero and NaN keys: no part in the bound.
+// Squares that leave 32 bits are taken again of scaled channels (2^70: squares of
+// 2^128 / 2^70 and of 2^-133 2^70 stay inside).
+__device__ __forceinline__ void note_norm(const __nv_bfloat16* row, int part, int* m) {
+  float sq = row_norm_sq(row, part);
+  int up = 0;
+  if (__any_sync(0xffffffffu, !(sq >= 0x1p-100f && sq < INFINITY))) {
+    const float large = row_norm_sq_scaled(row, part, 0x1p-70f);
+    const float small = row_norm_sq_scaled(row, part, 0x1p70f);
+    if (sq < 0x1p-100f) {
+      sq = small;
+      up = -140;
+    } else if (!(sq < INFINITY)) {      // NaN stays NaN
+      sq = large;
+      up = 140;
+    }
+  }
+  const int e = sq > 0.f && sq < INFINITY ? ilogbf(sq) + up : kNoNorm;
+  const int top = __reduce_max_sync(0xffffffffu, e);
+  if ((threadIdx.x & 31) == 0) atomicMax(m, top);
 }
 
 // need and full of query tile t of an item, by 256 threads.
@@ -408,18 +444,19 @@ __device__ void item_tiles(const ChunkArgs& a, ck::Item& item, int t, const Page
 // Blocks [0, cap): rotary keys of the listed pages at their request positions,
 // kr[64 e + r] = R(delta[version]) k_rope of page entry e's row r (a plain copy
 // where delta is zero; rows without data are zeros), and the largest norm of
-// the rows' latents.  The blocks after them: the largest norm of 64 rows of
-// W_UV each.  The latents and weights read here are read again by the expansion,
+// each sequence's latents.  The blocks after them: the largest norm of 64 rows of
+// W_UV each, into their head's.  The latents and weights read here are read again by the expansion,
 // from L2.  256 threads, four a row.  The last blocks: what each query tile of an
 // item sees (ck::Item::need and full), once for all heads: as a part of the
 // attention's own prologue it took 2 us of every 30 us item of a short context.
 // (Without kNorms, the rotary keys alone.)
 template <bool kNorms>
 __global__ void __launch_bounds__(256) chunk_rotary_kernel(const __grid_constant__ ChunkArgs a,
-                                                           int cap, ChunkPlan* plan,
+                                                           int cap, const ChunkPlan* plan,
                                                            const PageEntry* pages,
                                                            const __nv_bfloat16* w_uv,
-                                                           __nv_bfloat16* kr, ck::Item* items) {
+                                                           __nv_bfloat16* kr, ck::Item* items,
+                                                           int* norm_c, int* norm_w) {
   asm volatile("griddepcontrol.launch_dependents;");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   __shared__ double2 cs[ck::kDr / 2];
@@ -430,12 +467,8 @@ __global__ void __launch_bounds__(256) chunk_rotary_kernel(const __grid_constant
     return;
   }
   if ((int)blockIdx.x >= cap) {
-    const float sq =
-        row_norm_sq(w_uv + ((size_t)(blockIdx.x - cap) * 64 + r) * ck::kDc, part);
-    // a weight that is not finite keeps the call from halves
-    const int bits = __float_as_int(sq == sq ? sq : __int_as_float(0x7f800000));
-    const int top = __reduce_max_sync(0xffffffffu, bits);
-    if ((threadIdx.x & 31) == 0) atomicMax(&plan->w_sq, top);
+    const int k = blockIdx.x - cap;
+    note_norm(w_uv + ((size_t)k * 64 + r) * ck::kDc, part, &norm_w[k / (ck::kDv / 64)]);
     return;
   }
   if ((int)blockIdx.x >= 4 * plan->n_row_tiles) return;
@@ -449,7 +482,6 @@ __global__ void __launch_bounds__(256) chunk_rotary_kernel(const __grid_constant
   const __nv_bfloat16* row = static_cast<const __nv_bfloat16*>(a.cache) +
                              ((long long)e.row + r) * (ck::kDc + ck::kDr);
   uint4 u[2] = {make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)};
-  float sq = 0.f;
   if (r < e.n) {
     const uint4* src = reinterpret_cast<const uint4*>(row + ck::kDc + part * 16);
     u[0] = src[0];
@@ -469,14 +501,8 @@ __global__ void __launch_bounds__(256) chunk_rotary_kernel(const __grid_constant
   dst[0] = u[0];
   dst[1] = u[1];
   // rows 8 w .. 8 w + 7 of warp w; beyond the page's data the last row again
-  if (kNorms && e.n > 0) {
-    sq = row_norm_sq(row - (r < e.n ? 0 : (r - e.n + 1) * (ck::kDc + ck::kDr)), part);
-    // a NaN latent's values are stored as zeros; an infinite norm (which finite
-    // channels can have) keeps the call from halves
-    const int bits = __float_as_int(sq == sq ? sq : 0.f);
-    const int top = __reduce_max_sync(0xffffffffu, bits);
-    if ((threadIdx.x & 31) == 0) atomicMax(&plan->c_sq, top);
-  }
+  if (kNorms && e.n > 0)
+    note_norm(row - (r < e.n ? 0 : (r - e.n + 1) * (ck::kDc + ck::kDr)), part, &norm_c[e.seq]);
 }
 
 // ------------------------------------------------------------ absorbed route
@@ -987,7 +1013,7 @@ struct Layout {
   // expanded
   int cap, heads, groups;      // page entries; heads per launch; launches
   long long rows_cap;
-  size_t k, v;
+  size_t k, v, norms, as_half;
   // both
   size_t plan, seq, items, pages, kr;
   // absorbed
@@ -1053,6 +1079,8 @@ bool make_layout(const mla_dims_t* d, int B, int n_tok, int n_ver, int max_pages
     if (l->rows_cap * l->heads + 4 * kPage > INT32_MAX) return false;
     l->k = take((size_t)l->rows_cap * l->heads * ck::kDn * 2);
     l->v = take((size_t)l->rows_cap * l->heads * ck::kDv * 2);
+    l->norms = take(sizeof(int) * ((size_t)B + d->H));
+    l->as_half = take((size_t)l->rows_cap / ck::kKTile * l->heads);
   } else {
     // tokens per pass: 32768 (token, head) rows, which bounds the workspace
     l->slab = std::min(n_tok, std::max(1, 32768 / d->H));
@@ -1086,6 +1114,8 @@ mla_status_t run_expanded(const mla_dims_t* d, const ChunkArgs& a, const Layout&
   ck::Item* items = reinterpret_cast<ck::Item*>(ws + l.items);
   PageEntry* pages = reinterpret_cast<PageEntry*>(ws + l.pages);
   __nv_bfloat16* kr = reinterpret_cast<__nv_bfloat16*>(ws + l.kr);
+  int* norm_c = reinterpret_cast<int*>(ws + l.norms);
+  int* norm_w = norm_c + a.B;
   const uint64_t cache_rows = (uint64_t)a.n_pages * kPage;
 
   ex::Maps xm;
@@ -1112,19 +1142,23 @@ mla_status_t run_expanded(const mla_dims_t* d, const ChunkArgs& a, const Layout&
     return MLA_ERR_CUDA;
 
   chunk_plan_kernel<false><<<1, kPlanThreads, 0, st>>>(
-      a, FewPlan{}, l.cap, plan, reinterpret_cast<int*>(ws + l.seq), items, pages);
+      a, FewPlan{}, l.cap, plan, reinterpret_cast<int*>(ws + l.seq), items, pages, norm_c,
+      a.B + d->H);
   if (cudaGetLastError() != cudaSuccess) return MLA_ERR_CUDA;
   const int max_items = a.n_tok / ck::kItemTokens + a.B;
   if (launch_dependent(chunk_rotary_kernel<true>,
                        dim3(l.cap + d->H * ck::kDv / 64 + 2 * max_items), dim3(256), 0, st, true, a,
                        l.cap, plan, static_cast<const PageEntry*>(pages),
-                       static_cast<const __nv_bfloat16*>(w_uv), kr, items) != cudaSuccess)
+                       static_cast<const __nv_bfloat16*>(w_uv), kr, items, norm_c,
+                       norm_w) != cudaSuccess)
     return MLA_ERR_CUDA;
 
   ex::Params g;
   g.pages = pages;
   g.plan = plan;
   g.rows_cap = l.rows_cap;
+  g.norm_c = norm_c;
+  g.as_half = ws + l.as_half;
   ck::Params p;
   p.plan = plan;
   p.items = items;
@@ -1132,6 +1166,8 @@ mla_status_t run_expanded(const mla_dims_t* d, const ChunkArgs& a, const Layout&
   p.q_pos = a.q_pos;
   p.H = d->H;
   p.rows_cap = l.rows_cap;
+  p.norm_c = norm_c;
+  p.as_half = ws + l.as_half;
   p.scale = d->scale;
   p.scale_log2 = d->scale * ck::kLog2e;
   p.v = static_cast<__nv_bfloat16*>(v);
@@ -1145,6 +1181,7 @@ mla_status_t run_expanded(const mla_dims_t* d, const ChunkArgs& a, const Layout&
                   ck::kDc, w_rows, ck::kDc, 128))
       return MLA_ERR_CUDA;
     g.n_heads = nh;
+    g.norm_w = p.norm_w = norm_w + h0;
     const long long tiles = (long long)l.cap / 4 * nh;
     const int grid = 2 * (int)std::min<long long>(tiles, sms / 2 > 0 ? sms / 2 : 1);
     if (launch_dependent(ex::expand_kernel, dim3(grid), dim3(ex::kThreads), ex::kSmemBytes, st, true,
@@ -1218,13 +1255,14 @@ mla_status_t run_absorbed(const mla_dims_t* d, const ChunkArgs& a, const Layout&
     const FewPlan few = {t0, n, pairs, plan, streams, tokens};
     if (t0 == 0) {
       if (launch_dependent(chunk_plan_kernel<true>, dim3(1), dim3(kPlanThreads), 0, st, true, a, few,
-                           l.cap, cplan, seq, reinterpret_cast<ck::Item*>(ws + l.items),
-                           pages) != cudaSuccess)
+                           l.cap, cplan, seq, reinterpret_cast<ck::Item*>(ws + l.items), pages,
+                           static_cast<int*>(nullptr), 0) != cudaSuccess)
         return MLA_ERR_CUDA;
       if (p.rotary_moved &&
           launch_dependent(chunk_rotary_kernel<false>, dim3(l.cap), dim3(256), 0, st, true, a, l.cap,
                            cplan, static_cast<const PageEntry*>(pages), wv, kr,
-                           static_cast<ck::Item*>(nullptr)) != cudaSuccess)
+                           static_cast<ck::Item*>(nullptr), static_cast<int*>(nullptr),
+                           static_cast<int*>(nullptr)) != cudaSuccess)
         return MLA_ERR_CUDA;
     } else {
       few_plan_kernel<<<1, kPlanThreads, 0, st>>>(a, few, seq, pages);

@@ -516,14 +516,15 @@ mla_status_t mla_append_tokens(const mla_dims_t* dims, int32_t B, int32_t n_tok,
  *   workspace    ws_bytes >= mla_chunk_workspace_size(...) for the same
  *                arguments, 256-byte aligned, contents need not be initialised
  * A token that sees no row gets v = 0 and lse = -inf.  A row whose position is
- * past a token's does not reach it, whatever it holds.  A sequence with an
+ * past a token's adds nothing to it, whatever it holds (the 16-bit type of the
+ * values of the rows beside it may depend on it, see below).  A sequence with an
  * invalid segment table, page id or too many rows records BAD_INDEX and its
  * tokens get NaN; one whose tok_start is out of order records BAD_INDEX and
  * is left out.  bf16: sums and statistics are fp32, the operands of products
  * have 16 bits: for many tokens expanded keys (bf16), values and softmax weights
- * (fp16 while |c| |W_UV| over all rows of the call bounds the values to its
- * range, else bf16); for few, the absorbed query (bf16), weights and weighted
- * latents in two bf16 parts each.
+ * (fp16 for each 128 rows of a head whose values, times a power of two of its
+ * sequence and head, all lie in fp16's range, else bf16); for few, the absorbed
+ * query (bf16), weights and weighted latents in two bf16 parts each.
  * Errors: INVALID_ARG (scale must be > 0), UNSUPPORTED (page_size != 64,
  * n_ver > 8, H > 65535, row counts beyond 2^31 - 1; outside bf16 rows of 512 + 64, a query
  * of n_ver (d_c + d_r) and a latent of d_c floats that 48 KB do not hold),

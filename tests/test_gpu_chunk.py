@@ -502,3 +502,67 @@ def test_thousands_of_sequences():
     dims = mla.Dims(128, 512, 64, 128, 128, 256, 64, mla.MLA_BF16, 0.07, BASE)
     assert 0 < mla.chunk_workspace_size(dims, 4096, 4096, 1, 64, 1, 4096 * 64) < 2 ** 28
     Case("bf16", 128, [1, 0, 1, 1] * 175, [3, 64, 70, 0] * 175).run().check(heads=[0, 127])
+
+
+def _off(c, v, rows=slice(None), heads=slice(None), channels=slice(None)):
+    """Relative L2 error of a part of the result."""
+    want = v[rows][:, heads][:, :, channels]
+    return float((c.v[rows][:, heads][:, :, channels].double() - want).norm() / want.norm())
+
+
+def test_values_far_below_the_largest_keep_their_precision():
+    """A sequence, a head, a channel and the rows that a token sees, each 2^-20 of the others: every
+    one is held to the bar of roundings to bf16 (4.5e-3, the module's docstring) by its own size."""
+    c = Case("bf16", 4, [300, 280, 300], [100, 300, 256])
+    small = 2.0 ** -20
+    rows = [400, 580, 556]
+    at = lambda b, t: (_i32(c.bt[b].cpu().numpy()).long()[t // 64], t % 64)
+    t = torch.arange(rows[1], device="cuda")
+    c.cache[(*at(1, t), slice(0, 512))] *= small               # a sequence
+    t = torch.arange(128, device="cuda")
+    c.cache[(*at(2, t), slice(0, 512))] *= small               # the first rows of another
+    c.w_uv[1] *= small                                         # a head
+    c.w_uv[2, 77] *= small                                     # a channel
+    c.q_pos[580:600] = 127                                     # tokens that see the small rows alone
+    c.run().check()
+    v, _, _ = c.reference()
+    parts = {"others": dict(rows=slice(0, 300), heads=[0, 3]), "sequence": dict(rows=slice(300, 580), heads=[0, 3]),
+             "rows": dict(rows=slice(580, 600), heads=[0, 3]), "head": dict(rows=slice(0, 300), heads=[1]),
+             "head and sequence": dict(rows=slice(300, 580), heads=[1]),
+             "channel": dict(rows=slice(0, 300), heads=[2], channels=[77])}
+    for name, part in parts.items():
+        assert _off(c, v, **part) <= 4.5e-3, name
+    # what the small ones lose in halves is not lost: the others keep theirs
+    assert _off(c, v, **parts["others"]) <= 2.3e-3
+
+
+@pytest.mark.parametrize("size", [2.0 ** 40, 2.0 ** -40, math.inf])
+def test_neighbours_do_not_change_a_sequence(size):
+    """Latents of another sequence, of any size: the same bits."""
+    c = Case("bf16", 4, [300, 280], [100, 300])
+    c.run()
+    v, lse = c.v.clone(), c.lse.clone()
+    t = torch.arange(580, device="cuda")
+    c.cache[c.bt[1].long()[t // 64], t % 64, :512] *= size
+    c.run()
+    torch.cuda.synchronize()
+    assert mla.get_status() == 0
+    assert torch.equal(c.v[:300], v[:300]) and torch.equal(c.lse[:300], lse[:300])
+
+
+@pytest.mark.parametrize("up,values", [(58, 0), (70, 0), (-70, 0), (58, 118), (70, 118), (58, -60), (70, -50),
+                                       (-70, -110)])
+def test_latents_and_values_near_the_ends_of_their_range(up, values):
+    """Latents 2^up, keys of order one, values 2^values: the result stays finite and as near.  Squared
+    norms of latents of 2^70 are infinite in 32 bits, those of 2^-70 vanish."""
+    c = Case("bf16", 2, [300], [200])
+    c.cache[..., :512] *= 2.0 ** up
+    c.w_uk.mul_(2.0 ** -up)
+    c.w_uv.mul_(2.0 ** (values - up))
+    c.run()
+    torch.cuda.synchronize()
+    assert mla.get_status() == 0
+    v, lse, _ = c.reference()
+    assert torch.isfinite(c.v).all()
+    assert _off(c, v) <= 4.5e-3
+    assert (c.lse.double() - lse).abs().max() <= 1e-2
