@@ -117,6 +117,26 @@ __device__ __forceinline__ void tile_at(const Params& p, int t, int* mt, int* nt
   *nt = in / wide;
 }
 
+// GELU(v) = max(v, 0) - |v| Q(|v|) with the normal distribution's upper tail Q:
+// with 1 + erf nothing is left of the result below v = -5.  Q(a) exp(a^2 / 2) is t
+// times a polynomial of degree 8 in t = 1 / (1 + 0.35 a), fitted here by least
+// squares (reweighted towards equal relative errors, 3.2e-8 up to a = 13.5);
+// with erfcf the kernel spilled and every product took 10 to 35 % longer.
+__device__ __forceinline__ float gelu(float v) {
+  const float a = fabsf(v), t = __fdividef(1.f, fmaf(0.35f, a, 1.f));
+  float q = -0.0291259643f;
+  q = fmaf(q, t, 0.143872693f);
+  q = fmaf(q, t, -0.255505472f);
+  q = fmaf(q, t, 0.158930287f);
+  q = fmaf(q, t, -0.0229377802f);
+  q = fmaf(q, t, 0.105433188f);
+  q = fmaf(q, t, 0.119852379f);
+  q = fmaf(q, t, 0.139859095f);
+  q = fmaf(q, t, 0.139621571f);
+  q *= t * ex2_approx(a * a * -0.72134752f);
+  return v > 14.f ? v : fmaxf(v, 0.f) - a * q;
+}
+
 // v = act(v).  The choice stands outside of the loops: a branch per value keeps
 // one value's divide from overlapping the next one's (64 columns of SiLU took
 // 3.5 us of a 16 us call that way).
@@ -127,7 +147,7 @@ __device__ __forceinline__ void activate_all(float (&v)[n], int act) {
     for (int j = 0; j < n; ++j) v[j] = __fdividef(v[j], 1.f + __expf(-v[j]));
   } else if (act == kGelu) {
 #pragma unroll
-    for (int j = 0; j < n; ++j) v[j] = 0.5f * v[j] * (1.f + erff(v[j] * 0.70710678118654752f));
+    for (int j = 0; j < n; ++j) v[j] = gelu(v[j]);
   }
 }
 

@@ -194,3 +194,33 @@ def test_two_streams_and_a_replayed_graph():
     torch.cuda.synchronize()
     for i in range(2):
         _check(outs[i], xs[i], w, None, "none", None)
+
+
+def _passed_on(dt, M, N, K, values, act):
+    """act of given values, each the whole of a sum: x holds them in its first column, w ones."""
+    v = torch.tensor(values, dtype=torch.float64, device="cuda").to(dt)
+    x = torch.zeros(M, K, device="cuda", dtype=dt)
+    x[:, 0] = v[torch.arange(M, device="cuda") % len(values)]
+    w = torch.zeros(N, K, device="cuda", dtype=dt)
+    w[:, 0] = 1
+    out = torch.full((M, N), float("nan"), device="cuda", dtype=dt)
+    mla.linear(x, w, out, act=act, workspace=_ws(x, w))
+    assert mla.get_status() == 0
+    return x[:, :1].double(), out.double()
+
+
+SHAPES = [(BF, 4, 300, 16384), (BF, 100, 264, 512), (BF, 300, 520, 512), (BF, 5, 9, 7), (torch.float32, 40, 70, 33)]
+
+
+@pytest.mark.parametrize("dt,M,N,K", SHAPES)
+def test_gelu_of_negative_values(dt, M, N, K):
+    """Relative to the result, which is small there: v / sqrt 2 is off by 1.5 * 2^-24, which erfc makes
+    v^2 + 1 times larger, erfc itself by 4 of its last places (2^-21), two products by 2^-24 each.  (The
+    tensor-core kernel's form: half of v^2, twice rounded, enters an exponential that is off by 2^-22; its
+    polynomial by less than 2^-21.  No more than that.)"""
+    values = [-12, -9.5, -8, -7, -6, -5.5, -5, -4, -3, -1, -0.25, 0.0, 0.5, 2, 5, 30]
+    v, got = _passed_on(dt, M, N, K, values, "gelu")
+    want = 0.5 * v * torch.special.erfc(-v / 2 ** 0.5)
+    tol = (HALF[dt] + (1.5 * (v * v + 1) + 10) * 2.0 ** -24) * want.abs()
+    tol = torch.where(v > 0, (HALF[dt] + 2.0 ** -20) * want.abs(), tol)
+    assert (got - want).abs().le(tol * (1 + HALF[dt])).all()
