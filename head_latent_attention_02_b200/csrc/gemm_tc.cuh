@@ -144,7 +144,11 @@ template <int n>
 __device__ __forceinline__ void activate_all(float (&v)[n], int act) {
   if (act == kSilu) {
 #pragma unroll
-    for (int j = 0; j < n; ++j) v[j] = __fdividef(v[j], 1.f + __expf(-v[j]));
+    for (int j = 0; j < n; ++j) {
+      // below zero v e^v / (1 + e^v): e^-v leaves the range (and __fdividef's) near -88
+      const float t = __expf(-fabsf(v[j]));
+      v[j] = __fdividef(v[j] < 0.f ? v[j] * t : v[j], 1.f + t);
+    }
   } else if (act == kGelu) {
 #pragma unroll
     for (int j = 0; j < n; ++j) v[j] = gelu(v[j]);

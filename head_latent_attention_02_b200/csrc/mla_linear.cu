@@ -98,7 +98,10 @@ __global__ void __launch_bounds__(256) linear_simt_kernel(const __grid_constant_
       const int m = m0 + ty * R + u, n = n0 + tx * 4 + v;
       if (m >= a.M || n >= a.N) continue;
       float y = acc[u][v] + (a.bias ? a.bias[n] : 0.f);
-      if (a.act == gm::kSilu) y = y / (1.f + expf(-y));
+      if (a.act == gm::kSilu) {
+        const float t = expf(-fabsf(y));      // see activate_all
+        y = (y < 0.f ? y * t : y) / (1.f + t);
+      }
       if (a.act == gm::kGelu) y = 0.5f * y * erfcf(y * -0.70710678118654752f);
       if (a.residual) y += to_f(static_cast<const T*>(a.residual)[(long long)m * a.res_stride + n]);
       static_cast<T*>(a.out)[(long long)m * a.out_stride + n] = from_f<T>(y);

@@ -224,3 +224,14 @@ def test_gelu_of_negative_values(dt, M, N, K):
     tol = (HALF[dt] + (1.5 * (v * v + 1) + 10) * 2.0 ** -24) * want.abs()
     tol = torch.where(v > 0, (HALF[dt] + 2.0 ** -20) * want.abs(), tol)
     assert (got - want).abs().le(tol * (1 + HALF[dt])).all()
+
+
+@pytest.mark.parametrize("dt,M,N,K", SHAPES)
+def test_silu_of_far_negative_values(dt, M, N, K):
+    """Relative to the result, down to 3e-37: __expf(v) is off by 2 + 1.17 |v| of its last places, what
+    follows by four more; below 2^-126 an exponential has a step of 2^-149."""
+    values = [-89.5, -89, -88.5, -88, -87.5, -80, -20, -3, -0.5, 0.0, 1, 40, 90]
+    v, got = _passed_on(dt, M, N, K, values, "silu")
+    want = v / (1 + torch.exp(-v))
+    tol = (HALF[dt] + (6 + 1.17 * v.abs()) * 2.0 ** -23) * want.abs() + v.abs() * 2.0 ** -149
+    assert (got - want).abs().le(tol * (1 + HALF[dt])).all()
