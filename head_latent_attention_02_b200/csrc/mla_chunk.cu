@@ -92,9 +92,10 @@ __device__ bool page_at(const ChunkArgs& a, int b, int i, PageEntry* e) {
 }
 
 // Exclusive sums of x over the block's threads on top of *carry, which ends as
-// the running total; scratch holds 33 ints.
+// the running total; scratch holds an int a warp.
 __device__ int block_scan(int x, int* scratch, int* carry) {
   const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
+  const int warps = blockDim.x >> 5;
   int y = x;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
@@ -104,17 +105,17 @@ __device__ int block_scan(int x, int* scratch, int* carry) {
   if (lane == 31) scratch[wid] = y;
   __syncthreads();
   if (wid == 0) {
-    int t = scratch[lane];
+    int t = lane < warps ? scratch[lane] : 0;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
       const int z = __shfl_up_sync(0xffffffffu, t, d);
       if (lane >= d) t += z;
     }
-    scratch[lane] = t;
+    if (lane < warps) scratch[lane] = t;
   }
   __syncthreads();
   const int out = *carry + (wid ? scratch[wid - 1] : 0) + y - x;
-  const int total = scratch[31];
+  const int total = scratch[warps - 1];
   __syncthreads();
   if (threadIdx.x == 0) *carry += total;
   __syncthreads();
@@ -125,6 +126,7 @@ __device__ int block_scan(int x, int* scratch, int* carry) {
 // as the largest of all.
 __device__ int block_scan_max(int x, int* scratch, int* carry) {
   const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
+  const int warps = blockDim.x >> 5;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
     const int z = __shfl_up_sync(0xffffffffu, x, d);
@@ -133,17 +135,17 @@ __device__ int block_scan_max(int x, int* scratch, int* carry) {
   if (lane == 31) scratch[wid] = x;
   __syncthreads();
   if (wid == 0) {
-    int t = scratch[lane];
+    int t = lane < warps ? scratch[lane] : INT32_MIN;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
       const int z = __shfl_up_sync(0xffffffffu, t, d);
       if (lane >= d) t = max(t, z);
     }
-    scratch[lane] = t;
+    if (lane < warps) scratch[lane] = t;
   }
   __syncthreads();
   const int out = max(max(*carry, x), wid ? scratch[wid - 1] : INT32_MIN);
-  const int total = scratch[31];
+  const int total = scratch[warps - 1];
   __syncthreads();
   if (threadIdx.x == 0) *carry = max(*carry, total);
   __syncthreads();
@@ -158,6 +160,29 @@ __device__ __forceinline__ int last_at_most(const int* off, int n, int x) {
     if (off[mid] <= x) lo = mid; else hi = mid - 1;
   }
   return lo;
+}
+
+// A sequence's tokens and table.  A token range is only taken if it starts at or
+// behind every start before it: ranges are then disjoint.
+struct SeqRange {
+  bool ranged, wrong;     // its token range holds; the range or the segment table does not
+  int tokens, pages;      // of a range that holds; pages (0 if `wrong`)
+};
+
+// Sequence b by its thread, for all threads of a block at once (b >= B: none);
+// *latest: the last start so far.
+__device__ SeqRange read_sequence(const ChunkArgs& a, int b, int* scratch, int* latest) {
+  SeqRange r = {false, false, 0, 0};
+  const int from = b < a.B ? a.tok_start[b] : INT32_MIN;
+  const bool behind = from == block_scan_max(from, scratch, latest);
+  if (b < a.B) {
+    const int to = a.tok_start[b + 1], k = sequence_pages(a, b);
+    r.wrong = k < 0 || !behind;
+    r.ranged = behind && from >= 0 && to >= from && to <= a.n_tok;
+    if (r.ranged) r.tokens = to - from;
+    if (r.tokens > 0 && !r.wrong) r.pages = k;
+  }
+  return r;
 }
 
 // Flags of a sequence: its tokens get NaN; its token range is invalid (no tokens).
@@ -269,9 +294,8 @@ __global__ void __launch_bounds__(kPlanThreads) few_plan_kernel(
 // that a 128-row tile belongs to one sequence; a multiple of four in all) and
 // their 512-token items.  seq: page offset [B + 1], item offset [B + 1], flag
 // [B].  norms: cleared, for the n_norms that the next launch finds.
-// A sequence that does not fit `cap` pages is invalid.  A token range is
-// only taken if it starts at or behind every start before it: ranges are then
-// disjoint, which the item and stream lists rely on.
+// A sequence that does not fit `cap` pages is invalid.  The item and stream lists
+// rely on disjoint token ranges.
 // kFew: the absorbed route's streams follow, in place of the items.  That kernel
 // is launched as a dependent of the absorption, whose results it does not read:
 // it works beside it and only waits for it before it ends, so that what follows
@@ -293,27 +317,15 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(
   __syncthreads();
   for (int b0 = 0; b0 < a.B; b0 += kPlanThreads) {
     const int b = b0 + threadIdx.x;
-    int np = 0, ni = 0;
-    bool wrong = false, ranged = false;
-    const int from = b < a.B ? a.tok_start[b] : INT32_MIN;
-    const bool behind = from == block_scan_max(from, scratch, &latest);
-    if (b < a.B) {
-      const int t0 = from, t1 = a.tok_start[b + 1];
-      const int k = sequence_pages(a, b);
-      wrong = k < 0 || !behind;
-      ranged = behind && t0 >= 0 && t1 >= t0 && t1 <= a.n_tok;
-      if (ranged && t1 > t0) {
-        ni = (t1 - t0 - 1) / ck::kItemTokens + 1;
-        np = wrong ? 0 : (k + 1) / 2 * 2;
-      }
-    }
+    const SeqRange r = read_sequence(a, b, scratch, &latest);
+    const int np = (r.pages + 1) / 2 * 2;
     const int po = block_scan(np, scratch, &n_pg);
-    const int io = block_scan(ni, scratch, &n_it);
+    const int io = block_scan(r.tokens > 0 ? (r.tokens - 1) / ck::kItemTokens + 1 : 0, scratch, &n_it);
     if (b < a.B) {
-      if ((long long)po + np > cap) wrong = true;
+      const bool wrong = r.wrong || (long long)po + np > cap;
       pg[b] = min(po, cap);
       itm[b] = io;
-      bad[b] = !ranged ? kNoRange : wrong ? kInvalid : 0;
+      bad[b] = !r.ranged ? kNoRange : wrong ? kInvalid : 0;
       if (wrong) set_status(MLA_ERR_BAD_INDEX);
       else atomicMax(&used, po + np);
     }
@@ -851,20 +863,27 @@ __global__ void __launch_bounds__(kGenThreads) chunk_generic_kernel(
   float* score = pw + kGenThreads;           // [128]
   float* red = score + kGenThreads;          // [8]
   int* prow = reinterpret_cast<int*>(red + 8);   // [128] cache rows, -1: none
-  __shared__ int s_b, s_bad;
+  __shared__ int s_b, s_np, s_bad, latest, scratch[kGenThreads / 32];
   __shared__ PageEntry s_page[2][2];         // the pages of this chunk and of the next one
   if (tid == 0) {
     s_b = -1;
     s_bad = 0;
+    latest = INT32_MIN;
   }
   const T* q = static_cast<const T*>(a.q) + ((size_t)t * a.H + h) * (a.d_n + a.d_r);
   for (int k = tid; k < a.d_n + a.d_r; k += kGenThreads) qn[k] = to_f(q[k]);
   for (int k = tid; k < groups * d_c; k += kGenThreads) acc[k] = 0.f;
   __syncthreads();
-  for (int b = tid; b < a.B; b += kGenThreads) {
-    const int lo = a.tok_start[b], hi = a.tok_start[b + 1];
-    if (lo < 0 || hi < lo || hi > a.n_tok) set_status(MLA_ERR_BAD_INDEX);
-    else if (lo <= t && t < hi) atomicMax(&s_b, b);
+  // ranges that hold are disjoint: at most one thread finds the token in its own
+  for (int b0 = 0; b0 < a.B; b0 += kGenThreads) {
+    const int b = b0 + tid;
+    const SeqRange r = read_sequence(a, b, scratch, &latest);
+    if (r.wrong) set_status(MLA_ERR_BAD_INDEX);
+    if (r.tokens > 0 && t >= a.tok_start[b] && t - a.tok_start[b] < r.tokens) {
+      s_b = b;
+      s_np = r.pages;
+      s_bad = r.wrong;
+    }
   }
   for (int c = tid; c < d_c; c += kGenThreads) {
     const T* w = w_uk + (size_t)h * a.d_n * d_c + c;
@@ -884,9 +903,8 @@ __global__ void __launch_bounds__(kGenThreads) chunk_generic_kernel(
   __syncthreads();
   const int b = s_b;
   if (b < 0) return;
-  const int np = sequence_pages(a, b);
+  const int np = s_np;
   PageEntry e;
-  if (np < 0 && tid == 0) s_bad = 1;
   for (int k = tid; k < np; k += kGenThreads)
     if (!page_at(a, b, k, &e)) s_bad = 1;
   __syncthreads();

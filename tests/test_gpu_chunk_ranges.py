@@ -1,0 +1,67 @@
+"""Who owns a token when tok_start is out of order, alike in every route of mla_chunk_attn: a sequence
+whose range is not [lo, hi) with 0 <= lo <= hi <= n_tok, or starts before an earlier start, is left out."""
+import pytest
+import torch
+
+from head_latent_attention_02_b200 import mla
+from tests import chunk_reference as R
+from tests.test_gpu_chunk import Case, _i32, _lib  # noqa: F401  (the fixture)
+
+pytestmark = pytest.mark.gpu
+KINDS = {"generic": ("f32", None), "generic, bf16": ("bf16", dict(d_c=64, d_r=16, d_n=24, d_v=40)),
+         "expanded": ("bf16", None), "absorbed": ("bf16", dict(d_c=512, d_r=64, d_n=64, d_v=96))}
+
+
+def owned(ts, n):
+    """The ranges that hold, by the rule above: {sequence: (first token, last + 1)}."""
+    return {b: (ts[b], ts[b + 1]) for b in range(len(ts) - 1)
+            if 0 <= ts[b] < ts[b + 1] <= n and ts[b] >= max(ts[:b + 1])}
+
+
+STARTS = [
+    ([0, 10, 5, 20], 20, {0: (0, 10)}),                   # the last range begins inside the first one
+    ([0, 50, 10, 30], 60, {0: (0, 50)}),
+    ([30, 10, 20, 40], 40, {}),
+    ([0, 4, 4, 2, 9], 12, {0: (0, 4)}),
+    ([-3, 5, 9], 12, {1: (5, 9)}),
+    ([0, 5, 99], 12, {0: (0, 5)}),
+    ([0, 3, 2, 7, 12], 12, {0: (0, 3), 3: (7, 12)}),      # behind every start again
+]
+
+
+@pytest.mark.parametrize("kind", list(KINDS))
+@pytest.mark.parametrize("ts,n,want", STARTS)
+def test_token_ranges_out_of_order(kind, ts, n, want):
+    assert owned(ts, n) == want
+    k, d = KINDS[kind]
+    B = len(ts) - 1
+    c = Case(k, 3, [n] + [0] * (B - 1), [70 + 30 * b for b in range(B)], d=d)
+    c.q_pos.fill_(1000)                                    # every row is seen
+    c.ts = _i32(ts)
+    c.run()
+    torch.cuda.synchronize()
+    assert mla.get_status() == 6
+    assert mla.get_status() == 0
+    free = torch.ones(n, dtype=torch.bool, device="cuda")
+    for b, (lo, hi) in want.items():
+        v, lse, _ = R.chunk_attn(c.q, [lo, hi], c.q_pos, c.w_uk, c.w_uv, c.cache, c.bt[b:b + 1],
+                                 c.segs[b:b + 1], c.deltas, c.scale, 10000.0)
+        bar = 1e-5 if k == "f32" else 1e-2
+        assert (c.v[lo:hi].double() - v[lo:hi]).norm() <= bar * v[lo:hi].norm()
+        assert (c.lse[lo:hi].double() - lse[lo:hi]).abs().max() <= bar
+        free[lo:hi] = False
+    assert (c.v[free] == 7).all() and (c.lse[free] == 7).all()
+
+
+@pytest.mark.parametrize("kind", list(KINDS))
+def test_an_invalid_table_of_a_sequence_without_tokens(kind):
+    """It records BAD_INDEX, and changes nothing else."""
+    k, d = KINDS[kind]
+    c = Case(k, 3, [9, 0, 5], [70, 200, 64], d=d).run()
+    c.check()
+    v = c.v.clone()
+    c.segs[1, 0, 1] = 1 << 20
+    c.run()
+    torch.cuda.synchronize()
+    assert mla.get_status() == 6
+    assert torch.equal(c.v, v)
