@@ -850,7 +850,7 @@ __device__ __forceinline__ void load_some(const T* src, float (&x)[n]) {
 
 template <typename T, bool kVec>
 __global__ void __launch_bounds__(kGenThreads) chunk_generic_kernel(
-    const __grid_constant__ ChunkArgs a, int d_c, int groups, float scale, const T* w_uk,
+    const __grid_constant__ ChunkArgs a, int cap, int d_c, int groups, float scale, const T* w_uk,
     const T* w_uv, T* v, float* lse) {
   constexpr int V = kVec ? 4 : 1;
   extern __shared__ __align__(16) float sm_gen[];
@@ -863,12 +863,13 @@ __global__ void __launch_bounds__(kGenThreads) chunk_generic_kernel(
   float* score = pw + kGenThreads;           // [128]
   float* red = score + kGenThreads;          // [8]
   int* prow = reinterpret_cast<int*>(red + 8);   // [128] cache rows, -1: none
-  __shared__ int s_b, s_np, s_bad, latest, scratch[kGenThreads / 32];
+  __shared__ int s_b, s_np, s_bad, latest, n_pg, scratch[kGenThreads / 32];
   __shared__ PageEntry s_page[2][2];         // the pages of this chunk and of the next one
   if (tid == 0) {
     s_b = -1;
     s_bad = 0;
     latest = INT32_MIN;
+    n_pg = 0;
   }
   const T* q = static_cast<const T*>(a.q) + ((size_t)t * a.H + h) * (a.d_n + a.d_r);
   for (int k = tid; k < a.d_n + a.d_r; k += kGenThreads) qn[k] = to_f(q[k]);
@@ -877,11 +878,14 @@ __global__ void __launch_bounds__(kGenThreads) chunk_generic_kernel(
   // ranges that hold are disjoint: at most one thread finds the token in its own
   for (int b0 = 0; b0 < a.B; b0 += kGenThreads) {
     const int b = b0 + tid;
-    const SeqRange r = read_sequence(a, b, scratch, &latest);
+    SeqRange r = read_sequence(a, b, scratch, &latest);
+    const int np = (r.pages + 1) / 2 * 2;      // as chunk_plan_kernel counts them
+    const int po = block_scan(np, scratch, &n_pg);
+    if (b < a.B && (long long)po + np > cap) r.wrong = true;
     if (r.wrong) set_status(MLA_ERR_BAD_INDEX);
     if (r.tokens > 0 && t >= a.tok_start[b] && t - a.tok_start[b] < r.tokens) {
       s_b = b;
-      s_np = r.pages;
+      s_np = r.wrong ? 0 : r.pages;
       s_bad = r.wrong;
     }
   }
@@ -1028,8 +1032,9 @@ bool decodable(const mla_dims_t* d) {
 
 struct Layout {
   bool expanded, generic;
+  int cap;                     // page entries
   // expanded
-  int cap, heads, groups;      // page entries; heads per launch; launches
+  int heads, groups;           // heads per launch; launches
   long long rows_cap;
   size_t k, v, norms, as_half;
   // both
@@ -1072,6 +1077,9 @@ bool make_layout(const mla_dims_t* d, int B, int n_tok, int n_ver, int max_pages
     at = up256(at + bytes);
     return here;
   };
+  // page entries, an even number a sequence
+  const long long cap = ((max_rows + kPage - 1) / kPage + B + 3) / 4 * 4;
+  l->cap = (int)std::min<long long>(cap, INT32_MAX);
   l->expanded = chunk_route(d, B, n_tok, max_rows);
   l->generic = !decodable(d);
   if (l->generic) {        // 48 KB of shared memory, a little of it static
@@ -1080,9 +1088,6 @@ bool make_layout(const mla_dims_t* d, int B, int n_tok, int n_ver, int max_pages
     l->total = at;
     return true;
   }
-  // page entries, an even number a sequence
-  const long long cap = ((max_rows + kPage - 1) / kPage + B + 3) / 4 * 4;
-  l->cap = (int)cap;
   l->plan = take(sizeof(ChunkPlan));
   l->seq = take(sizeof(int) * (3 * (size_t)B + 2));
   l->items = take(sizeof(ck::Item) * ((size_t)n_tok / ck::kItemTokens + B));
@@ -1215,12 +1220,12 @@ mla_status_t run_expanded(const mla_dims_t* d, const ChunkArgs& a, const Layout&
 }
 
 template <typename T>
-mla_status_t run_generic(const mla_dims_t* d, const ChunkArgs& a, const void* w_uk, const void* w_uv,
-                         void* v, float* lse, cudaStream_t st) {
+mla_status_t run_generic(const mla_dims_t* d, const ChunkArgs& a, int cap, const void* w_uk,
+                         const void* w_uv, void* v, float* lse, cudaStream_t st) {
   const bool vec = generic_vec(d);
   auto kernel = vec ? chunk_generic_kernel<T, true> : chunk_generic_kernel<T, false>;
   kernel<<<dim3(a.n_tok, d->H), kGenThreads, generic_smem(d, a.n_ver), st>>>(
-      a, d->d_c, generic_groups(d->d_c, vec), d->scale, static_cast<const T*>(w_uk),
+      a, cap, d->d_c, generic_groups(d->d_c, vec), d->scale, static_cast<const T*>(w_uk),
       static_cast<const T*>(w_uv), static_cast<T*>(v), lse);
   return cudaGetLastError() == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
 }
@@ -1370,6 +1375,6 @@ extern "C" mla_status_t mla_chunk_attn(const mla_dims_t* dims, int32_t B, int32_
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   if (l.expanded) return run_expanded(dims, a, l, ws, w_uk, w_uv, v, lse, st);
   if (!l.generic) return run_absorbed(dims, a, l, ws, w_uk, w_uv, v, lse, st);
-  if (dims->dtype == MLA_BF16) return run_generic<__nv_bfloat16>(dims, a, w_uk, w_uv, v, lse, st);
-  return run_generic<float>(dims, a, w_uk, w_uv, v, lse, st);
+  if (dims->dtype == MLA_BF16) return run_generic<__nv_bfloat16>(dims, a, l.cap, w_uk, w_uv, v, lse, st);
+  return run_generic<float>(dims, a, l.cap, w_uk, w_uv, v, lse, st);
 }

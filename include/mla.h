@@ -509,7 +509,7 @@ mla_status_t mla_append_tokens(const mla_dims_t* dims, int32_t B, int32_t n_tok,
  *   delta        [n_ver] HOST relocation offsets of the segments' versions, as
  *                given to mla_absorb_q ([RK]); every axis is shifted by delta
  *   max_rows     bound on the rows of all sequences, each segment rounded up
- *                to whole pages; a sequence that exceeds it is invalid
+ *                to whole pages; in their order, a sequence past it is invalid
  *   v            [n_tok, H, d_v] out (dtype), 16-byte aligned: mla_linear's x
  *   lse          [n_tok, H] out (float) or NULL: natural-log sum of exp of the
  *                scaled visible scores

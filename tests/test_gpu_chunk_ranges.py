@@ -65,3 +65,23 @@ def test_an_invalid_table_of_a_sequence_without_tokens(kind):
     torch.cuda.synchronize()
     assert mla.get_status() == 6
     assert torch.equal(c.v, v)
+
+
+@pytest.mark.parametrize("kind", list(KINDS))
+def test_more_rows_than_announced_in_every_route(kind):
+    """The sequences up to max_rows are attended, those past it get NaN."""
+    k, d = KINDS[kind]
+    c = Case(k, 3, [9, 4, 5, 6], [70, 200, 5000, 40], d=d)
+    full = c.run()
+    torch.cuda.synchronize()
+    assert mla.get_status() == 0
+    v = full.v.clone()
+    c.max_rows = 64 * 6                     # two pages and four; 79 and one more do not fit
+    c.v.fill_(7)
+    c.run()
+    torch.cuda.synchronize()
+    assert mla.get_status() == 6
+    assert mla.get_status() == 0
+    bar = 1e-5 if k == "f32" else 1e-2      # another bound may take another route
+    assert (c.v[:13].double() - v[:13].double()).norm() <= bar * v[:13].double().norm()
+    assert torch.isnan(c.v[13:]).all() and torch.isnan(c.lse[13:]).all()
