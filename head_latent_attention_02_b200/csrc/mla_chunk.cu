@@ -92,30 +92,32 @@ __device__ bool page_at(const ChunkArgs& a, int b, int i, PageEntry* e) {
 }
 
 // Exclusive sums of x over the block's threads on top of *carry, which ends as
-// the running total; scratch holds an int a warp.
-__device__ int block_scan(int x, int* scratch, int* carry) {
+// the running total; scratch holds an element a warp.  Page counts are summed in 64
+// bits: tables may list any number of pages, whatever max_rows allows of them.
+template <typename T>
+__device__ T block_scan(T x, T* scratch, T* carry) {
   const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
   const int warps = blockDim.x >> 5;
-  int y = x;
+  T y = x;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
-    const int z = __shfl_up_sync(0xffffffffu, y, d);
+    const T z = __shfl_up_sync(0xffffffffu, y, d);
     if (lane >= d) y += z;
   }
   if (lane == 31) scratch[wid] = y;
   __syncthreads();
   if (wid == 0) {
-    int t = lane < warps ? scratch[lane] : 0;
+    T t = lane < warps ? scratch[lane] : 0;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
-      const int z = __shfl_up_sync(0xffffffffu, t, d);
+      const T z = __shfl_up_sync(0xffffffffu, t, d);
       if (lane >= d) t += z;
     }
     if (lane < warps) scratch[lane] = t;
   }
   __syncthreads();
-  const int out = *carry + (wid ? scratch[wid - 1] : 0) + y - x;
-  const int total = scratch[warps - 1];
+  const T out = *carry + (wid ? scratch[wid - 1] : 0) + y - x;
+  const T total = scratch[warps - 1];
   __syncthreads();
   if (threadIdx.x == 0) *carry += total;
   __syncthreads();
@@ -305,7 +307,8 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(
     const __grid_constant__ ChunkArgs a, const __grid_constant__ FewPlan f, int cap, ChunkPlan* plan,
     int* seq, ck::Item* items, PageEntry* pages, int* norms, int n_norms) {
   asm volatile("griddepcontrol.launch_dependents;");
-  __shared__ int scratch[33], n_pg, n_it, used, latest;
+  __shared__ int scratch[33], n_it, used, latest;
+  __shared__ long long page_scratch[33], n_pg;
   for (int i = threadIdx.x; i < n_norms; i += kPlanThreads) norms[i] = kNoNorm;
   int* pg = seq;
   int* itm = seq + a.B + 1;
@@ -318,22 +321,21 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(
   for (int b0 = 0; b0 < a.B; b0 += kPlanThreads) {
     const int b = b0 + threadIdx.x;
     const SeqRange r = read_sequence(a, b, scratch, &latest);
-    const int np = (r.pages + 1) / 2 * 2;
-    const int po = block_scan(np, scratch, &n_pg);
+    const long long np = (r.pages + 1) / 2 * 2, po = block_scan(np, page_scratch, &n_pg);
     const int io = block_scan(r.tokens > 0 ? (r.tokens - 1) / ck::kItemTokens + 1 : 0, scratch, &n_it);
     if (b < a.B) {
-      const bool wrong = r.wrong || (long long)po + np > cap;
-      pg[b] = min(po, cap);
+      const bool wrong = r.wrong || po + np > cap;
+      pg[b] = (int)min(po, (long long)cap);
       itm[b] = io;
       bad[b] = !r.ranged ? kNoRange : wrong ? kInvalid : 0;
       if (wrong) set_status(MLA_ERR_BAD_INDEX);
-      else atomicMax(&used, po + np);
+      else atomicMax(&used, (int)(po + np));
     }
   }
   __syncthreads();
   const int in_use = used, whole = (in_use + 3) / 4 * 4;      // cap is a multiple of four
   if (threadIdx.x == 0) {
-    pg[a.B] = min(n_pg, cap);
+    pg[a.B] = (int)min(n_pg, (long long)cap);
     itm[a.B] = n_it;
     plan->n_items = n_it;
     plan->n_row_tiles = whole / 4;
@@ -863,7 +865,8 @@ __global__ void __launch_bounds__(kGenThreads) chunk_generic_kernel(
   float* score = pw + kGenThreads;           // [128]
   float* red = score + kGenThreads;          // [8]
   int* prow = reinterpret_cast<int*>(red + 8);   // [128] cache rows, -1: none
-  __shared__ int s_b, s_np, s_bad, latest, n_pg, scratch[kGenThreads / 32];
+  __shared__ long long page_scratch[kGenThreads / 32], n_pg;
+  __shared__ int s_b, s_np, s_bad, latest, scratch[kGenThreads / 32];
   __shared__ PageEntry s_page[2][2];         // the pages of this chunk and of the next one
   if (tid == 0) {
     s_b = -1;
@@ -879,9 +882,9 @@ __global__ void __launch_bounds__(kGenThreads) chunk_generic_kernel(
   for (int b0 = 0; b0 < a.B; b0 += kGenThreads) {
     const int b = b0 + tid;
     SeqRange r = read_sequence(a, b, scratch, &latest);
-    const int np = (r.pages + 1) / 2 * 2;      // as chunk_plan_kernel counts them
-    const int po = block_scan(np, scratch, &n_pg);
-    if (b < a.B && (long long)po + np > cap) r.wrong = true;
+    const long long np = (r.pages + 1) / 2 * 2;      // as chunk_plan_kernel counts them
+    const long long po = block_scan(np, page_scratch, &n_pg);
+    if (b < a.B && po + np > cap) r.wrong = true;
     if (r.wrong) set_status(MLA_ERR_BAD_INDEX);
     if (r.tokens > 0 && t >= a.tok_start[b] && t - a.tok_start[b] < r.tokens) {
       s_b = b;
@@ -1111,6 +1114,10 @@ bool make_layout(const mla_dims_t* d, int B, int n_tok, int n_ver, int max_pages
     const int pairs = current_sms() / 2;
     if (pairs == 0) return false;
     l->max_streams = (int)(rows / fw::kRows) + std::min(B, l->slab);   // with a token in it
+    // (stream, page) units and rows of the page list are counted in 32 bits
+    if (cap * kPage > INT32_MAX ||
+        (long long)(rows / fw::kRows) * std::min<long long>(cap, max_pages) + cap > INT32_MAX)
+      return false;
     l->few_plan = take(sizeof(fw::Plan));
     l->streams = take(sizeof(fw::Stream) * (size_t)l->max_streams);
     l->tokens = take(n * sizeof(FewToken));

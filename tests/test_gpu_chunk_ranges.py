@@ -85,3 +85,25 @@ def test_more_rows_than_announced_in_every_route(kind):
     bar = 1e-5 if k == "f32" else 1e-2      # another bound may take another route
     assert (c.v[:13].double() - v[:13].double()).norm() <= bar * v[:13].double().norm()
     assert torch.isnan(c.v[13:]).all() and torch.isnan(c.lse[13:]).all()
+
+
+@pytest.mark.parametrize("kind", list(KINDS))
+def test_tables_of_more_pages_than_32_bits_count(kind):
+    """70 sequences, all but the first of 2^25 - 1 pages each, a table of 2^31 entries: past max_rows."""
+    k, d = KINDS[kind]
+    B, wide = 70, 2 ** 25 - 1
+    c = Case(k, 2, [2] * B, [100] + [3] * (B - 1), d=d).run()
+    c.check()
+    v = c.v.clone()
+    bt = torch.zeros(B, wide, dtype=torch.int32, device="cuda")
+    bt[:, :c.bt.shape[1]] = c.bt
+    c.bt = bt
+    c.segs[1:, 0, 1] = wide * 64
+    c.run()
+    torch.cuda.synchronize()
+    assert mla.get_status() == 6
+    bar = 1e-5 if k == "f32" else 1e-2
+    assert (c.v[:2].double() - v[:2].double()).norm() <= bar * v[:2].double().norm()
+    assert torch.isnan(c.v[2:]).all() and torch.isnan(c.lse[2:]).all()
+    c.bt = bt = None
+    torch.cuda.empty_cache()
