@@ -242,14 +242,43 @@ struct AppendTokArgs {
 // The sequence that token t belongs to, by the whole warp: the number of
 // starts at or before t, less one (the loads of a batch of 32 sequences are
 // independent of one another, where a binary search chains them).  -1: the
-// token lies behind the last sequence; -2: the starts are not in order.
-__device__ __forceinline__ int owner_of(const int32_t* tok_start, int B, int t, int lane) {
-  int n = 0;
-  for (int j = 0; j <= B; j += 32)
-    n += __popc(__ballot_sync(0xffffffffu, j + lane <= B && tok_start[min(j + lane, B)] <= t));
-  if (n == B + 1) return -1;
-  if (n == 0 || tok_start[n - 1] > t || tok_start[n] <= t) return -2;
-  return n - 1;
+// token lies behind the last sequence; -2: it is left out because starts are not in
+// order.  A range that does not hold (0 <= start <= end <= n_tok) or starts before an
+// earlier start owns nothing, as in mla_chunk_attn.
+__device__ __noinline__ int owner_out_of_order(const int32_t* tok_start, int B, int n_tok, int t,
+                                               int lane) {
+  int latest = INT32_MIN;
+  bool behind = true;
+  for (int j = 0; j < B; j += 32) {
+    const int b = min(j + lane, B - 1), from = tok_start[b], to = tok_start[b + 1];
+    const unsigned in = __ballot_sync(0xffffffffu, j + lane < B && from >= 0 && from <= t && t < to &&
+                                                       to <= n_tok);
+    behind = behind && from <= t;
+    // the first range with t in it: a later one would start inside of it
+    const int k = in ? __ffs(in) - 1 : 32;
+    latest = max(latest, __reduce_max_sync(0xffffffffu, lane < k ? from : INT32_MIN));
+    if (in) return __shfl_sync(0xffffffffu, from, k) >= latest ? j + k : -2;
+  }
+  return __all_sync(0xffffffffu, behind && tok_start[B] <= t) ? -1 : -2;
+}
+
+__device__ __forceinline__ int owner_of(const int32_t* tok_start, int B, int n_tok, int t, int lane) {
+  int n = 0, last = INT32_MIN;
+  bool ordered = true;
+  for (int j = 0; j <= B; j += 32) {
+    const int from = tok_start[min(j + lane, B)];
+    const unsigned in = __ballot_sync(0xffffffffu, j + lane <= B && from <= t);
+    // the starts at or before t come first
+    ordered = ordered && (in & (in + 1u)) == 0u && (in == 0u || n == j);
+    n += __popc(in);
+    if (from <= t) last = max(last, from);
+  }
+  if (n == 0 && ordered) return -2;
+  if (ordered && __reduce_max_sync(0xffffffffu, last) == tok_start[n - 1]) {
+    if (n == B + 1) return -1;
+    if (tok_start[n - 1] >= 0 && tok_start[n] <= n_tok) return n - 1;
+  }
+  return owner_out_of_order(tok_start, B, n_tok, t, lane);
 }
 
 template <typename T>
@@ -305,7 +334,12 @@ __global__ void __launch_bounds__(kTokThreads) append_tokens_kernel(
   if (has_pair)
     trig<kExact>((double)a.pos[(size_t)ax.axis_of(lane) * a.n_tok + t] * ax.theta[lane], cs.x, cs.y);
 
-  const int b = owner_of(a.tok_start, a.B, t, lane);
+  const int b = owner_of(a.tok_start, a.B, a.n_tok, t, lane);
+  if (t == 0)        // for all tokens: a range that does not hold
+    for (int j = lane; j < a.B; j += 32) {
+      const int from = a.tok_start[j], to = a.tok_start[j + 1];
+      if (from < 0 || to < from || to > a.n_tok) set_status(MLA_ERR_BAD_INDEX);
+    }
   if (b == -1) return;
   int page = -1, slot = 0;
   if (b >= 0) {

@@ -442,7 +442,8 @@ mla_status_t mla_decode_qknorm(const mla_dims_t* dims, int32_t B, int32_t s_q,
  * [tok_start[b], tok_start[b + 1]) (tok_start [B + 1], int32, device,
  * ascending from >= 0 to <= n_tok; equal neighbours: no new token).  Tokens
  * outside every range (a padded batch) are left out and their output rows keep
- * what they held.
+ * what they held.  A range that is not within [0, n_tok] and ascending, or that
+ * starts before an earlier start, owns no token, and records BAD_INDEX.
  *
  * mla_rope_axes -- rotary positions with several axes (time, height, width of
  * images and video; one axis for text).  [T27] "Position Rotations Complicate
@@ -483,8 +484,8 @@ mla_status_t mla_rope_axes(const mla_dims_t* dims, int32_t n_tok, int32_t n_head
  *                [d_c] and scale_r [d_r] (float; NULL exactly for plain rows).
  *                What decides a code is computed in double.
  * Only the addressed rows change.  Two tokens naming one row race.
- * A token whose row or page id is out of range, or whose tok_start
- * is out of order, is skipped and records BAD_INDEX.  Errors: INVALID_ARG;
+ * A token whose row or page id is out of range is skipped and records BAD_INDEX,
+ * and so is one before the first start (padding stands at the end).  Errors: INVALID_ARG;
  * UNSUPPORTED (page_size != 64, other bit pairs or widths, n_axes > 4,
  * d_r > 128). */
 mla_status_t mla_append_tokens(const mla_dims_t* dims, int32_t B, int32_t n_tok, const void* kv,
@@ -519,8 +520,7 @@ mla_status_t mla_append_tokens(const mla_dims_t* dims, int32_t B, int32_t n_tok,
  * past a token's adds nothing to it, whatever it holds (the 16-bit type of the
  * values of the rows beside it may depend on it, see below).  A sequence with an
  * invalid segment table, page id or too many rows records BAD_INDEX and its
- * tokens get NaN; one whose tok_start is out of order records BAD_INDEX and
- * is left out.  bf16: sums and statistics are fp32, the operands of products
+ * tokens get NaN.  bf16: sums and statistics are fp32, the operands of products
  * have 16 bits: for many tokens expanded keys (bf16), values and softmax weights
  * (fp16 for each 128 rows of a head whose values, times a power of two of its
  * sequence and head, all lie in fp16's range, else bf16); for few, the absorbed
