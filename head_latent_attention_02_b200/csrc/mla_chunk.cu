@@ -1352,7 +1352,9 @@ extern "C" mla_status_t mla_chunk_attn(const mla_dims_t* dims, int32_t B, int32_
   if (B == 0 || n_tok == 0) return MLA_OK;
   if (!q || !tok_start || !q_pos || !w_uk || !w_uv || !cache || !block_table || !segs || !v ||
       !ptr_aligned(cache, 256) || !ptr_aligned(q, 16) || !ptr_aligned(w_uk, 16) ||
-      !ptr_aligned(w_uv, 16) || !ptr_aligned(v, 16) || !ptr_aligned(lse, 4))
+      !ptr_aligned(w_uv, 16) || !ptr_aligned(v, 16) || !ptr_aligned(lse, 4) ||
+      !ptr_aligned(tok_start, 4) || !ptr_aligned(q_pos, 4) || !ptr_aligned(block_table, 4) ||
+      !ptr_aligned(segs, 4))
     return MLA_ERR_INVALID_ARG;
   Layout l;
   if (!make_layout(dims, B, n_tok, n_ver, max_pages, max_segs, max_rows, &l))

@@ -536,7 +536,9 @@ extern "C" mla_status_t mla_append_tokens(const mla_dims_t* dims, int32_t B, int
   if (n_tok == 0 || B == 0) return MLA_OK;
   const size_t es = dims->dtype == MLA_BF16 ? 2 : 4;
   if (!kv || !tok_start || !row0 || !pos || !cache || !block_table || !aligned_to(kv, es) ||
-      !aligned_to(cache, low ? 4 : es))
+      !aligned_to(cache, low ? 4 : es) || !aligned_to(tok_start, 4) || !aligned_to(row0, 4) ||
+      !aligned_to(pos, 4) || !aligned_to(block_table, 4) || !aligned_to(norm_weight, 4) ||
+      !aligned_to(scale_c, 4) || !aligned_to(scale_r, 4))
     return MLA_ERR_INVALID_ARG;
   AppendTokArgs a;
   a.B = B;
