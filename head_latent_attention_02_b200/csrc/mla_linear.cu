@@ -264,6 +264,8 @@ extern "C" mla_status_t mla_linear(int32_t dtype, int32_t M, int32_t N, int32_t 
   if (!x || !w || !out || !ptr_aligned(x, es) || !ptr_aligned(w, es) || !ptr_aligned(out, es) ||
       !ptr_aligned(residual, es) || !ptr_aligned(bias, 4))
     return MLA_ERR_INVALID_ARG;
+  // in place: the same rows, or one thread's results are another one's residual
+  if (residual == out && M > 1 && res_stride != out_stride) return MLA_ERR_INVALID_ARG;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const bool tma = dtype == MLA_BF16 && ptr_aligned(x, 16) && ptr_aligned(w, 16) &&
                    x_stride % 8 == 0 && w_stride % 8 == 0 && x_stride < (1ll << 38) &&

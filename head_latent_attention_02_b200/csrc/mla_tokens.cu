@@ -470,6 +470,10 @@ extern "C" mla_status_t mla_rope_axes(const mla_dims_t* dims, int32_t n_tok, int
   if (x_tok_stride < 0 || x_head_stride < 0 ||
       (!apart(out_tok_stride, out_head_stride) && (n_tok > 1 || n_heads > 1)))
     return MLA_ERR_INVALID_ARG;
+  // in place: the same vectors, or one thread's results are another one's input
+  if (x == out && ((n_tok > 1 && x_tok_stride != out_tok_stride) ||
+                   (n_heads > 1 && x_head_stride != out_head_stride)))
+    return MLA_ERR_INVALID_ARG;
   RopeArgs a;
   a.n_tok = n_tok;
   a.n_heads = n_heads;

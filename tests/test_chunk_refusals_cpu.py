@@ -1,7 +1,7 @@
 """More refusals of the prompt-chunk entry points, on the CPU: none of the fake pointers is ever used."""
 import pytest
 
-from tests.test_chunk_abi_cpu import FAKE, INVALID, L, _append, _chunk  # noqa: F401  (L: the fixture)
+from tests.test_chunk_abi_cpu import FAKE, INVALID, L, _append, _chunk, _linear, _rope  # noqa: F401  (L: the fixture)
 
 
 @pytest.mark.parametrize("name", ["ts", "row0", "pos", "bt", "norm"])
@@ -18,3 +18,12 @@ def test_append_refuses_misaligned_scales(L, name):
 @pytest.mark.parametrize("off", [1, 2])
 def test_chunk_refuses_misaligned_arrays(L, name, off):
     assert _chunk(L, **{name: FAKE + off}) == INVALID
+
+
+def test_in_place_with_other_strides_is_refused(L):
+    assert _rope(L, xt=0) == INVALID                    # x and out are the same pointer
+    assert _rope(L, xh=0) == INVALID
+    assert _rope(L, xt=8 * 64 + 64) == INVALID
+    assert _rope(L, ot=16 * 64, oh=128) == INVALID
+    assert _linear(L, res=FAKE, rs=16) == INVALID
+    assert _linear(L, res=FAKE, rs=8, os=9) == INVALID
