@@ -285,6 +285,8 @@ def _ints(values: Sequence[int]):
     key = tuple(values)
     arr = _arrays.get(key)
     if arr is None:
+        if any(int(v) != v or not -2 ** 31 <= int(v) < 2 ** 31 for v in key):
+            raise ValueError(f"32-bit integers expected, got {list(key)}")     # ctypes would wrap them
         if len(_arrays) > 256:
             _arrays.clear()
         arr = _arrays[key] = (_i32 * len(key))(*[int(v) for v in key])

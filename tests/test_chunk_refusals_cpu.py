@@ -1,6 +1,8 @@
 """More refusals of the prompt-chunk entry points, on the CPU: none of the fake pointers is ever used."""
+import numpy as np
 import pytest
 
+from head_latent_attention_02_b200 import mla
 from tests.test_chunk_abi_cpu import FAKE, INVALID, L, _append, _chunk, _linear, _rope  # noqa: F401  (L: the fixture)
 
 
@@ -27,3 +29,14 @@ def test_in_place_with_other_strides_is_refused(L):
     assert _rope(L, ot=16 * 64, oh=128) == INVALID
     assert _linear(L, res=FAKE, rs=16) == INVALID
     assert _linear(L, res=FAKE, rs=8, os=9) == INVALID
+
+
+@pytest.mark.parametrize("values", [[0, 2 ** 31], [-2 ** 31 - 1], [2 ** 32 + 5], [0.5], [8, 2 ** 40, 8]])
+def test_binding_refuses_integers_that_32_bits_do_not_hold(values):
+    """Relocation offsets and sections: wrapped, they would be other ones."""
+    with pytest.raises(ValueError, match="32-bit"):
+        mla._ints(values)
+
+
+def test_binding_takes_integers_of_any_kind():
+    assert list(mla._ints([2 ** 31 - 1, -2 ** 31, np.int64(7), 8.0])) == [2 ** 31 - 1, -2 ** 31, 7, 8]
