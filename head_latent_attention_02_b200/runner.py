@@ -233,12 +233,12 @@ def chunk_problem(dims: mla.Dims, w_uk, w_uv, w_o, cache, block_table, segs, del
     out = torch.empty((n_tok, w_o.shape[0]), dtype=dt, device=dev)
     size = mla.chunk_workspace_size(dims, B, n_tok, len(deltas), block_table.shape[1], segs.shape[1],
                                     max_rows)
-    if size == 0:
+    if size == 0 and n_tok and B:        # without tokens or sequences it needs none
         raise ValueError("sizes that mla_chunk_attn does not take")
-    linear = mla.linear_workspace_size(v.view(n_tok, -1), w_o)
+    linear = mla.linear_workspace_size(v.flatten(1), w_o)
     return ChunkProblem(dims, w_uk, w_uv, w_o, norm_weight, norm_eps, cache, block_table, segs,
                         list(deltas), max_rows, tok_start, row0, q_pos, pos, list(sections), v, out,
-                        torch.empty(size, dtype=torch.uint8, device=dev),
+                        torch.empty(max(size, 256), dtype=torch.uint8, device=dev),
                         torch.empty(max(linear, 256), dtype=torch.uint8, device=dev))
 
 
@@ -267,6 +267,6 @@ def run_chunk(p: ChunkProblem, q: torch.Tensor, kv: torch.Tensor, residual=None,
         mla.chunk_attn(p.dims, q, p.tok_start, p.q_pos, p.w_uk, p.w_uv, p.cache, p.block_table, p.segs,
                        p.deltas, p.max_rows, p.v, p.workspace, stream=stream)
     with _nvtx("mla_linear"):
-        mla.linear(p.v.view(p.v.shape[0], -1), p.w_o, p.out, residual=residual,
+        mla.linear(p.v.flatten(1), p.w_o, p.out, residual=residual,
                    workspace=p.linear_workspace, stream=stream)
     return p.out

@@ -3,7 +3,7 @@ whose range is not [lo, hi) with 0 <= lo <= hi <= n_tok, or starts before an ear
 import pytest
 import torch
 
-from head_latent_attention_02_b200 import mla
+from head_latent_attention_02_b200 import mla, runner
 from tests import chunk_reference as R
 from tests.test_gpu_chunk import Case, _i32, _lib  # noqa: F401  (the fixture)
 
@@ -107,3 +107,23 @@ def test_tables_of_more_pages_than_32_bits_count(kind):
     assert torch.isnan(c.v[2:]).all() and torch.isnan(c.lse[2:]).all()
     c.bt = bt = None
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+@pytest.mark.parametrize("B,n", [(2, 0), (0, 0), (0, 3)])
+def test_a_layer_without_tokens_or_sequences(kind, B, n):
+    """run_chunk on an empty step: nothing appended, every row (padding) keeps the residual."""
+    c = Case(kind, 2, [1, 1], [70, 3])
+    dt, d = c.q.dtype, c.d
+    new = lambda *s: torch.randn(*s, device="cuda").to(dt)
+    empty = torch.zeros(n, dtype=torch.int32, device="cuda")
+    p = runner.chunk_problem(c.dims, c.w_uk, c.w_uv, new(48, 2 * d["d_v"]), c.cache, c.bt[:B], c.segs[:B],
+                             c.deltas, c.max_rows, torch.zeros(B + 1, dtype=torch.int32, device="cuda"),
+                             _i32([70, 3])[:B], empty, empty[None].clone(), [d["d_r"] // 2])
+    before = c.cache.clone()
+    q, kv, res = new(n, 2, d["d_n"] + d["d_r"]), new(n, d["d_c"] + d["d_r"]), new(n, 48)
+    out = runner.run_chunk(p, q, kv, residual=res)
+    torch.cuda.synchronize()
+    assert mla.get_status() == 0
+    assert out.shape == (n, 48) and torch.equal(out, res)
+    assert torch.equal(c.cache.view(torch.uint8), before.view(torch.uint8))
