@@ -253,7 +253,14 @@ def run_chunk(p: ChunkProblem, q: torch.Tensor, kv: torch.Tensor, residual=None,
     part is rotated in place), kv [n_tok, d_c + d_r] raw rows of the
     down-projection, residual [n_tok, d_model] or None.  Appends the tokens to the
     cache, attends and projects; returns p.out.  Rows of tokens outside every
-    sequence project zeros: they keep the residual."""
+    sequence project zeros: they keep the residual.  Tensors that do not fit the
+    problem are refused before q or the cache is touched."""
+    n_tok, dt, dev = p.q_pos.shape[0], p.cache.dtype, torch.cuda.current_device()
+    d = p.dims
+    mla._at(q, "q", dt, (n_tok, d.H, d.d_n + d.d_r), dev)
+    for name, t, shape in (("kv", kv, (n_tok, d.d_c + d.d_r)), ("residual", residual, tuple(p.out.shape))):
+        if t is not None and mla._pitch(t, name, dt, shape, dev) < shape[1]:
+            raise ValueError(f"{name}: rows must not overlap")
     with _nvtx("mla_rope_axes"):
         rot = q[..., p.dims.d_n:]
         mla.rope_axes(p.dims, rot, p.pos, p.sections, rot, stream=stream)

@@ -127,3 +127,26 @@ def test_a_layer_without_tokens_or_sequences(kind, B, n):
     assert mla.get_status() == 0
     assert out.shape == (n, 48) and torch.equal(out, res)
     assert torch.equal(c.cache.view(torch.uint8), before.view(torch.uint8))
+
+
+def test_a_refused_layer_call_changes_nothing():
+    """A query, latent rows or residual that a later step would refuse: q is not rotated, nothing appended."""
+    c = Case("f32", 2, [5, 4], [70, 3])
+    p = runner.chunk_problem(c.dims, c.w_uk, c.w_uv, torch.randn(48, 32, device="cuda"), c.cache, c.bt, c.segs,
+                             c.deltas, c.max_rows, c.ts, _i32([70, 3]), c.q_pos, c.q_pos[None].clone(), [8])
+    new = lambda *s: torch.randn(*s, device="cuda")
+    wide = new(9, 2, 40)
+    good = (new(9, 2, 32), new(9, 48), new(9, 48))
+    cache = c.cache.clone()
+    for bad in ((wide[..., :32], good[1], good[2]), (good[0], new(8, 48), good[2]), (good[0], good[1], new(9, 47)),
+                (good[0], good[1].double(), good[2]), (good[0], good[1], good[2].bfloat16()),
+                (good[0], good[1], torch.randn(9, 48)), (good[0], good[1], new(1, 48).expand(9, 48)),
+                (good[0], new(1, 48).expand(9, 48), good[2])):
+        q = bad[0].clone()
+        with pytest.raises(ValueError):
+            runner.run_chunk(p, bad[0], bad[1], residual=bad[2])
+        torch.cuda.synchronize()
+        assert torch.equal(bad[0], q)
+        assert torch.equal(c.cache.view(torch.uint8), cache.view(torch.uint8))
+    runner.run_chunk(p, *good[:2], residual=good[2])
+    assert mla.get_status() == 0
