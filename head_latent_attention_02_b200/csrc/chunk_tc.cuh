@@ -24,7 +24,7 @@
 // At 192 + 128 columns a tile costs the tensor core 1280 clocks and its
 // exponentials the special-function units 1024.  What bounds it is the way from
 // scores to weights, about 1500 clocks, against 1280 of the other query tile's
-// products: 2048 tokens over 10 240 rows, 128 heads take 1202 us (1.29 PFLOP/s).
+// products: 2048 tokens over 10 240 rows, 128 heads take 1175 us (1.32 PFLOP/s).
 //
 // Roles (384 threads a CTA): warp 0 loads by TMA, warp 1 of the first CTA
 // issues the MMAs, warps 4-7 and 8-11 run the softmax of query tiles 0 and 1 (a

@@ -11,7 +11,7 @@
 // a CTA where the general tile of gemm_tc.cuh, which streams both operands,
 // loads 256 KB; at 512 channels a tile lasts 4096 clocks, and 64 bytes a clock
 // and SM is more than L2 delivers (8192 + 2048 rows, 128 heads: 400 us streaming
-// both, 257 us this way, 1.34 PFLOP/s).  Two accumulators let the epilogue
+// both, 260 us this way, 1.32 PFLOP/s).  Two accumulators let the epilogue
 // overlap the next tile.
 //
 // Roles per CTA (192 threads): warp 0 loads, warp 1 of the first CTA issues,

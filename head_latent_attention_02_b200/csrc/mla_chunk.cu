@@ -1048,7 +1048,11 @@ struct Layout {
   size_t total;
 };
 
-// Expanded when its estimated time (microseconds) is the lower one.
+// Expanded when its estimated time (microseconds) is the lower one.  The host knows
+// the tokens and the rows of all sequences only, and one route serves the whole
+// call: the estimates take every sequence to be of the average size, and both
+// sides were measured on equal ones.  A chunk beside many single tokens counts as
+// rows x average tokens, below what the absorbed route then computes.
 //   Expanded: a row's expansion costs 2 * 512 * 256 flops a head at 1.15 PFLOP/s;
 //   a query, row and head 2 * 320 at 0.7, in query tiles of 256, but no less than
 //   one item's way through a sequence, 1.9 us per 128 rows.

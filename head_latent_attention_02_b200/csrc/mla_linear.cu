@@ -111,7 +111,11 @@ __global__ void __launch_bounds__(256) linear_simt_kernel(const __grid_constant_
 template <typename T>
 void launch_simt(const SimtArgs& a, cudaStream_t st) {
   const unsigned nb = (unsigned)((a.N + kTN - 1) / kTN);
-  // few rows: tiles of 16 rows, so that a short product has blocks for more SMs
+  // few rows: tiles of 16 rows, so that a short product has blocks for more SMs.
+  // Tiles of 16 and of 64 rows, fp32 (us): 16 x 1024 x 1001 45, 68; 256 x 1024 x 1001 68, 69;
+  // 512 x 256 x 1001 46, 69; 512 x 1024 x 1001 111, 70; 1024 x 256 x 1001 68, 69;
+  // 1024 x 1024 x 1001 200, 97.  They cross near 256 tiles of 16 rows; 512 rows is late
+  // for wide results and early for narrow ones.
   if (a.M <= 512)
     linear_simt_kernel<T, 16><<<dim3(nb, (unsigned)((a.M + 15) / 16)), 256, 0, st>>>(a);
   else
@@ -188,7 +192,10 @@ TilePlan plan_tiles(int M, int N, int K, int sms) {
   TilePlan t = {};
   const int pairs = sms / 2 > 0 ? sms / 2 : 1;
   t.swapped = M <= 128;
-  // panels of a stage: long box rows where W is streamed once
+  // panels of a stage: long box rows where W is streamed once.  Four, two and one
+  // panel (us): 16 x 7168 x 16384 45.5, 47.2, 48.2; 32 rows 45.6, 47.1, 48.4; 48 rows
+  // 48.1, 47.1, 48.8; 128 rows 51.3, 49.9, 50.8; 16 x 7168 x 2048 10.5, 12.2, 14.0; 64 rows
+  // 13.7, 14.8, 14.7 (four would be the better choice there: a short K).
   t.P = K % 64 == 0 && t.swapped ? (M <= 32 ? 4 : 2) : 1;
   const int step_k = gm::kKStep * t.P;
   t.k_steps = (K + step_k - 1) / step_k;

@@ -491,7 +491,11 @@ extern "C" mla_status_t mla_rope_axes(const mla_dims_t* dims, int32_t n_tok, int
   const int per = vec ? ax.half / 4 : ax.half;
   // One batch of loads a thread: as many tokens as fill it, heads split when
   // one token holds more.  Few tokens: one load a thread, so that the heads
-  // of a token spread over several SMs.
+  // of a token spread over several SMs.  Slices of 192-wide queries, few and many
+  // loads a thread (us): 8 heads 64 tokens 2.6, 3.0; 256 3.1, 3.1; 512 5.0, 3.1;
+  // 64 heads 64 2.9, 3.6; 128 3.4, 3.6; 256 5.3, 3.7; 512 8.9, 3.7; 128 heads 64 3.3, 3.7;
+  // 128 5.3, 3.7; 512 14.9, 4.8.  So the sides cross at about 8192 (token, head) pairs,
+  // and 512 tokens is late for many heads.
   const int items = kRopeThreads * (n_tok >= 512 ? kRopeUnroll : 1);
   int hpb = items / per > 0 ? items / per : 1, tpb = 1;
   if (hpb > n_heads) hpb = n_heads;
