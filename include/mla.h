@@ -518,7 +518,9 @@ mla_status_t mla_append_tokens(const mla_dims_t* dims, int32_t B, int32_t n_tok,
  *                arguments, 256-byte aligned, contents need not be initialised
  * One of three forms is taken for the whole call, by dims, B, n_tok and max_rows:
  * the same sequence has other roundings (within the precision below) in a call of
- * other sizes.  For the same sizes, other sequences' contents do not change its bits.
+ * other sizes, or beside sequences of other lengths or positions, which move the
+ * places where sums are split.  Other sequences' queries and cached values do not
+ * change its bits.
  * A token that sees no row gets v = 0 and lse = -inf.  A row whose position is
  * past a token's adds nothing to it, whatever it holds (the 16-bit type of the
  * values of the rows beside it may depend on it, see below).  A sequence with an
